@@ -17,6 +17,10 @@
  *   moe_router          top-k softmax router over a bf16 gate (upstream of
  *                       the layer: produces the ids and weights it takes)
  *   mx_linear           dense MXFP8 linear layer (activation quant + MX GEMM)
+ *   mx_add_rmsnorm      residual addition + RMSNorm with MXFP8 and bf16 outputs
+ *   moe_route_mx, moe_mxfp8_forward_mx
+ *                       routing and the layer for token rows that are already
+ *                       MXFP8 (as mx_add_rmsnorm writes them)
  *   mx_pack_weights, gmm_swiglu_mxquant_packed, gmm_mx_packed,
  *   moe_mxfp8_forward_packed
  *                       load-time weight cast into the GEMMs' tile layout,
@@ -384,6 +388,70 @@ size_t mx_linear_workspace_size(int64_t T, int64_t K);
 int mx_linear(const void* x_bf16, const void* w_u8, const void* w_s,
               int64_t T, int64_t K, int64_t N, void* y_bf16,
               void* workspace, size_t ws_bytes, void* stream);
+
+/* Element types of the weight of mx_add_rmsnorm. */
+typedef enum mx_type { MX_TYPE_BF16 = 0, MX_TYPE_F32 = 1 } mx_type;
+
+/*
+ * Residual addition, root-mean-square norm and MX quantisation in one pass,
+ * the step in front of the router, the layer and the dense linears.  For each
+ * of `rows` rows of `kd` elements:
+ *   h = x + residual                (h = x without a residual)
+ *   n = h / sqrt(mean(h^2) + eps) * weight
+ *   residual_out = bf16_rne(h),  y = bf16_rne(n),
+ *   (q, s) = MX quantisation of n along kd, as mx_quantize's of a row
+ * in fp32 throughout, each output rounded once: the norm reads h before it is
+ * rounded to bf16, and q rounds n itself and not y.
+ *   x         bf16 [rows, kd], row stride ldx >= kd elements
+ *   residual  bf16 [rows, kd], row stride ldr >= kd, or NULL (ldr unused)
+ *   weight    [kd], bf16 or fp32 (weight_type); a norm that multiplies by
+ *             (1 + w) takes 1 + w in fp32
+ *   residual_out  bf16 [rows, kd] or NULL (only with a residual)
+ *   y         bf16 [rows, kd] or NULL
+ *   q, s      uint8 [rows, kd], [rows, ceil(kd/64), 2], or both NULL; at least
+ *             one of y and q is given
+ * residual_out or y may be x or the residual itself (the same address, dense
+ * rows); any other overlap of an output is MX_ERR_INVALID_ARG.  eps is a
+ * positive normal float.  Any kd from 1 to 2^24 and any alignment of whole
+ * elements (rows of a multiple of 8 elements on 16-byte boundaries, q on 8,
+ * take the fast path).  A row's mean square has to stay within fp32 (|h|
+ * below about 1e18).
+ */
+int mx_add_rmsnorm(const void* x_bf16, int64_t ldx, const void* residual_bf16,
+                   int64_t ldr, const void* weight, int weight_type, float eps,
+                   int64_t rows, int64_t kd, void* residual_out_bf16,
+                   void* y_bf16, void* q_u8, void* s_u8, void* stream);
+
+/*
+ * moe_route_quant for token rows that are MXFP8 already: q uint8 [T, K] and
+ * s uint8 [T, K/64, 2] are sent to their experts' rows as they are (xq, xs);
+ * the maps, the group list, the workspace (moe_route_quant_workspace_size,
+ * on an 8-byte boundary), the limits and the bounded waits are those of
+ * moe_route_quant.  q needs 16-byte alignment; s any.
+ */
+int moe_route_mx(const void* q_u8, const void* s_u8, const int32_t* topk_ids,
+                 int64_t T, int64_t K, int64_t k, int64_t E, void* xq_u8,
+                 void* xs_u8, int32_t* sorted_row, int32_t* expanded_row_idx,
+                 int64_t* group_list, void* workspace, size_t ws_bytes,
+                 void* stream);
+
+/* Formats of the expert weights of moe_mxfp8_forward_mx: e4m3 rows, packed
+ * e2m1 (mx_quantize_fp4), e4m3 tile-packed by mx_pack_weights. */
+typedef enum mx_weights { MX_WEIGHTS_E4M3 = 0, MX_WEIGHTS_E2M1 = 1, MX_WEIGHTS_PACKED = 2 } mx_weights;
+
+/*
+ * The whole layer on token rows that are MXFP8 already (moe_route_mx in the
+ * place of moe_route_quant), with expert weights in any of the layer's
+ * formats: moe_mxfp8_forward, moe_w4a8_forward or moe_mxfp8_forward_packed
+ * with x's quantisation left out.  Same workspace, layout and limits.
+ */
+int moe_mxfp8_forward_mx(const void* q_u8, const void* s_u8,
+                         const int32_t* topk_ids, const float* topk_w,
+                         int weight_format, const void* w13_u8,
+                         const void* w13_s, const void* w2_u8, const void* w2_s,
+                         int64_t T, int64_t K, int64_t I, int64_t E, int64_t k,
+                         void* out_bf16, void* workspace, size_t ws_bytes,
+                         void* stream);
 
 /* Description of the last non-OK status returned on this thread. */
 const char* mx_last_error(void);

@@ -25,6 +25,7 @@ __all__ = [
     "route_workspace_size", "forward_workspace_size", "last_error", "moe_router", "mx_linear",
     "linear_workspace_size", "mx_quantize_fp4", "moe_route_quant_noalloc", "mx_pack_weights", "route_set_wait_limit",
     "gmm_swiglu_mxquant_packed", "gmm_mx_packed", "moe_mxfp8_forward_packed", "gmm_mx_w4a8", "gmm_swiglu_mxquant_w4a8", "moe_w4a8_forward",
+    "mx_add_rmsnorm", "moe_route_mx", "moe_mxfp8_forward_mx",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -78,6 +79,9 @@ def load():
         "gmm_swiglu_mxquant_packed": (I32, [P, P, P, P, P, I32, I64, I64, I64, I64, P, P, P, P]),
         "gmm_mx_packed": (I32, [P, P, P, P, P, I32, I64, I64, I64, I64, P, P]),
         "moe_mxfp8_forward_packed": (I32, [P, P, P, P, P, P, P, I64, I64, I64, I64, I64, P, P, SZ, P]),
+        "mx_add_rmsnorm": (I32, [P, I64, P, I64, P, I32, ctypes.c_float, I64, I64, P, P, P, P, P]),
+        "moe_route_mx": (I32, [P, P, P, I64, I64, I64, I64, P, P, P, P, P, P, SZ, P]),
+        "moe_mxfp8_forward_mx": (I32, [P, P, P, P, I32, P, P, P, P, I64, I64, I64, I64, I64, P, P, SZ, P]),
         "mx_last_error": (ctypes.c_char_p, []),
     }
     for name, (res, args) in sig.items():
@@ -564,3 +568,187 @@ def moe_mxfp8_forward_packed(x, topk_ids, topk_w, w13_packed, w13_s, w2_packed, 
     """moe_mxfp8_forward with w13 and w2 tile-packed by mx_pack_weights."""
     return moe_mxfp8_forward(x, topk_ids, topk_w, w13_packed, w13_s, w2_packed, w2_s, out, workspace, stream,
                              _packed=True)
+
+
+# The operators below keep their per-call work on the host small (they are
+# called once per layer and decode step), and run on the device of their first
+# tensor whichever device is current.
+
+TYPE_BF16 = 0
+TYPE_F32 = 1
+
+
+def _on_device(fn):
+    """Run ``fn`` (its first argument a tensor) with that tensor's device
+    current, on the ``stream`` argument (keyword) or the device's current
+    stream.  With a stream given, what the call allocates comes from that
+    stream's pool (see _stream_scoped)."""
+    @functools.wraps(fn)
+    def wrapper(x, *args, stream=None, **kw):
+        if not isinstance(x, torch.Tensor) or not x.is_cuda:
+            return fn(x, *args, **kw)      # fails its checks
+        if stream is not None:
+            if stream.device != x.device:
+                raise ValueError(f"stream is on {stream.device}, the tensors on {x.device}")
+            with torch.cuda.stream(stream):
+                return fn(x, *args, **kw)
+        if x.device.index != torch.cuda.current_device():
+            with torch.cuda.device(x.device):
+                return fn(x, *args, **kw)
+        return fn(x, *args, **kw)
+    return wrapper
+
+
+def _rows(t, name):
+    """t [..., K] as (a 2-D view or copy, row stride) with unit inner stride."""
+    t2 = t if t.dim() == 2 else t.reshape(-1, t.shape[-1])
+    rows, k = t2.shape
+    if k > 1 and t2.stride(1) != 1:
+        raise ValueError(f"{name} must have unit stride along the last dim")
+    ld = t2.stride(0) if rows > 1 else k
+    if ld < k:
+        raise ValueError(f"{name} must not repeat its rows (row stride {ld} < {k})")
+    return t2, ld
+
+
+@_on_device
+def mx_add_rmsnorm(x, weight, residual=None, eps=1e-6, quantize=True, norm_out=False, out=None):
+    """Residual addition, RMSNorm and MX quantisation of the last dim, one pass:
+    h = x + residual, n = h / sqrt(mean(h^2) + eps) * weight in fp32.
+
+    x, residual: bf16 [..., K] (rows may be strided); weight: bf16 or fp32 [K].
+    Returns (q, s, residual_out, y): the MXFP8 of n (uint8 [..., K] and
+    [..., ceil(K/64), 2]; None without ``quantize``), bf16(h) (None without a
+    residual) and bf16(n) (None without ``norm_out``).  ``out`` gives the four
+    buffers instead, None for an output that is not wanted; its residual_out
+    or y may be x or residual itself.  ``stream`` as everywhere."""
+    _need(x, torch.bfloat16, "x")
+    if x.dim() == 0:
+        raise ValueError("x must have at least one dim")
+    shape, dev = x.shape, x.device
+    K = shape[-1]
+    if residual is not None:
+        _need(residual, torch.bfloat16, "residual")
+        if residual.shape != shape:
+            raise ValueError(f"residual must have shape {tuple(shape)}, got {tuple(residual.shape)}")
+        if residual.device != dev:
+            raise ValueError(f"residual must be on {dev}, got {residual.device}")
+    wtype = weight.dtype if isinstance(weight, torch.Tensor) else None
+    _need_shape(weight, (K,), "weight", torch.float32 if wtype is torch.float32 else torch.bfloat16, dev)
+    x2, ldx = _rows(x, "x")
+    r2, ldr = _rows(residual, "residual") if residual is not None else (None, 0)
+    s_shape = shape[:-1] + (_pairs(K), 2)
+    if out is None:
+        q = torch.empty(shape, dtype=torch.uint8, device=dev) if quantize else None
+        s = torch.empty(s_shape, dtype=torch.uint8, device=dev) if quantize else None
+        r_out = torch.empty(shape, dtype=torch.bfloat16, device=dev) if residual is not None else None
+        y = torch.empty(shape, dtype=torch.bfloat16, device=dev) if norm_out else None
+    else:
+        q, s, r_out, y = out
+        if q is not None:
+            _need_shape(q, shape, "q", torch.uint8, dev)
+        if s is not None:
+            _need_shape(s, s_shape, "s", torch.uint8, dev)
+        if r_out is not None:
+            _need_shape(r_out, shape, "residual_out", torch.bfloat16, dev)
+        if y is not None:
+            _need_shape(y, shape, "y", torch.bfloat16, dev)
+    _need_gpu(x, "x")
+    rc = load().mx_add_rmsnorm(x2.data_ptr(), ldx, _addr(r2), ldr, weight.data_ptr(),
+                               TYPE_F32 if wtype is torch.float32 else TYPE_BF16, eps, x2.shape[0], K,
+                               _addr(r_out), _addr(y), _addr(q), _addr(s), torch.cuda.current_stream().cuda_stream)
+    _check(rc, "mx_add_rmsnorm")
+    return q, s, r_out, y
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+@_on_device
+def moe_route_mx(q, s, topk_ids, E, out=None, workspace=None):
+    """moe_route_quant for rows that are MXFP8 already: q uint8 [T, K] and
+    s uint8 [T, K/64, 2] (as mx_add_rmsnorm or mx_quantize make them).
+    Returns (xq, xs, sorted_row, expanded_row_idx, group_list)."""
+    _need(q, torch.uint8, "q", 2); _need(topk_ids, torch.int32, "topk_ids", 2)
+    T, K = q.shape
+    k = topk_ids.shape[1]
+    M = T * k
+    dev = q.device
+    _need_shape(q, (T, K), "q", torch.uint8, dev)
+    _need_shape(s, (T, _pairs(K), 2), "s", torch.uint8, dev)
+    _need_shape(topk_ids, (T, k), "topk_ids", torch.int32, dev)
+    if out is None:
+        out = (torch.empty((M, K), dtype=torch.uint8, device=dev),
+               torch.empty((M, _pairs(K), 2), dtype=torch.uint8, device=dev),
+               torch.empty(M, dtype=torch.int32, device=dev),
+               torch.empty(M, dtype=torch.int32, device=dev),
+               torch.empty(E, dtype=torch.int64, device=dev))
+    xq, xs, sr, eri, gl = out
+    _need_shape(xq, (M, K), "xq", torch.uint8, dev)
+    _need_shape(xs, (M, _pairs(K), 2), "xs", torch.uint8, dev)
+    _need_shape(sr, (M,), "sorted_row", torch.int32, dev)
+    _need_shape(eri, (M,), "expanded_row_idx", torch.int32, dev)
+    _need_shape(gl, (E,), "group_list", torch.int64, dev)
+    lib = load()
+    need = lib.moe_route_quant_workspace_size(T, k, E)
+    if workspace is not None:
+        _need_workspace(workspace, need, dev)
+    _need_gpu(q, "q")
+    if workspace is None and need:
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    rc = lib.moe_route_mx(q.data_ptr(), s.data_ptr(), topk_ids.data_ptr(), T, K, k, E, xq.data_ptr(), xs.data_ptr(),
+                          sr.data_ptr(), eri.data_ptr(), gl.data_ptr(), _addr(workspace),
+                          0 if workspace is None else workspace.numel(), torch.cuda.current_stream().cuda_stream)
+    _check(rc, "moe_route_mx")
+    return xq, xs, sr, eri, gl
+
+
+WEIGHTS_E4M3 = 0     # e4m3 rows
+WEIGHTS_E2M1 = 1     # packed e2m1 (mx_quantize_fp4)
+WEIGHTS_PACKED = 2   # e4m3, tile-packed (mx_pack_weights)
+
+
+@_on_device
+def moe_mxfp8_forward_mx(q, s, topk_ids, topk_w, w13, w13_s, w2, w2_s, weight_format=WEIGHTS_E4M3, out=None,
+                         workspace=None):
+    """The whole layer on token rows that are MXFP8 already (q uint8 [T, K],
+    s uint8 [T, K/64, 2]); weights as moe_mxfp8_forward, moe_w4a8_forward or
+    moe_mxfp8_forward_packed take them, by ``weight_format``.  Returns out
+    [T, K] bf16."""
+    _need(q, torch.uint8, "q", 2); _need(topk_ids, torch.int32, "topk_ids", 2)
+    _need(w13, torch.uint8, "w13", 3)
+    if weight_format not in (WEIGHTS_E4M3, WEIGHTS_E2M1, WEIGHTS_PACKED):
+        raise ValueError(f"weight_format must be 0, 1 or 2, got {weight_format}")
+    w4 = weight_format == WEIGHTS_E2M1
+    T, K = q.shape
+    k = topk_ids.shape[1]
+    E, twoI, Kw = w13.shape
+    Kb = K // 2 if w4 else K
+    if Kw != Kb or twoI % 2:
+        raise ValueError(f"w13 must be [E, 2I, {Kb}], got {tuple(w13.shape)}")
+    I = twoI // 2
+    dev = q.device
+    _need_shape(q, (T, K), "q", torch.uint8, dev)
+    _need_shape(s, (T, _pairs(K), 2), "s", torch.uint8, dev)
+    _need_shape(topk_ids, (T, k), "topk_ids", torch.int32, dev)
+    _need_shape(topk_w, (T, k), "topk_w", torch.float32, dev)
+    _need_shape(w13, (E, twoI, Kb), "w13", torch.uint8, dev)
+    _need_shape(w13_s, (E, twoI, _pairs(K), 2), "w13_s", torch.uint8, dev)
+    _need_shape(w2, (E, K, I // 2 if w4 else I), "w2", torch.uint8, dev)
+    _need_shape(w2_s, (E, K, _pairs(I), 2), "w2_s", torch.uint8, dev)
+    if out is not None:
+        _need_shape(out, (T, K), "out", torch.bfloat16, dev)
+    if workspace is not None:
+        _need_workspace(workspace, forward_workspace_size(T, K, I, E, k), dev)
+    _need_gpu(q, "q")
+    if out is None:
+        out = torch.empty((T, K), dtype=torch.bfloat16, device=dev)
+    if workspace is None:
+        workspace = forward_workspace(T, K, I, E, k, dev)
+    rc = load().moe_mxfp8_forward_mx(q.data_ptr(), s.data_ptr(), topk_ids.data_ptr(), topk_w.data_ptr(),
+                                     weight_format, w13.data_ptr(), w13_s.data_ptr(), w2.data_ptr(), w2_s.data_ptr(),
+                                     T, K, I, E, k, out.data_ptr(), workspace.data_ptr(), workspace.numel(),
+                                     torch.cuda.current_stream().cuda_stream)
+    _check(rc, "moe_mxfp8_forward_mx")
+    return out

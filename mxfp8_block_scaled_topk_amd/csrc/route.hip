@@ -44,6 +44,10 @@
 //
 // The order inside an expert is the flat index order, so the permutation is
 // deterministic and equals a stable sort by expert.
+//
+// moe_route_mx is the same routing for rows that are already MXFP8 (kMx): a
+// share's payload and scale rows go to LDS as they are instead of being
+// quantised on the way.
 #include <algorithm>
 #include <atomic>
 #include <chrono>
@@ -74,7 +78,9 @@ constexpr int kScatterPerCU = 4;
 constexpr int kSingleShares = 16;
 
 struct RouteParams {
-  const uint16_t* x;
+  const uint16_t* x;     // bf16 rows (moe_route_quant)
+  const uint8_t* mxq;    // MXFP8 rows and their scales (moe_route_mx)
+  const uint8_t* mxs;
   const int32_t* ids;
   uint8_t* xq;
   uint8_t* xs;
@@ -93,7 +99,7 @@ struct RouteParams {
   int nbuf;             // tokens of a share quantised into LDS before the wait
   int row_bytes;        // LDS bytes per such token: K payload, then the scales, padded to 16
   int lds_ints;         // dynamic LDS of the launch, in ints
-  int scales16;         // xs rows can be written 16 bytes at a time
+  int scales16;         // xs rows can be written (and mxs rows read) 16 bytes at a time
 };
 
 // Exclusive scan of v[0..n) (n <= 1024) into out[0..n) by one 256-thread block.
@@ -257,8 +263,9 @@ __device__ __forceinline__ void quant_half_block(const RouteParams& p, int64_t t
   quant_half_regs(src[0], src[1], q, sb);
 }
 
-// kSingle: all assignments in one chunk (no leaders, no waits).
-template <bool kSingle>
+// kSingle: all assignments in one chunk (no leaders, no waits).  kMx: the
+// token rows are MXFP8 already.
+template <bool kSingle, bool kMx>
 __global__ __launch_bounds__(kThreads) void route_quant_kernel(RouteParams p) {
   // dynamic LDS: [4E ints: per-wave expert counts, or a leader's chunk counts
   // (its whole LDS)] [kThreads ints: s_pos] [the share's quantised rows,
@@ -341,7 +348,42 @@ __global__ __launch_bounds__(kThreads) void route_quant_kernel(RouteParams p) {
   const int rowb = p.row_bytes;   // payload K bytes, then s_stride scale bytes, padded to 16
   const int n_it = nbt * hpr;     // half-blocks; even, so lane pairs stay together
   constexpr int kLd = 4;          // half-blocks whose loads a lane has in flight at once
-  for (int it0 = tid; it0 < n_it; it0 += kLd * kThreads) {
+  if constexpr (kMx) {
+    // a payload row is hpr 16-byte pieces
+    for (int it0 = tid; it0 < n_it; it0 += kLd * kThreads) {
+      uint4 u[kLd];
+#pragma unroll
+      for (int i = 0; i < kLd; ++i) {
+        const int it = it0 + i * kThreads;
+        if (it < n_it) {
+          const int tl = it / hpr, hb = it - tl * hpr;
+          u[i] = *reinterpret_cast<const uint4*>(p.mxq + (t0 + tb + tl) * p.K + hb * 16);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kLd; ++i) {
+        const int it = it0 + i * kThreads;
+        if (it < n_it) {
+          const int tl = it / hpr, hb = it - tl * hpr;
+          *reinterpret_cast<uint4*>(xbuf + tl * rowb + hb * 16) = u[i];
+        }
+      }
+    }
+    if (p.scales16) {
+      const int s16 = s_stride / 16;
+      for (int it = tid; it < nbt * s16; it += kThreads) {
+        const int tl = it / s16, ch = it - tl * s16;
+        *reinterpret_cast<uint4*>(xbuf + tl * rowb + p.K + ch * 16) =
+            *reinterpret_cast<const uint4*>(p.mxs + (t0 + tb + tl) * s_stride + ch * 16);
+      }
+    } else {
+      for (int it = tid; it < nbt * s_stride; it += kThreads) {
+        const int tl = it / s_stride, ch = it - tl * s_stride;
+        xbuf[tl * rowb + p.K + ch] = p.mxs[(t0 + tb + tl) * s_stride + ch];
+      }
+    }
+  }
+  for (int it0 = tid; !kMx && it0 < n_it; it0 += kLd * kThreads) {
     uint4 u[kLd][2];
 #pragma unroll
     for (int i = 0; i < kLd; ++i) {
@@ -500,14 +542,20 @@ __global__ __launch_bounds__(kThreads) void route_quant_kernel(RouteParams p) {
     const int half = hb & 1;
     uint4 q;
     uint32_t sb;
-    quant_half_block(p, t0 + tl, b, half, q, sb);
+    if constexpr (kMx) {
+      q = *reinterpret_cast<const uint4*>(p.mxq + (t0 + tl) * p.K + hb * 16);
+      sb = p.mxs[(t0 + tl) * s_stride + b];
+    } else {
+      quant_half_block(p, t0 + tl, b, half, q, sb);
+    }
     for (int j = 0; j < k; ++j) {
       const int r = s_pos[tl * k + j];
       if (r < 0) continue;
       *reinterpret_cast<uint4*>(p.xq + (int64_t)r * p.K + (b * 32 + half * 16)) = q;
       if (half == 0) {
         p.xs[(int64_t)r * s_stride + b] = static_cast<uint8_t>(sb);
-        if ((nb & 1) && b == nb - 1) p.xs[(int64_t)r * s_stride + nb] = 0;
+        if ((nb & 1) && b == nb - 1)
+          p.xs[(int64_t)r * s_stride + nb] = kMx ? p.mxs[(t0 + tl) * s_stride + nb] : 0;
       }
     }
   }
@@ -574,25 +622,28 @@ size_t route_workspace_bytes(int64_t T, int64_t k, int64_t E) {
          align_up((size_t)(s.S + 1) * 8, 256);
 }
 
-int check_route_args(int64_t T, int64_t K, int64_t k, int64_t E) {
+int check_route_args(int64_t T, int64_t K, int64_t k, int64_t E, const char* name) {
   if (T < 0 || K <= 0 || k <= 0 || E <= 0)
-    return fail(MX_ERR_INVALID_ARG, "moe_route_quant: bad sizes T=%lld K=%lld k=%lld E=%lld",
+    return fail(MX_ERR_INVALID_ARG, "%s: bad sizes T=%lld K=%lld k=%lld E=%lld", name,
                 (long long)T, (long long)K, (long long)k, (long long)E);
-  if (k > E) return fail(MX_ERR_INVALID_ARG, "moe_route_quant: k=%lld > E=%lld", (long long)k, (long long)E);
-  if (!dims_in_range({T, K})) return fail(MX_ERR_UNSUPPORTED, "moe_route_quant: T or K above 2^31 - 1");
-  if (K % 32 != 0) return fail(MX_ERR_UNSUPPORTED, "moe_route_quant: K=%lld is not a multiple of 32", (long long)K);
-  if (K > (int64_t)1 << 24) return fail(MX_ERR_UNSUPPORTED, "moe_route_quant: K=%lld > 2^24", (long long)K);
-  if (k > kThreads) return fail(MX_ERR_UNSUPPORTED, "moe_route_quant: k=%lld > %d", (long long)k, kThreads);
-  if (E > kMaxE) return fail(MX_ERR_UNSUPPORTED, "moe_route_quant: E=%lld > %d", (long long)E, kMaxE);
+  if (k > E) return fail(MX_ERR_INVALID_ARG, "%s: k=%lld > E=%lld", name, (long long)k, (long long)E);
+  if (!dims_in_range({T, K})) return fail(MX_ERR_UNSUPPORTED, "%s: T or K above 2^31 - 1", name);
+  if (K % 32 != 0) return fail(MX_ERR_UNSUPPORTED, "%s: K=%lld is not a multiple of 32", name, (long long)K);
+  if (K > (int64_t)1 << 24) return fail(MX_ERR_UNSUPPORTED, "%s: K=%lld > 2^24", name, (long long)K);
+  if (k > kThreads) return fail(MX_ERR_UNSUPPORTED, "%s: k=%lld > %d", name, (long long)k, kThreads);
+  if (E > kMaxE) return fail(MX_ERR_UNSUPPORTED, "%s: E=%lld > %d", name, (long long)E, kMaxE);
   // the launch holds 16 workgroups of 256 threads per 256 assignments, and a
   // grid holds fewer than 2^32 threads
-  if (T * k > (int64_t)1 << 27) return fail(MX_ERR_UNSUPPORTED, "moe_route_quant: T*k > 2^27");
+  if (T * k > (int64_t)1 << 27) return fail(MX_ERR_UNSUPPORTED, "%s: T*k > 2^27", name);
   return MX_OK;
 }
 
-int launch_route_quant(const uint16_t* x, const int32_t* ids, int64_t T, int64_t K, int64_t k,
-                       int64_t E, uint8_t* xq, uint8_t* xs, int32_t* sorted_row, int32_t* eri,
-                       int64_t* group_list, void* ws, hipStream_t stream) {
+namespace {
+
+// x: bf16 rows, or null when the rows are MXFP8 (mxq, mxs).
+int launch_route(const uint16_t* x, const uint8_t* mxq, const uint8_t* mxs, const int32_t* ids, int64_t T, int64_t K,
+                 int64_t k, int64_t E, uint8_t* xq, uint8_t* xs, int32_t* sorted_row, int32_t* eri,
+                 int64_t* group_list, void* ws, hipStream_t stream) {
   if (T == 0) {
     zero_i64<<<dim3((unsigned)((E + 255) / 256)), dim3(256), 0, stream>>>(group_list, (int)E);
     return check_launch("moe_route_quant(zero)");
@@ -600,6 +651,8 @@ int launch_route_quant(const uint16_t* x, const int32_t* ids, int64_t T, int64_t
   const Split sp = split_of(T, k);
   RouteParams p{};
   p.x = x;
+  p.mxq = mxq;
+  p.mxs = mxs;
   p.ids = ids;
   p.xq = xq;
   p.xs = xs;
@@ -646,10 +699,12 @@ int launch_route_quant(const uint16_t* x, const int32_t* ids, int64_t T, int64_t
   p.row_bytes = (int)row_bytes;
   const size_t lds = (size_t)(4 * E + kThreads) * 4 + (size_t)p.nbuf * (size_t)row_bytes;
   p.lds_ints = (int)(lds / 4);
-  p.scales16 = (reinterpret_cast<uintptr_t>(xs) % 16 == 0 && s_stride % 16 == 0) ? 1 : 0;
+  p.scales16 =
+      ((reinterpret_cast<uintptr_t>(xs) | reinterpret_cast<uintptr_t>(mxs)) % 16 == 0 && s_stride % 16 == 0) ? 1 : 0;
   const int64_t grid = sp.S + sp.nch * split;
   if (sp.S == 0) {
-    route_quant_kernel<true><<<dim3((unsigned)grid), dim3(kThreads), lds, stream>>>(p);
+    if (x) route_quant_kernel<true, false><<<dim3((unsigned)grid), dim3(kThreads), lds, stream>>>(p);
+    else route_quant_kernel<true, true><<<dim3((unsigned)grid), dim3(kThreads), lds, stream>>>(p);
   } else {
     hipStreamCaptureStatus cs = hipStreamCaptureStatusNone;
     if (hipStreamIsCapturing(stream, &cs) != hipSuccess)
@@ -659,9 +714,24 @@ int launch_route_quant(const uint16_t* x, const int32_t* ids, int64_t T, int64_t
       const int rc = check_launch("moe_route_quant(generation)");
       if (rc) return rc;
     }
-    route_quant_kernel<false><<<dim3((unsigned)grid), dim3(kThreads), lds, stream>>>(p);
+    if (x) route_quant_kernel<false, false><<<dim3((unsigned)grid), dim3(kThreads), lds, stream>>>(p);
+    else route_quant_kernel<false, true><<<dim3((unsigned)grid), dim3(kThreads), lds, stream>>>(p);
   }
   return check_launch("route_quant_kernel");
+}
+
+}  // namespace
+
+int launch_route_quant(const uint16_t* x, const int32_t* ids, int64_t T, int64_t K, int64_t k,
+                       int64_t E, uint8_t* xq, uint8_t* xs, int32_t* sorted_row, int32_t* eri,
+                       int64_t* group_list, void* ws, hipStream_t stream) {
+  return launch_route(x, nullptr, nullptr, ids, T, K, k, E, xq, xs, sorted_row, eri, group_list, ws, stream);
+}
+
+int launch_route_mx(const uint8_t* q, const uint8_t* s, const int32_t* ids, int64_t T, int64_t K, int64_t k,
+                    int64_t E, uint8_t* xq, uint8_t* xs, int32_t* sorted_row, int32_t* eri, int64_t* group_list,
+                    void* ws, hipStream_t stream) {
+  return launch_route(nullptr, q, s, ids, T, K, k, E, xq, xs, sorted_row, eri, group_list, ws, stream);
 }
 
 }  // namespace mxmoe
@@ -672,7 +742,7 @@ extern "C" int64_t moe_route_quant_set_wait_limit(int64_t polls) {
 
 extern "C" size_t moe_route_quant_workspace_size(int64_t T, int64_t k, int64_t E) {
   // 0 for sizes the routing rejects (the workspace of a call that fails)
-  if (mxmoe::check_route_args(T, 32, k, E) != MX_OK) return 0;
+  if (mxmoe::check_route_args(T, 32, k, E, "moe_route_quant") != MX_OK) return 0;
   return mxmoe::route_workspace_bytes(T, k, E);
 }
 
@@ -681,7 +751,7 @@ extern "C" int moe_route_quant(const void* x_bf16, const int32_t* topk_ids, int6
                                int32_t* expanded_row_idx, int64_t* group_list, void* workspace,
                                size_t ws_bytes, void* stream) {
   using namespace mxmoe;
-  int rc = check_route_args(T, K, k, E);
+  int rc = check_route_args(T, K, k, E, "moe_route_quant");
   if (rc) return rc;
   const size_t need = route_workspace_bytes(T, k, E);
   if (!group_list || (need > 0 && !workspace)) return fail(MX_ERR_INVALID_ARG, "moe_route_quant: null pointer");
@@ -694,6 +764,27 @@ extern "C" int moe_route_quant(const void* x_bf16, const int32_t* topk_ids, int6
   return launch_route_quant(static_cast<const uint16_t*>(x_bf16), topk_ids, T, K, k, E,
                             static_cast<uint8_t*>(xq_u8), static_cast<uint8_t*>(xs_u8), sorted_row,
                             expanded_row_idx, group_list, workspace, as_stream(stream));
+}
+
+extern "C" int moe_route_mx(const void* q_u8, const void* s_u8, const int32_t* topk_ids, int64_t T, int64_t K,
+                            int64_t k, int64_t E, void* xq_u8, void* xs_u8, int32_t* sorted_row,
+                            int32_t* expanded_row_idx, int64_t* group_list, void* workspace, size_t ws_bytes,
+                            void* stream) {
+  using namespace mxmoe;
+  int rc = check_route_args(T, K, k, E, "moe_route_mx");
+  if (rc) return rc;
+  const size_t need = route_workspace_bytes(T, k, E);
+  if (!group_list || (need > 0 && !workspace)) return fail(MX_ERR_INVALID_ARG, "moe_route_mx: null pointer");
+  if (T > 0 && (!q_u8 || !s_u8 || !topk_ids || !xq_u8 || !xs_u8 || !sorted_row || !expanded_row_idx))
+    return fail(MX_ERR_INVALID_ARG, "moe_route_mx: null pointer");
+  if (ws_bytes < need)
+    return fail(MX_ERR_WORKSPACE, "moe_route_mx: workspace %zu bytes < %zu needed", ws_bytes, need);
+  if (reinterpret_cast<uintptr_t>(q_u8) % 16 || reinterpret_cast<uintptr_t>(xq_u8) % 16 ||
+      reinterpret_cast<uintptr_t>(workspace) % 8)
+    return fail(MX_ERR_UNSUPPORTED, "moe_route_mx: q and xq must be 16-byte aligned, the workspace 8-byte");
+  return launch_route_mx(static_cast<const uint8_t*>(q_u8), static_cast<const uint8_t*>(s_u8), topk_ids, T, K, k, E,
+                         static_cast<uint8_t*>(xq_u8), static_cast<uint8_t*>(xs_u8), sorted_row, expanded_row_idx,
+                         group_list, workspace, as_stream(stream));
 }
 
 // ---------------------------------------------------------------------------
@@ -747,7 +838,7 @@ extern "C" int moe_route_quant_noalloc(const void* x_bf16, const int32_t* topk_i
                                        int64_t k, int64_t E, void* xq_u8, void* xs_u8, int32_t* sorted_row,
                                        int32_t* expanded_row_idx, int64_t* group_list, void* stream) {
   using namespace mxmoe;
-  int rc = check_route_args(T, K, k, E);
+  int rc = check_route_args(T, K, k, E, "moe_route_quant");
   if (rc) return rc;
   if (!group_list) return fail(MX_ERR_INVALID_ARG, "moe_route_quant_noalloc: null pointer");
   if (T > 0 && (!x_bf16 || !topk_ids || !xq_u8 || !xs_u8 || !sorted_row || !expanded_row_idx))
