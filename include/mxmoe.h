@@ -17,6 +17,8 @@
  *   moe_router          top-k softmax router over a bf16 gate (upstream of
  *                       the layer: produces the ids and weights it takes)
  *   mx_linear           dense MXFP8 linear layer (activation quant + MX GEMM)
+ *   mx_linear_fused     dense MXFP8 linear layer with bias, activation and
+ *                       residual in its epilogue, bf16 or MXFP8 in and out
  *   mx_add_rmsnorm      residual addition + RMSNorm with MXFP8 and bf16 outputs
  *   moe_route_mx, moe_mxfp8_forward_mx
  *                       routing and the layer for token rows that are already
@@ -389,7 +391,7 @@ int mx_linear(const void* x_bf16, const void* w_u8, const void* w_s,
               int64_t T, int64_t K, int64_t N, void* y_bf16,
               void* workspace, size_t ws_bytes, void* stream);
 
-/* Element types of the weight of mx_add_rmsnorm. */
+/* Element types of a norm's weight and of a linear's bias. */
 typedef enum mx_type { MX_TYPE_BF16 = 0, MX_TYPE_F32 = 1 } mx_type;
 
 /*
@@ -452,6 +454,41 @@ int moe_mxfp8_forward_mx(const void* q_u8, const void* s_u8,
                          int64_t T, int64_t K, int64_t I, int64_t E, int64_t k,
                          void* out_bf16, void* workspace, size_t ws_bytes,
                          void* stream);
+
+/* Activations of mx_linear_fused: none; max(z, 0); z / (1 + e^-z);
+ * z Phi(z); (z / 2)(1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))). */
+typedef enum mx_activation {
+  MX_ACT_NONE = 0, MX_ACT_RELU = 1, MX_ACT_SILU = 2, MX_ACT_GELU = 3, MX_ACT_GELU_TANH = 4
+} mx_activation;
+
+/* Workspace bytes mx_linear_fused needs (x_is_mx: x comes as MXFP8). */
+size_t mx_linear_fused_workspace_size(int64_t T, int64_t K, int64_t N, int x_is_mx);
+
+/*
+ * mx_linear with its epilogue fused and without its limits on the sizes:
+ *   z[t, n]   = sum over 32-blocks b of 2^(sx[t,b] + sw[n,b]) * (xq[t,b] . wq[n,b])
+ *   out[t, n] = activation(z[t, n] + bias[n]) + residual[t, n]
+ * in fp32, rounded once: to bf16 (y), or along n to MXFP8 (yq, ys: the x of
+ * the next linear, or the rows of moe_route_mx).
+ *   x         uint8 [T, K] e4m3 with x_s uint8 [T, ceil(K/64), 2], or with a
+ *             NULL x_s bf16 [T, K], quantised first (as mx_quantize) into
+ *             the workspace
+ *   w, w_s    uint8 [N, K], [N, ceil(K/64), 2]
+ *   bias      [N] bf16 or fp32 (bias_type), or NULL
+ *   residual  bf16 [T, N] or NULL
+ *   y         bf16 [T, N], or yq uint8 [T, N] and ys uint8 [T, ceil(N/64), 2]
+ *             (an odd count of scales padded with a zero byte)
+ * y may be the residual itself (the same address); any other overlap of an
+ * output with another buffer of the call is MX_ERR_INVALID_ARG.  Limits:
+ * K % 32 == 0, K <= 2^20; T and N as they are.  Alignment: MXFP8 payloads that
+ * are read on 16-byte boundaries, their scales on 4, the workspace on 256.
+ */
+int mx_linear_fused(const void* x, const void* x_s, const void* w_u8,
+                    const void* w_s, const void* bias, int bias_type,
+                    int activation, const void* residual_bf16, int64_t T,
+                    int64_t K, int64_t N, void* y_bf16, void* yq_u8,
+                    void* ys_u8, void* workspace, size_t ws_bytes,
+                    void* stream);
 
 /* Description of the last non-OK status returned on this thread. */
 const char* mx_last_error(void);

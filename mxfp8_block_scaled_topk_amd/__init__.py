@@ -25,7 +25,7 @@ __all__ = [
     "route_workspace_size", "forward_workspace_size", "last_error", "moe_router", "mx_linear",
     "linear_workspace_size", "mx_quantize_fp4", "moe_route_quant_noalloc", "mx_pack_weights", "route_set_wait_limit",
     "gmm_swiglu_mxquant_packed", "gmm_mx_packed", "moe_mxfp8_forward_packed", "gmm_mx_w4a8", "gmm_swiglu_mxquant_w4a8", "moe_w4a8_forward",
-    "mx_add_rmsnorm", "moe_route_mx", "moe_mxfp8_forward_mx",
+    "mx_linear_fused", "linear_fused_workspace_size", "mx_add_rmsnorm", "moe_route_mx", "moe_mxfp8_forward_mx",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -82,6 +82,8 @@ def load():
         "mx_add_rmsnorm": (I32, [P, I64, P, I64, P, I32, ctypes.c_float, I64, I64, P, P, P, P, P]),
         "moe_route_mx": (I32, [P, P, P, I64, I64, I64, I64, P, P, P, P, P, P, SZ, P]),
         "moe_mxfp8_forward_mx": (I32, [P, P, P, P, I32, P, P, P, P, I64, I64, I64, I64, I64, P, P, SZ, P]),
+        "mx_linear_fused_workspace_size": (SZ, [I64, I64, I64, I32]),
+        "mx_linear_fused": (I32, [P, P, P, P, P, I32, I32, P, I64, I64, I64, P, P, P, P, SZ, P]),
         "mx_last_error": (ctypes.c_char_p, []),
     }
     for name, (res, args) in sig.items():
@@ -752,3 +754,73 @@ def moe_mxfp8_forward_mx(q, s, topk_ids, topk_w, w13, w13_s, w2, w2_s, weight_fo
                                      torch.cuda.current_stream().cuda_stream)
     _check(rc, "moe_mxfp8_forward_mx")
     return out
+
+
+ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
+
+
+def linear_fused_workspace_size(T, K, N, x_is_mx):
+    return int(load().mx_linear_fused_workspace_size(T, K, N, int(x_is_mx)))
+
+
+@_on_device
+def mx_linear_fused(x, w, w_s, x_s=None, bias=None, act="none", residual=None, quantize_out=False, out=None,
+                    workspace=None):
+    """Dense MXFP8 linear with its epilogue: act(x . w^T + bias) + residual in
+    fp32, rounded once.
+
+    x: bf16 [T, K], or uint8 [T, K] with x_s uint8 [T, ceil(K/64), 2]; w, w_s:
+    uint8 [N, K], [N, ceil(K/64), 2] (as mx_quantize makes them); bias: bf16 or
+    fp32 [N]; act: a key of ACTIVATIONS; residual: bf16 [T, N].
+    Returns y bf16 [T, N], or with ``quantize_out`` its MXFP8 (yq uint8 [T, N],
+    ys uint8 [T, ceil(N/64), 2]).  ``out`` gives that tensor or pair instead
+    (y may be the residual).  ``stream`` as everywhere."""
+    mx_in = x_s is not None
+    _need(x, torch.uint8 if mx_in else torch.bfloat16, "x", 2); _need(w, torch.uint8, "w", 2)
+    T, K = x.shape
+    N = w.shape[0]
+    dev = x.device
+    _need_shape(x, (T, K), "x", x.dtype, dev)
+    if mx_in:
+        _need_shape(x_s, (T, _pairs(K), 2), "x_s", torch.uint8, dev)
+    _need_shape(w, (N, K), "w", torch.uint8, dev)
+    _need_shape(w_s, (N, _pairs(K), 2), "w_s", torch.uint8, dev)
+    btype = TYPE_BF16
+    if bias is not None:
+        if isinstance(bias, torch.Tensor) and bias.dtype is torch.float32:
+            btype = TYPE_F32
+        _need_shape(bias, (N,), "bias", torch.float32 if btype else torch.bfloat16, dev)
+    if act not in ACTIVATIONS:
+        raise ValueError(f"act must be one of {', '.join(ACTIVATIONS)}, got {act!r}")
+    if residual is not None:
+        _need_shape(residual, (T, N), "residual", torch.bfloat16, dev)
+    if out is not None:
+        quantize_out = isinstance(out, (tuple, list))
+    y = yq = ys = None
+    if quantize_out:
+        yq, ys = out if out is not None else (None, None)
+        if out is not None:
+            _need_shape(yq, (T, N), "yq", torch.uint8, dev)
+            _need_shape(ys, (T, _pairs(N), 2), "ys", torch.uint8, dev)
+    elif out is not None:
+        y = out
+        _need_shape(y, (T, N), "out", torch.bfloat16, dev)
+    lib = load()
+    need = lib.mx_linear_fused_workspace_size(T, K, N, mx_in)
+    if workspace is not None:
+        _need_workspace(workspace, need, dev)
+    _need_gpu(x, "x")
+    if workspace is None and need:
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    if out is None:
+        if quantize_out:
+            yq = torch.empty((T, N), dtype=torch.uint8, device=dev)
+            ys = torch.empty((T, _pairs(N), 2), dtype=torch.uint8, device=dev)
+        else:
+            y = torch.empty((T, N), dtype=torch.bfloat16, device=dev)
+    rc = lib.mx_linear_fused(x.data_ptr(), _addr(x_s), w.data_ptr(), w_s.data_ptr(), _addr(bias), btype,
+                             ACTIVATIONS[act], _addr(residual), T, K, N, _addr(y), _addr(yq), _addr(ys),
+                             _addr(workspace), 0 if workspace is None else workspace.numel(),
+                             torch.cuda.current_stream().cuda_stream)
+    _check(rc, "mx_linear_fused")
+    return (yq, ys) if quantize_out else y

@@ -1,0 +1,114 @@
+// Shared by the kernels of mx_linear_fused: parameters, the direct
+// global->LDS loads and the epilogue's arithmetic.
+#pragma once
+
+#include "fused.h"
+
+namespace mxmoe {
+
+struct LinParams {
+  const uint8_t* x;    // [T, K] e4m3
+  const uint8_t* xs;   // [T, s_stride] e8m0
+  const uint8_t* w;    // [N, K] e4m3
+  const uint8_t* ws;   // [N, s_stride] e8m0
+  const void* bias;    // [N] bf16 or fp32, or null
+  const uint16_t* res; // [T, N] bf16, or null
+  uint16_t* y;         // [T, N] bf16, or null: then yq and ys
+  uint8_t* yq;         // [T, N] e4m3
+  uint8_t* ys;         // [T, ys_stride] e8m0
+  int64_t T, K, N;
+  int64_t s_stride, ys_stride;
+  int nk;              // 128-element k stages, the last one with
+  int tail_blocks;     // this many 32-element blocks (1 .. 4)
+  int bias_f32;
+  int act;             // mx_activation
+};
+
+typedef int v8i __attribute__((ext_vector_type(8)));
+typedef float v16f __attribute__((ext_vector_type(16)));
+typedef __attribute__((address_space(3))) uint8_t lds_u8;
+
+constexpr int kStageK = 128;   // elements (bytes) of a row per k stage
+
+__device__ __forceinline__ uint32_t lds_offset(const void* p) {
+  return (uint32_t)(uintptr_t)(const lds_u8*)p;
+}
+// Direct global->LDS loads: lane l's bytes land at lds + l * 16 (or * 4).
+// Uniform base plus a per-lane 32-bit offset:
+__device__ __forceinline__ void load_lds16(uint32_t voff, const void* sbase, uint32_t lds) {
+  asm volatile("global_load_lds_dwordx4 %0, %1" ::"v"(voff), "s"(sbase), "{m0}"(lds) : "memory");
+}
+// Per-lane addresses:
+__device__ __forceinline__ void load_lds4(const uint8_t* p, uint32_t lds) {
+  asm volatile("global_load_lds_dword %0, off" ::"v"(p), "{m0}"(lds) : "memory");
+}
+// two bytes per lane, zero-extended to the lane's LDS word
+__device__ __forceinline__ void load_lds2(const uint8_t* p, uint32_t lds) {
+  asm volatile("global_load_lds_ushort %0, off" ::"v"(p), "{m0}"(lds) : "memory");
+}
+template <int N>
+__device__ __forceinline__ void wait_loads() {   // at most N loads outstanding
+  static_assert(N >= 0 && N < 64, "vmcnt range");
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+// every LDS read of this wave has returned
+__device__ __forceinline__ void wait_lds() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
+
+// erfc(x) / 2 for x >= 0, as t exp(g(t) - x^2) with t = 1 / (1 + x / 2): g is
+// the degree-9 polynomial through log(erfc(x) exp(x^2) / (2 t)) at Chebyshev
+// nodes in t over 0 <= x <= 12.  Its relative error is under 4e-7 in fp32 up to
+// the exponential's own, so gelu keeps its digits in the left tail, where
+// 1 + erf(x) would cancel.
+__device__ __forceinline__ float half_erfc(float x) {
+  const float t = __builtin_amdgcn_rcpf(fmaf(0.5f, x, 1.0f));
+  float g = 0.15775100886821747f;
+  g = fmaf(g, t, -0.7501815557479858f);
+  g = fmaf(g, t, 1.3186529874801636f);
+  g = fmaf(g, t, -0.909740686416626f);
+  g = fmaf(g, t, 0.09432142972946167f);
+  g = fmaf(g, t, -0.09025566279888153f);
+  g = fmaf(g, t, 0.06523264944553375f);
+  g = fmaf(g, t, 0.3803541362285614f);
+  g = fmaf(g, t, 0.9993481040000916f);
+  g = fmaf(g, t, -1.9586294889450073f);
+  return t * __expf(fmaf(-x, x, g));
+}
+
+// The activation of n values (act is uniform over the launch).  The hardware
+// exp and reciprocal are good to about 1 ulp; every form below is a product
+// whose factors keep their relative accuracy over the whole range.
+template <int n>
+__device__ __forceinline__ void activate(float (&z)[n], int act) {
+  switch (act) {
+    case MX_ACT_RELU:
+#pragma unroll
+      for (int i = 0; i < n; ++i) z[i] = fmaxf(z[i], 0.0f);
+      break;
+    case MX_ACT_SILU:   // z / (1 + e^-z)
+#pragma unroll
+      for (int i = 0; i < n; ++i) z[i] *= __builtin_amdgcn_rcpf(1.0f + __expf(-z[i]));
+      break;
+    case MX_ACT_GELU:   // z Phi(z), Phi(z) = erfc(-z / sqrt 2) / 2
+#pragma unroll
+      for (int i = 0; i < n; ++i) {
+        const float e = half_erfc(fabsf(z[i]) * 0.70710678118654752f);
+        z[i] *= z[i] > 0.0f ? 1.0f - e : e;
+      }
+      break;
+    case MX_ACT_GELU_TANH:   // (z / 2)(1 + tanh u) = z / (1 + e^-2u)
+#pragma unroll
+      for (int i = 0; i < n; ++i) {
+        const float u2 = z[i] * fmaf(z[i] * z[i], 2.0f * 0.79788456080286536f * 0.044715f, 2.0f * 0.79788456080286536f);
+        z[i] *= __builtin_amdgcn_rcpf(1.0f + __expf(-u2));
+      }
+      break;
+    default:
+      break;
+  }
+}
+
+__device__ __forceinline__ float bias_at(const LinParams& p, int64_t n) {
+  return p.bias_f32 ? static_cast<const float*>(p.bias)[n] : bf16_to_f32(static_cast<const uint16_t*>(p.bias)[n]);
+}
+
+}  // namespace mxmoe

@@ -1,0 +1,359 @@
+// mx_linear_fused: a dense MXFP8 linear layer with its epilogue fused:
+//
+//   z[t, n] = sum over 32-blocks b of 2^(sx[t,b] + sw[n,b]) (xq[t,b] . wq[n,b])
+//   out     = act(z + bias) + residual      fp32, rounded once: to bf16, or
+//             per 32 outputs to MXFP8
+//
+// The MFMA orientation and operand layout are the grouped GEMMs': weight rows
+// are the A operand, tokens the B operand of V_MFMA_SCALE_F32_32X32X64 (lane l
+// holds operand row l % 32; of its 32 bytes, 0-15 and 16-31 belong to scale
+// blocks 0 and 1 of the 64-wide step, lane group l / 32 supplying 16 elements
+// of each; output lane l holds token l % 32 and features 8 q + 4 (l / 32) +
+// (0..3) in accumulator elements 4 q ..).
+//
+// lin_stream_kernel.  A workgroup of WV waves computes 32 NF weight rows x
+// 32 MF tokens; the waves share the tile and split K (wave w takes the
+// 128-element stages w, w + WV, ...), so the waves of a workgroup read whole
+// kilobytes of a weight row together.  Each wave streams its stages through an
+// LDS ring of its own by direct global->LDS loads, S stages ahead, with no
+// barrier in the loop; the accumulators meet in LDS at the end.
+#include <algorithm>
+
+#include "linear_fused.h"
+
+namespace mxmoe {
+
+int launch_mx_quantize(const uint16_t* x, int64_t rows, int64_t kd, int64_t ld, uint8_t* q, uint8_t* s,
+                       hipStream_t stream);
+
+namespace {
+
+constexpr int64_t kMaxK = (int64_t)1 << 20;   // 32-bit offsets within a tile's rows
+
+// byte offset of 16-byte chunk c of row r in a tile of 128-byte rows: the 16
+// lanes of one LDS access (consecutive rows, one chunk) hit distinct banks
+__device__ __forceinline__ int swz(int r, int c) { return r * kStageK + ((c ^ ((r >> 1) & 7)) << 4); }
+
+// kTail: K is not a multiple of 128.  The last stage's absent blocks repeat
+// bytes of the row's first present ones (nothing past a row is read), and the
+// token operand's are zeroed, so they add nothing; scale rows are then only
+// 2-byte aligned and come two bytes at a time.
+template <int NF, int MF, int WV, int S, bool kTail>
+__global__ __launch_bounds__(64 * WV) void lin_stream_kernel(LinParams p) {
+  constexpr int kRows = 32 * (NF + MF);              // LDS rows per slot: weights, then tokens
+  constexpr int kScaleOps = (kRows + 63) / 64;       // 64 rows per scale load
+  constexpr int kScaleBytes = kScaleOps * 256 * (kTail ? 2 : 1);
+  constexpr int kSlot = kRows * kStageK + kScaleBytes;
+  constexpr int kOps = kRows / 8 + kScaleOps * (kTail ? 2 : 1);
+  constexpr int kRing = WV * S * kSlot;
+  constexpr int kPitch = 36;                         // floats per token row of a partial tile
+  static_assert(S >= 2 && S <= 3 && (S - 1) * kOps < 64, "vmcnt range");
+  static_assert(WV * NF * MF * 32 * kPitch * 4 <= kRing, "the partial tiles reuse the ring");
+  __shared__ __attribute__((aligned(16))) uint8_t ring[kRing];
+
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int64_t n_tiles = (p.N + 32 * NF - 1) / (32 * NF);
+  const int64_t tt = blockIdx.x / n_tiles;
+  const int64_t n0 = (blockIdx.x - tt * n_tiles) * (32 * NF), t0 = tt * (32 * MF);
+  const int n_last = (int)std::min<int64_t>(p.N - 1 - n0, 32 * NF - 1);   // last row that exists
+  const int t_last = (int)std::min<int64_t>(p.T - 1 - t0, 32 * MF - 1);
+
+  // ---- loads of one stage ------------------------------------------------------------
+  // instruction j fills LDS rows [8 j, 8 j + 8): lane l row 8 j + l / 8, chunk
+  // position l % 8, which holds chunk (l % 8) ^ ((row / 2) % 8)
+  const int drow = lane >> 3;
+  const uint8_t* wbase = p.w + n0 * p.K;
+  const uint8_t* xbase = p.x + t0 * p.K;
+  const uint32_t ring0 = lds_offset(ring) + (uint32_t)(wave * S * kSlot);
+  const uint8_t* sptr[kScaleOps];
+#pragma unroll
+  for (int j = 0; j < kScaleOps; ++j) {
+    const int r = 64 * j + lane;
+    sptr[j] = r < 32 * NF ? p.ws + (n0 + std::min(r, n_last)) * p.s_stride
+                          : p.xs + (t0 + std::min(r - 32 * NF, t_last)) * p.s_stride;
+  }
+  auto issue = [&](int ks, int slot) __attribute__((always_inline)) {
+    const uint32_t dst = ring0 + (uint32_t)(slot * kSlot);
+    const int present = kTail && ks == p.nk - 1 ? 2 * p.tail_blocks : 8;   // 16-byte chunks
+#pragma unroll
+    for (int j = 0; j < kRows / 8; ++j) {
+      const int r = 8 * j + drow;
+      int c = (lane & 7) ^ ((r >> 1) & 7);
+      if (kTail && c >= present) c &= 1;
+      const bool is_w = 8 * j < 32 * NF;
+      const int row = is_w ? std::min(r, n_last) : std::min(r - 32 * NF, t_last);
+      const uint32_t voff = (uint32_t)row * (uint32_t)p.K + (uint32_t)(ks * kStageK + c * 16);
+      load_lds16(voff, is_w ? wbase : xbase, dst + (uint32_t)(j * 1024));
+    }
+#pragma unroll
+    for (int j = 0; j < kScaleOps; ++j) {
+      if constexpr (kTail) {
+        // two pairs of scale bytes; a pair that does not exist repeats the first
+        const uint8_t* s = sptr[j] + 4 * ks;
+        load_lds2(s, dst + (uint32_t)(kRows * kStageK + j * 512));
+        load_lds2(present > 4 ? s + 2 : s, dst + (uint32_t)(kRows * kStageK + j * 512 + 256));
+      } else {
+        load_lds4(sptr[j] + 4 * ks, dst + (uint32_t)(kRows * kStageK + j * 256));
+      }
+    }
+  };
+
+  v16f acc[NF][MF];
+#pragma unroll
+  for (int f = 0; f < NF; ++f)
+#pragma unroll
+    for (int m = 0; m < MF; ++m)
+#pragma unroll
+      for (int v = 0; v < 16; ++v) acc[f][m][v] = 0.0f;
+
+  const int li = lane & 31, lg = lane >> 5;
+  const int cnt = wave < p.nk ? (p.nk - wave + WV - 1) / WV : 0;   // this wave's stages
+#pragma unroll
+  for (int i = 0; i < S; ++i)
+    if (i < cnt) issue(wave + i * WV, i);
+  int slot = 0;
+  for (int i = 0; i < cnt; ++i) {
+    const int ks = wave + i * WV;
+    // stage i has landed once only the later stages' loads are outstanding
+    const int later = std::min(cnt, i + S) - (i + 1);
+    if (later == 0) wait_loads<0>();
+    else if (S == 2 || later == 1) wait_loads<kOps>();
+    else wait_loads<(S - 1) * kOps>();
+    const uint8_t* sl = ring + wave * S * kSlot + slot * kSlot;
+    const uint8_t* sc = sl + kRows * kStageK;
+    v8i fa[2][NF], fb[2][MF];
+    int sa[2][NF], sb[2][MF];
+    auto frag = [&](int r, int s) __attribute__((always_inline)) -> v8i {
+      const uint4 u0 = *reinterpret_cast<const uint4*>(sl + swz(r, 4 * s + lg));
+      const uint4 u1 = *reinterpret_cast<const uint4*>(sl + swz(r, 4 * s + 2 + lg));
+      return v8i{(int)u0.x, (int)u0.y, (int)u0.z, (int)u0.w, (int)u1.x, (int)u1.y, (int)u1.z, (int)u1.w};
+    };
+    auto scale = [&](int r, int s) __attribute__((always_inline)) -> int {
+      if constexpr (kTail)   // pair s of row r: word r % 64 of its half of the row group's 512 bytes
+        return sc[(r >> 6) * 512 + s * 256 + (r & 63) * 4 + lg];
+      else
+        return sc[r * 4 + 2 * s + lg];
+    };
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+#pragma unroll
+      for (int f = 0; f < NF; ++f) {
+        fa[s][f] = frag(32 * f + li, s);
+        sa[s][f] = scale(32 * f + li, s);
+      }
+#pragma unroll
+      for (int m = 0; m < MF; ++m) {
+        fb[s][m] = frag(32 * (NF + m) + li, s);
+        sb[s][m] = scale(32 * (NF + m) + li, s);
+      }
+    }
+    wait_lds();   // the slot is read: refill it
+    if (i + S < cnt) issue(ks + S * WV, slot);
+    if (kTail && ks == p.nk - 1) {
+#pragma unroll
+      for (int s = 0; s < 2; ++s)
+#pragma unroll
+        for (int m = 0; m < MF; ++m)
+#pragma unroll
+          for (int v = 0; v < 8; ++v)
+            if (2 * s + (v >> 2) >= p.tail_blocks) fb[s][m][v] = 0;
+    }
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+#pragma unroll
+      for (int m = 0; m < MF; ++m)
+#pragma unroll
+        for (int f = 0; f < NF; ++f)
+          acc[f][m] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fa[s][f], fb[s][m], acc[f][m], 0, 0, 0,
+                                                                      sa[s][f], 0, sb[s][m]);
+    slot = slot + 1 == S ? 0 : slot + 1;
+  }
+
+  // ---- the waves' partial tiles meet in LDS ----------------------------------------
+  __syncthreads();   // every wave has read its last stage, and no load is outstanding
+  float* part = reinterpret_cast<float*>(ring);
+  constexpr int kTile = 32 * kPitch;   // one 32 x 32 fragment, token-major
+#pragma unroll
+  for (int f = 0; f < NF; ++f)
+#pragma unroll
+    for (int m = 0; m < MF; ++m)
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        *reinterpret_cast<float4*>(part + (wave * NF * MF + f * MF + m) * kTile + li * kPitch + 8 * q + 4 * lg) =
+            make_float4(acc[f][m][4 * q], acc[f][m][4 * q + 1], acc[f][m][4 * q + 2], acc[f][m][4 * q + 3]);
+  __syncthreads();
+
+  // 16 lanes per (fragment, token): two features each
+  const int j = lane & 15;
+  for (int u = tid >> 4; u < NF * MF * 32; u += WV * 4) {
+    const int f = u / (MF * 32), m = (u / 32) % MF, tl = u & 31;
+    const int64_t t = t0 + 32 * m + tl;
+    if (t >= p.T) continue;   // the 16 lanes agree
+    float z[2] = {0.0f, 0.0f};
+#pragma unroll
+    for (int w = 0; w < WV; ++w) {
+      const float2 v = *reinterpret_cast<const float2*>(part + (w * NF * MF + f * MF + m) * kTile + tl * kPitch + 2 * j);
+      z[0] += v.x;
+      z[1] += v.y;
+    }
+    const int64_t n = n0 + 32 * f + 2 * j;
+    const bool in0 = n < p.N, in1 = n + 1 < p.N;
+    if (p.bias) {
+      if (in0) z[0] += bias_at(p, n);
+      if (in1) z[1] += bias_at(p, n + 1);
+    }
+    activate(z, p.act);
+    if (p.res) {
+      if (in0) z[0] += bf16_to_f32(p.res[t * p.N + n]);
+      if (in1) z[1] += bf16_to_f32(p.res[t * p.N + n + 1]);
+    }
+    if (p.y) {
+      const uint32_t o = bf16x2(z[0], z[1]);
+      uint16_t* y = p.y + t * p.N + n;
+      if (in0) y[0] = static_cast<uint16_t>(o);
+      if (in1) y[1] = static_cast<uint16_t>(o >> 16);
+    } else {
+      if (!in0) z[0] = 0.0f;
+      if (!in1) z[1] = 0.0f;
+      float a = fmaxf(fabsf(z[0]), fabsf(z[1]));
+      a = quad_max(a);
+      a = fmaxf(a, dpp_f32<0x141>(a, a));   // row_half_mirror: the other quad of 8 lanes
+      a = fmaxf(a, dpp_f32<0x140>(a, a));   // row_mirror: the other half of 16
+      const uint32_t sb = e8m0_from_amax(a);
+      const float inv = e8m0_inverse(sb);
+      const uint32_t o = e4m3x4(z[0] * inv, z[1] * inv, 0.0f, 0.0f);
+      uint8_t* q = p.yq + t * p.N + n;
+      if (in0) q[0] = static_cast<uint8_t>(o);
+      if (in1) q[1] = static_cast<uint8_t>(o >> 8);
+      if (j == 0 && in0) {
+        const int64_t b = n >> 5;
+        uint8_t* s = p.ys + t * p.ys_stride;
+        s[b] = static_cast<uint8_t>(sb);
+        if (b == (p.N - 1) >> 5 && b + 1 < p.ys_stride) s[b + 1] = 0;
+      }
+    }
+  }
+}
+
+template <int NF, int MF, int WV, int S>
+int launch_stream(const LinParams& p, hipStream_t stream) {
+  const int64_t grid = ((p.N + 32 * NF - 1) / (32 * NF)) * ((p.T + 32 * MF - 1) / (32 * MF));
+  if (grid * 64 * WV >= (int64_t)1 << 32) return fail(MX_ERR_UNSUPPORTED, "mx_linear_fused: too many tiles");
+  if (p.K % kStageK)
+    lin_stream_kernel<NF, MF, WV, S, true><<<dim3((unsigned)grid), dim3(64 * WV), 0, stream>>>(p);
+  else
+    lin_stream_kernel<NF, MF, WV, S, false><<<dim3((unsigned)grid), dim3(64 * WV), 0, stream>>>(p);
+  return check_launch("mx_linear_fused");
+}
+
+int launch_linear(const LinParams& p, hipStream_t stream) {
+  if (p.T <= 32) return launch_stream<1, 1, 8, 2>(p, stream);
+  return launch_stream<2, 2, 4, 2>(p, stream);
+}
+
+// Workspace: the MXFP8 form of bf16 tokens.
+struct FusedLayout {
+  size_t xq, xs, total;
+};
+FusedLayout fused_layout(int64_t T, int64_t K, int x_is_mx) {
+  FusedLayout L{0, 0, 0};
+  if (x_is_mx) return L;
+  L.xs = align_up((size_t)(T * K), 256);
+  L.total = L.xs + align_up((size_t)(T * 2 * ((K + 63) / 64)), 256);
+  return L;
+}
+
+int check_sizes(int64_t T, int64_t K, int64_t N) {
+  if (T < 0 || K <= 0 || N <= 0)
+    return fail(MX_ERR_INVALID_ARG, "mx_linear_fused: bad sizes T=%lld K=%lld N=%lld", (long long)T, (long long)K,
+                (long long)N);
+  if (!dims_in_range({T, N})) return fail(MX_ERR_UNSUPPORTED, "mx_linear_fused: T or N above 2^31 - 1");
+  if (K % 32 != 0) return fail(MX_ERR_UNSUPPORTED, "mx_linear_fused: K=%lld is not a multiple of 32", (long long)K);
+  if (K > kMaxK) return fail(MX_ERR_UNSUPPORTED, "mx_linear_fused: K=%lld > 2^20", (long long)K);
+  return MX_OK;
+}
+
+}  // namespace
+
+}  // namespace mxmoe
+
+extern "C" size_t mx_linear_fused_workspace_size(int64_t T, int64_t K, int64_t N, int x_is_mx) {
+  // 0 for sizes mx_linear_fused rejects
+  if (mxmoe::check_sizes(T, K, N) != MX_OK) return 0;
+  return mxmoe::fused_layout(T, K, x_is_mx).total;
+}
+
+extern "C" int mx_linear_fused(const void* x, const void* x_s, const void* w_u8, const void* w_s, const void* bias,
+                               int bias_type, int activation, const void* residual_bf16, int64_t T, int64_t K,
+                               int64_t N, void* y_bf16, void* yq_u8, void* ys_u8, void* workspace, size_t ws_bytes,
+                               void* stream) {
+  using namespace mxmoe;
+  int rc = check_sizes(T, K, N);
+  if (rc) return rc;
+  if (bias && bias_type != MX_TYPE_BF16 && bias_type != MX_TYPE_F32)
+    return fail(MX_ERR_INVALID_ARG, "mx_linear_fused: bias_type must be MX_TYPE_BF16 or MX_TYPE_F32, got %d",
+                bias_type);
+  if (activation < MX_ACT_NONE || activation > MX_ACT_GELU_TANH)
+    return fail(MX_ERR_INVALID_ARG, "mx_linear_fused: unknown activation %d", activation);
+  if (!yq_u8 != !ys_u8) return fail(MX_ERR_INVALID_ARG, "mx_linear_fused: yq and ys go together");
+  if (y_bf16 && yq_u8) return fail(MX_ERR_INVALID_ARG, "mx_linear_fused: y or (yq, ys), not both");
+  const FusedLayout L = fused_layout(T, K, x_s != nullptr);
+  if (T > 0 && (!x || !w_u8 || !w_s || (!y_bf16 && !yq_u8) || (L.total > 0 && !workspace)))
+    return fail(MX_ERR_INVALID_ARG, "mx_linear_fused: null pointer");
+  if (ws_bytes < L.total)
+    return fail(MX_ERR_WORKSPACE, "mx_linear_fused: workspace %zu bytes < %zu", ws_bytes, L.total);
+  const bool mx_in = x_s != nullptr;
+  if (reinterpret_cast<uintptr_t>(x) % (mx_in ? 16 : 2) || reinterpret_cast<uintptr_t>(w_u8) % 16 ||
+      reinterpret_cast<uintptr_t>(x_s) % 4 || reinterpret_cast<uintptr_t>(w_s) % 4 ||
+      reinterpret_cast<uintptr_t>(bias) % (bias_type == MX_TYPE_F32 ? 4 : 2) ||
+      reinterpret_cast<uintptr_t>(residual_bf16) % 2 || reinterpret_cast<uintptr_t>(y_bf16) % 2 ||
+      (L.total > 0 && reinterpret_cast<uintptr_t>(workspace) % 256))
+    return fail(MX_ERR_UNSUPPORTED, "mx_linear_fused: misaligned pointer");
+  if (T == 0) return MX_OK;
+  LinParams p{};
+  p.T = T;
+  p.K = K;
+  p.N = N;
+  p.s_stride = 2 * ((K + 63) / 64);
+  p.ys_stride = 2 * ((N + 63) / 64);
+  p.nk = (int)((K + kStageK - 1) / kStageK);
+  p.tail_blocks = (int)((K - (int64_t)(p.nk - 1) * kStageK) / 32);
+  p.w = static_cast<const uint8_t*>(w_u8);
+  p.ws = static_cast<const uint8_t*>(w_s);
+  p.bias = bias;
+  p.bias_f32 = bias_type == MX_TYPE_F32;
+  p.act = activation;
+  p.res = static_cast<const uint16_t*>(residual_bf16);
+  p.y = static_cast<uint16_t*>(y_bf16);
+  p.yq = static_cast<uint8_t*>(yq_u8);
+  p.ys = static_cast<uint8_t*>(ys_u8);
+  // Outputs overlap nothing, except that y may take the residual's place.
+  const uint64_t s_bytes = (uint64_t)p.s_stride, dense = (uint64_t)T * (uint64_t)N;
+  const Span in[7] = {{x, (uint64_t)T * (uint64_t)K * (mx_in ? 1 : 2)},
+                      {x_s, (uint64_t)T * s_bytes},
+                      {w_u8, (uint64_t)N * (uint64_t)K},
+                      {w_s, (uint64_t)N * s_bytes},
+                      {bias, (uint64_t)N * (p.bias_f32 ? 4 : 2)},
+                      {workspace, L.total},
+                      {residual_bf16, dense * 2}};
+  const Span out[3] = {{y_bf16, dense * 2}, {yq_u8, dense}, {ys_u8, (uint64_t)T * (uint64_t)p.ys_stride}};
+  for (int o = 0; o < 3; ++o)
+    for (int i = 0; i < 7; ++i)
+      if (overlaps(out[o], in[i]) && !(o == 0 && i == 6 && y_bf16 == residual_bf16))
+        return fail(MX_ERR_INVALID_ARG, "mx_linear_fused: an output overlaps an input or the workspace");
+  if (overlaps(out[1], out[2])) return fail(MX_ERR_INVALID_ARG, "mx_linear_fused: two outputs overlap");
+  hipStream_t s = as_stream(stream);
+  if (mx_in) {
+    p.x = static_cast<const uint8_t*>(x);
+    p.xs = static_cast<const uint8_t*>(x_s);
+  } else {
+    uint8_t* xq = static_cast<uint8_t*>(workspace);
+    uint8_t* xs = xq + L.xs;
+    rc = launch_mx_quantize(static_cast<const uint16_t*>(x), T, K, K, xq, xs, s);
+    if (rc) return rc;
+    p.x = xq;
+    p.xs = xs;
+  }
+  return launch_linear(p, s);
+}
