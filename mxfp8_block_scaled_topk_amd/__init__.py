@@ -572,33 +572,43 @@ def moe_mxfp8_forward_packed(x, topk_ids, topk_w, w13_packed, w13_s, w2_packed, 
                              _packed=True)
 
 
-# The operators below keep their per-call work on the host small (they are
-# called once per layer and decode step), and run on the device of their first
-# tensor whichever device is current.
+# The operators below are called once per layer and decode step, so their
+# per-call work on the host is kept small: one pass over the arguments whose
+# slow, explaining branch runs only for a wrong one (together about 6 us a call
+# less than the checks above).  They run on the device of their first tensor
+# whichever device is current.
 
 TYPE_BF16 = 0
 TYPE_F32 = 1
 
+# the current stream's handle on a device, without a Stream object around it
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
 
-def _on_device(fn):
-    """Run ``fn`` (its first argument a tensor) with that tensor's device
-    current, on the ``stream`` argument (keyword) or the device's current
-    stream.  With a stream given, what the call allocates comes from that
+
+def _need_like(t, shape, name, dtype, device):
+    """_need_shape, quick for a right tensor."""
+    try:
+        if t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.device == device:
+            return
+    except AttributeError:
+        pass
+    _need_shape(t, shape, name, dtype, device)
+
+
+def _elsewhere(device, stream):
+    """The context a call has to run in: None when `device` is current and no
+    stream is given.  With a stream, what the call allocates comes from that
     stream's pool (see _stream_scoped)."""
-    @functools.wraps(fn)
-    def wrapper(x, *args, stream=None, **kw):
-        if not isinstance(x, torch.Tensor) or not x.is_cuda:
-            return fn(x, *args, **kw)      # fails its checks
-        if stream is not None:
-            if stream.device != x.device:
-                raise ValueError(f"stream is on {stream.device}, the tensors on {x.device}")
-            with torch.cuda.stream(stream):
-                return fn(x, *args, **kw)
-        if x.device.index != torch.cuda.current_device():
-            with torch.cuda.device(x.device):
-                return fn(x, *args, **kw)
-        return fn(x, *args, **kw)
-    return wrapper
+    if stream is None:
+        return None if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+    if stream.device != device:
+        raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
+    return torch.cuda.stream(stream)
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
 
 
 def _rows(t, name):
@@ -613,8 +623,7 @@ def _rows(t, name):
     return t2, ld
 
 
-@_on_device
-def mx_add_rmsnorm(x, weight, residual=None, eps=1e-6, quantize=True, norm_out=False, out=None):
+def mx_add_rmsnorm(x, weight, residual=None, eps=1e-6, quantize=True, norm_out=False, out=None, stream=None):
     """Residual addition, RMSNorm and MX quantisation of the last dim, one pass:
     h = x + residual, n = h / sqrt(mean(h^2) + eps) * weight in fp32.
 
@@ -623,52 +632,52 @@ def mx_add_rmsnorm(x, weight, residual=None, eps=1e-6, quantize=True, norm_out=F
     [..., ceil(K/64), 2]; None without ``quantize``), bf16(h) (None without a
     residual) and bf16(n) (None without ``norm_out``).  ``out`` gives the four
     buffers instead, None for an output that is not wanted; its residual_out
-    or y may be x or residual itself.  ``stream`` as everywhere."""
+    or y may be x or residual itself."""
     _need(x, torch.bfloat16, "x")
-    if x.dim() == 0:
-        raise ValueError("x must have at least one dim")
     shape, dev = x.shape, x.device
+    if not shape or shape[-1] == 0:
+        raise ValueError("x must have at least one element per row")
     K = shape[-1]
+    x2, ldx = _rows(x, "x")
+    r2, ldr = None, 0
     if residual is not None:
         _need(residual, torch.bfloat16, "residual")
         if residual.shape != shape:
             raise ValueError(f"residual must have shape {tuple(shape)}, got {tuple(residual.shape)}")
         if residual.device != dev:
             raise ValueError(f"residual must be on {dev}, got {residual.device}")
-    wtype = weight.dtype if isinstance(weight, torch.Tensor) else None
-    _need_shape(weight, (K,), "weight", torch.float32 if wtype is torch.float32 else torch.bfloat16, dev)
-    x2, ldx = _rows(x, "x")
-    r2, ldr = _rows(residual, "residual") if residual is not None else (None, 0)
+        r2, ldr = _rows(residual, "residual")
+    wtype = TYPE_F32 if isinstance(weight, torch.Tensor) and weight.dtype is torch.float32 else TYPE_BF16
+    _need_like(weight, (K,), "weight", torch.float32 if wtype else torch.bfloat16, dev)
     s_shape = shape[:-1] + (_pairs(K), 2)
+    if out is not None:
+        q, s, r_out, y = out
+        if q is not None:
+            _need_like(q, shape, "q", torch.uint8, dev)
+        if s is not None:
+            _need_like(s, s_shape, "s", torch.uint8, dev)
+        if r_out is not None:
+            _need_like(r_out, shape, "residual_out", torch.bfloat16, dev)
+        if y is not None:
+            _need_like(y, shape, "y", torch.bfloat16, dev)
+    _need_gpu(x, "x")
+    there = _elsewhere(dev, stream)
+    if there is not None:
+        with there:
+            return mx_add_rmsnorm(x, weight, residual, eps, quantize, norm_out, out)
     if out is None:
         q = torch.empty(shape, dtype=torch.uint8, device=dev) if quantize else None
         s = torch.empty(s_shape, dtype=torch.uint8, device=dev) if quantize else None
         r_out = torch.empty(shape, dtype=torch.bfloat16, device=dev) if residual is not None else None
         y = torch.empty(shape, dtype=torch.bfloat16, device=dev) if norm_out else None
-    else:
-        q, s, r_out, y = out
-        if q is not None:
-            _need_shape(q, shape, "q", torch.uint8, dev)
-        if s is not None:
-            _need_shape(s, s_shape, "s", torch.uint8, dev)
-        if r_out is not None:
-            _need_shape(r_out, shape, "residual_out", torch.bfloat16, dev)
-        if y is not None:
-            _need_shape(y, shape, "y", torch.bfloat16, dev)
-    _need_gpu(x, "x")
-    rc = load().mx_add_rmsnorm(x2.data_ptr(), ldx, _addr(r2), ldr, weight.data_ptr(),
-                               TYPE_F32 if wtype is torch.float32 else TYPE_BF16, eps, x2.shape[0], K,
-                               _addr(r_out), _addr(y), _addr(q), _addr(s), torch.cuda.current_stream().cuda_stream)
-    _check(rc, "mx_add_rmsnorm")
+    rc = load().mx_add_rmsnorm(x2.data_ptr(), ldx, _addr(r2), ldr, weight.data_ptr(), wtype, eps, x2.shape[0], K,
+                               _addr(r_out), _addr(y), _addr(q), _addr(s), _raw_stream(dev.index))
+    if rc:
+        _check(rc, "mx_add_rmsnorm")
     return q, s, r_out, y
 
 
-def _addr(t):
-    return None if t is None else t.data_ptr()
-
-
-@_on_device
-def moe_route_mx(q, s, topk_ids, E, out=None, workspace=None):
+def moe_route_mx(q, s, topk_ids, E, out=None, workspace=None, stream=None):
     """moe_route_quant for rows that are MXFP8 already: q uint8 [T, K] and
     s uint8 [T, K/64, 2] (as mx_add_rmsnorm or mx_quantize make them).
     Returns (xq, xs, sorted_row, expanded_row_idx, group_list)."""
@@ -677,32 +686,39 @@ def moe_route_mx(q, s, topk_ids, E, out=None, workspace=None):
     k = topk_ids.shape[1]
     M = T * k
     dev = q.device
-    _need_shape(q, (T, K), "q", torch.uint8, dev)
-    _need_shape(s, (T, _pairs(K), 2), "s", torch.uint8, dev)
-    _need_shape(topk_ids, (T, k), "topk_ids", torch.int32, dev)
-    if out is None:
-        out = (torch.empty((M, K), dtype=torch.uint8, device=dev),
-               torch.empty((M, _pairs(K), 2), dtype=torch.uint8, device=dev),
-               torch.empty(M, dtype=torch.int32, device=dev),
-               torch.empty(M, dtype=torch.int32, device=dev),
-               torch.empty(E, dtype=torch.int64, device=dev))
-    xq, xs, sr, eri, gl = out
-    _need_shape(xq, (M, K), "xq", torch.uint8, dev)
-    _need_shape(xs, (M, _pairs(K), 2), "xs", torch.uint8, dev)
-    _need_shape(sr, (M,), "sorted_row", torch.int32, dev)
-    _need_shape(eri, (M,), "expanded_row_idx", torch.int32, dev)
-    _need_shape(gl, (E,), "group_list", torch.int64, dev)
+    P = _pairs(K)
+    _need_like(q, (T, K), "q", torch.uint8, dev)
+    _need_like(s, (T, P, 2), "s", torch.uint8, dev)
+    _need_like(topk_ids, (T, k), "topk_ids", torch.int32, dev)
+    if out is not None:
+        xq, xs, sr, eri, gl = out
+        _need_like(xq, (M, K), "xq", torch.uint8, dev)
+        _need_like(xs, (M, P, 2), "xs", torch.uint8, dev)
+        _need_like(sr, (M,), "sorted_row", torch.int32, dev)
+        _need_like(eri, (M,), "expanded_row_idx", torch.int32, dev)
+        _need_like(gl, (E,), "group_list", torch.int64, dev)
     lib = load()
     need = lib.moe_route_quant_workspace_size(T, k, E)
     if workspace is not None:
         _need_workspace(workspace, need, dev)
     _need_gpu(q, "q")
+    there = _elsewhere(dev, stream)
+    if there is not None:
+        with there:
+            return moe_route_mx(q, s, topk_ids, E, out, workspace)
+    if out is None:
+        xq = torch.empty((M, K), dtype=torch.uint8, device=dev)
+        xs = torch.empty((M, P, 2), dtype=torch.uint8, device=dev)
+        sr = torch.empty(M, dtype=torch.int32, device=dev)
+        eri = torch.empty(M, dtype=torch.int32, device=dev)
+        gl = torch.empty(E, dtype=torch.int64, device=dev)
     if workspace is None and need:
         workspace = torch.empty(need, dtype=torch.uint8, device=dev)
     rc = lib.moe_route_mx(q.data_ptr(), s.data_ptr(), topk_ids.data_ptr(), T, K, k, E, xq.data_ptr(), xs.data_ptr(),
                           sr.data_ptr(), eri.data_ptr(), gl.data_ptr(), _addr(workspace),
-                          0 if workspace is None else workspace.numel(), torch.cuda.current_stream().cuda_stream)
-    _check(rc, "moe_route_mx")
+                          0 if workspace is None else workspace.numel(), _raw_stream(dev.index))
+    if rc:
+        _check(rc, "moe_route_mx")
     return xq, xs, sr, eri, gl
 
 
@@ -711,9 +727,8 @@ WEIGHTS_E2M1 = 1     # packed e2m1 (mx_quantize_fp4)
 WEIGHTS_PACKED = 2   # e4m3, tile-packed (mx_pack_weights)
 
 
-@_on_device
 def moe_mxfp8_forward_mx(q, s, topk_ids, topk_w, w13, w13_s, w2, w2_s, weight_format=WEIGHTS_E4M3, out=None,
-                         workspace=None):
+                         workspace=None, stream=None):
     """The whole layer on token rows that are MXFP8 already (q uint8 [T, K],
     s uint8 [T, K/64, 2]); weights as moe_mxfp8_forward, moe_w4a8_forward or
     moe_mxfp8_forward_packed take them, by ``weight_format``.  Returns out
@@ -731,19 +746,23 @@ def moe_mxfp8_forward_mx(q, s, topk_ids, topk_w, w13, w13_s, w2, w2_s, weight_fo
         raise ValueError(f"w13 must be [E, 2I, {Kb}], got {tuple(w13.shape)}")
     I = twoI // 2
     dev = q.device
-    _need_shape(q, (T, K), "q", torch.uint8, dev)
-    _need_shape(s, (T, _pairs(K), 2), "s", torch.uint8, dev)
-    _need_shape(topk_ids, (T, k), "topk_ids", torch.int32, dev)
-    _need_shape(topk_w, (T, k), "topk_w", torch.float32, dev)
-    _need_shape(w13, (E, twoI, Kb), "w13", torch.uint8, dev)
-    _need_shape(w13_s, (E, twoI, _pairs(K), 2), "w13_s", torch.uint8, dev)
-    _need_shape(w2, (E, K, I // 2 if w4 else I), "w2", torch.uint8, dev)
-    _need_shape(w2_s, (E, K, _pairs(I), 2), "w2_s", torch.uint8, dev)
+    _need_like(q, (T, K), "q", torch.uint8, dev)
+    _need_like(s, (T, _pairs(K), 2), "s", torch.uint8, dev)
+    _need_like(topk_ids, (T, k), "topk_ids", torch.int32, dev)
+    _need_like(topk_w, (T, k), "topk_w", torch.float32, dev)
+    _need_like(w13, (E, twoI, Kb), "w13", torch.uint8, dev)
+    _need_like(w13_s, (E, twoI, _pairs(K), 2), "w13_s", torch.uint8, dev)
+    _need_like(w2, (E, K, I // 2 if w4 else I), "w2", torch.uint8, dev)
+    _need_like(w2_s, (E, K, _pairs(I), 2), "w2_s", torch.uint8, dev)
     if out is not None:
-        _need_shape(out, (T, K), "out", torch.bfloat16, dev)
+        _need_like(out, (T, K), "out", torch.bfloat16, dev)
     if workspace is not None:
         _need_workspace(workspace, forward_workspace_size(T, K, I, E, k), dev)
     _need_gpu(q, "q")
+    there = _elsewhere(dev, stream)
+    if there is not None:
+        with there:
+            return moe_mxfp8_forward_mx(q, s, topk_ids, topk_w, w13, w13_s, w2, w2_s, weight_format, out, workspace)
     if out is None:
         out = torch.empty((T, K), dtype=torch.bfloat16, device=dev)
     if workspace is None:
@@ -751,8 +770,9 @@ def moe_mxfp8_forward_mx(q, s, topk_ids, topk_w, w13, w13_s, w2, w2_s, weight_fo
     rc = load().moe_mxfp8_forward_mx(q.data_ptr(), s.data_ptr(), topk_ids.data_ptr(), topk_w.data_ptr(),
                                      weight_format, w13.data_ptr(), w13_s.data_ptr(), w2.data_ptr(), w2_s.data_ptr(),
                                      T, K, I, E, k, out.data_ptr(), workspace.data_ptr(), workspace.numel(),
-                                     torch.cuda.current_stream().cuda_stream)
-    _check(rc, "moe_mxfp8_forward_mx")
+                                     _raw_stream(dev.index))
+    if rc:
+        _check(rc, "moe_mxfp8_forward_mx")
     return out
 
 
@@ -763,9 +783,8 @@ def linear_fused_workspace_size(T, K, N, x_is_mx):
     return int(load().mx_linear_fused_workspace_size(T, K, N, int(x_is_mx)))
 
 
-@_on_device
 def mx_linear_fused(x, w, w_s, x_s=None, bias=None, act="none", residual=None, quantize_out=False, out=None,
-                    workspace=None):
+                    workspace=None, stream=None):
     """Dense MXFP8 linear with its epilogue: act(x . w^T + bias) + residual in
     fp32, rounded once.
 
@@ -774,42 +793,46 @@ def mx_linear_fused(x, w, w_s, x_s=None, bias=None, act="none", residual=None, q
     fp32 [N]; act: a key of ACTIVATIONS; residual: bf16 [T, N].
     Returns y bf16 [T, N], or with ``quantize_out`` its MXFP8 (yq uint8 [T, N],
     ys uint8 [T, ceil(N/64), 2]).  ``out`` gives that tensor or pair instead
-    (y may be the residual).  ``stream`` as everywhere."""
+    (y may be the residual)."""
     mx_in = x_s is not None
     _need(x, torch.uint8 if mx_in else torch.bfloat16, "x", 2); _need(w, torch.uint8, "w", 2)
     T, K = x.shape
     N = w.shape[0]
     dev = x.device
-    _need_shape(x, (T, K), "x", x.dtype, dev)
+    _need_like(x, (T, K), "x", x.dtype, dev)
     if mx_in:
-        _need_shape(x_s, (T, _pairs(K), 2), "x_s", torch.uint8, dev)
-    _need_shape(w, (N, K), "w", torch.uint8, dev)
-    _need_shape(w_s, (N, _pairs(K), 2), "w_s", torch.uint8, dev)
+        _need_like(x_s, (T, _pairs(K), 2), "x_s", torch.uint8, dev)
+    _need_like(w, (N, K), "w", torch.uint8, dev)
+    _need_like(w_s, (N, _pairs(K), 2), "w_s", torch.uint8, dev)
     btype = TYPE_BF16
     if bias is not None:
         if isinstance(bias, torch.Tensor) and bias.dtype is torch.float32:
             btype = TYPE_F32
-        _need_shape(bias, (N,), "bias", torch.float32 if btype else torch.bfloat16, dev)
+        _need_like(bias, (N,), "bias", torch.float32 if btype else torch.bfloat16, dev)
     if act not in ACTIVATIONS:
         raise ValueError(f"act must be one of {', '.join(ACTIVATIONS)}, got {act!r}")
     if residual is not None:
-        _need_shape(residual, (T, N), "residual", torch.bfloat16, dev)
+        _need_like(residual, (T, N), "residual", torch.bfloat16, dev)
     if out is not None:
         quantize_out = isinstance(out, (tuple, list))
     y = yq = ys = None
     if quantize_out:
         yq, ys = out if out is not None else (None, None)
         if out is not None:
-            _need_shape(yq, (T, N), "yq", torch.uint8, dev)
-            _need_shape(ys, (T, _pairs(N), 2), "ys", torch.uint8, dev)
+            _need_like(yq, (T, N), "yq", torch.uint8, dev)
+            _need_like(ys, (T, _pairs(N), 2), "ys", torch.uint8, dev)
     elif out is not None:
         y = out
-        _need_shape(y, (T, N), "out", torch.bfloat16, dev)
+        _need_like(y, (T, N), "out", torch.bfloat16, dev)
     lib = load()
     need = lib.mx_linear_fused_workspace_size(T, K, N, mx_in)
     if workspace is not None:
         _need_workspace(workspace, need, dev)
     _need_gpu(x, "x")
+    there = _elsewhere(dev, stream)
+    if there is not None:
+        with there:
+            return mx_linear_fused(x, w, w_s, x_s, bias, act, residual, quantize_out, out, workspace)
     if workspace is None and need:
         workspace = torch.empty(need, dtype=torch.uint8, device=dev)
     if out is None:
@@ -821,6 +844,7 @@ def mx_linear_fused(x, w, w_s, x_s=None, bias=None, act="none", residual=None, q
     rc = lib.mx_linear_fused(x.data_ptr(), _addr(x_s), w.data_ptr(), w_s.data_ptr(), _addr(bias), btype,
                              ACTIVATIONS[act], _addr(residual), T, K, N, _addr(y), _addr(yq), _addr(ys),
                              _addr(workspace), 0 if workspace is None else workspace.numel(),
-                             torch.cuda.current_stream().cuda_stream)
-    _check(rc, "mx_linear_fused")
+                             _raw_stream(dev.index))
+    if rc:
+        _check(rc, "mx_linear_fused")
     return (yq, ys) if quantize_out else y

@@ -22,6 +22,8 @@ struct LinParams {
   int tail_blocks;     // this many 32-element blocks (1 .. 4)
   int bias_f32;
   int act;             // mx_activation
+  int vec_out;         // rows of y and of the residual are whole 16-byte pieces
+  int vec_q;           // rows of yq are whole 8-byte pieces
 };
 
 typedef int v8i __attribute__((ext_vector_type(8)));
@@ -107,8 +109,83 @@ __device__ __forceinline__ void activate(float (&z)[n], int act) {
   }
 }
 
-__device__ __forceinline__ float bias_at(const LinParams& p, int64_t n) {
-  return p.bias_f32 ? static_cast<const float*>(p.bias)[n] : bf16_to_f32(static_cast<const uint16_t*>(p.bias)[n]);
+// ---- the epilogue of 8 consecutive features n .. of token t -------------------------
+// n is a multiple of 8; cnt (at most 8) of the features exist, none when cnt <=
+// 0.  The four lanes of a quad hold one 32-feature block of one token.
+
+// their bias (0 where there is none)
+__device__ __forceinline__ void epilogue_bias(const LinParams& p, int64_t n, int cnt, float (&b)[8]) {
+  if (!p.bias || cnt <= 0) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) b[i] = 0.0f;
+  } else if (p.bias_f32) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) b[i] = static_cast<const float*>(p.bias)[n + (i < cnt ? i : 0)];
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) b[i] = bf16_to_f32(static_cast<const uint16_t*>(p.bias)[n + (i < cnt ? i : 0)]);
+  }
+}
+
+// res: the residual's 16 bytes when p.vec_out (zeros without a residual)
+__device__ __forceinline__ void epilogue8(const LinParams& p, int64_t t, int64_t n, int cnt, const float (&b)[8],
+                                          const uint4& res, float (&z)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) z[i] += b[i];
+  activate(z, p.act);
+  if (p.vec_out) {
+    float r[8];
+    unpack_bf16x8(res, r);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) z[i] += r[i];
+  } else if (p.res && cnt > 0) {
+    const uint16_t* row = p.res + t * p.N + n;
+    uint16_t r[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) r[i] = row[i < cnt ? i : 0];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) z[i] += bf16_to_f32(r[i]);
+  }
+  if (p.y) {
+    if (cnt <= 0) return;
+    const uint4 o = make_uint4(bf16x2(z[0], z[1]), bf16x2(z[2], z[3]), bf16x2(z[4], z[5]), bf16x2(z[6], z[7]));
+    uint16_t* y = p.y + t * p.N + n;
+    if (p.vec_out) {
+      *reinterpret_cast<uint4*>(y) = o;
+    } else {
+      const uint32_t w[4] = {o.x, o.y, o.z, o.w};
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (i < cnt) y[i] = static_cast<uint16_t>(w[i >> 1] >> (16 * (i & 1)));
+    }
+  } else {
+    float a = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (i >= cnt) z[i] = 0.0f;
+      a = fmaxf(a, fabsf(z[i]));
+    }
+    a = quad_max(a);
+    if (cnt <= 0) return;
+    const uint32_t sb = e8m0_from_amax(a);
+    const float inv = e8m0_inverse(sb);
+    const uint2 o = make_uint2(e4m3x4(z[0] * inv, z[1] * inv, z[2] * inv, z[3] * inv),
+                               e4m3x4(z[4] * inv, z[5] * inv, z[6] * inv, z[7] * inv));
+    uint8_t* q = p.yq + t * p.N + n;
+    if (p.vec_q) {
+      *reinterpret_cast<uint2*>(q) = o;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (i < cnt) q[i] = static_cast<uint8_t>((i < 4 ? o.x : o.y) >> (8 * (i & 3)));
+    }
+    if ((n & 31) == 0) {
+      const int64_t blk = n >> 5;
+      uint8_t* s = p.ys + t * p.ys_stride;
+      s[blk] = static_cast<uint8_t>(sb);
+      if (blk == (p.N - 1) >> 5 && blk + 1 < p.ys_stride) s[blk + 1] = 0;
+    }
+  }
 }
 
 }  // namespace mxmoe

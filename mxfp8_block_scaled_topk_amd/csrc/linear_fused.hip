@@ -26,6 +26,9 @@ namespace mxmoe {
 int launch_mx_quantize(const uint16_t* x, int64_t rows, int64_t kd, int64_t ld, uint8_t* q, uint8_t* s,
                        hipStream_t stream);
 
+int launch_lin_tile256(const LinParams& p, hipStream_t stream);
+int launch_lin_tile128(const LinParams& p, hipStream_t stream);
+
 namespace {
 
 constexpr int64_t kMaxK = (int64_t)1 << 20;   // 32-bit offsets within a tile's rows
@@ -184,55 +187,25 @@ __global__ __launch_bounds__(64 * WV) void lin_stream_kernel(LinParams p) {
             make_float4(acc[f][m][4 * q], acc[f][m][4 * q + 1], acc[f][m][4 * q + 2], acc[f][m][4 * q + 3]);
   __syncthreads();
 
-  // 16 lanes per (fragment, token): two features each
-  const int j = lane & 15;
-  for (int u = tid >> 4; u < NF * MF * 32; u += WV * 4) {
+  // four lanes per (fragment, token), 8 features each
+  for (int u0 = wave * 16; u0 < NF * MF * 32; u0 += WV * 16) {   // NF MF 32 is a multiple of 16: whole quads
+    const int u = u0 + (lane >> 2);
     const int f = u / (MF * 32), m = (u / 32) % MF, tl = u & 31;
     const int64_t t = t0 + 32 * m + tl;
-    if (t >= p.T) continue;   // the 16 lanes agree
-    float z[2] = {0.0f, 0.0f};
+    const int64_t n = n0 + 32 * f + 8 * (lane & 3);
+    const int cnt = t < p.T ? (int)std::min<int64_t>(p.N - n, 8) : 0;
+    float z[8] = {}, b[8];
+    uint4 res = make_uint4(0, 0, 0, 0);
+    epilogue_bias(p, n, cnt, b);
+    if (p.vec_out && p.res && cnt > 0) res = *reinterpret_cast<const uint4*>(p.res + t * p.N + n);
 #pragma unroll
     for (int w = 0; w < WV; ++w) {
-      const float2 v = *reinterpret_cast<const float2*>(part + (w * NF * MF + f * MF + m) * kTile + tl * kPitch + 2 * j);
-      z[0] += v.x;
-      z[1] += v.y;
+      const float* src = part + (w * NF * MF + f * MF + m) * kTile + tl * kPitch + 8 * (lane & 3);
+      const float4 v0 = reinterpret_cast<const float4*>(src)[0], v1 = reinterpret_cast<const float4*>(src)[1];
+      z[0] += v0.x; z[1] += v0.y; z[2] += v0.z; z[3] += v0.w;
+      z[4] += v1.x; z[5] += v1.y; z[6] += v1.z; z[7] += v1.w;
     }
-    const int64_t n = n0 + 32 * f + 2 * j;
-    const bool in0 = n < p.N, in1 = n + 1 < p.N;
-    if (p.bias) {
-      if (in0) z[0] += bias_at(p, n);
-      if (in1) z[1] += bias_at(p, n + 1);
-    }
-    activate(z, p.act);
-    if (p.res) {
-      if (in0) z[0] += bf16_to_f32(p.res[t * p.N + n]);
-      if (in1) z[1] += bf16_to_f32(p.res[t * p.N + n + 1]);
-    }
-    if (p.y) {
-      const uint32_t o = bf16x2(z[0], z[1]);
-      uint16_t* y = p.y + t * p.N + n;
-      if (in0) y[0] = static_cast<uint16_t>(o);
-      if (in1) y[1] = static_cast<uint16_t>(o >> 16);
-    } else {
-      if (!in0) z[0] = 0.0f;
-      if (!in1) z[1] = 0.0f;
-      float a = fmaxf(fabsf(z[0]), fabsf(z[1]));
-      a = quad_max(a);
-      a = fmaxf(a, dpp_f32<0x141>(a, a));   // row_half_mirror: the other quad of 8 lanes
-      a = fmaxf(a, dpp_f32<0x140>(a, a));   // row_mirror: the other half of 16
-      const uint32_t sb = e8m0_from_amax(a);
-      const float inv = e8m0_inverse(sb);
-      const uint32_t o = e4m3x4(z[0] * inv, z[1] * inv, 0.0f, 0.0f);
-      uint8_t* q = p.yq + t * p.N + n;
-      if (in0) q[0] = static_cast<uint8_t>(o);
-      if (in1) q[1] = static_cast<uint8_t>(o >> 8);
-      if (j == 0 && in0) {
-        const int64_t b = n >> 5;
-        uint8_t* s = p.ys + t * p.ys_stride;
-        s[b] = static_cast<uint8_t>(sb);
-        if (b == (p.N - 1) >> 5 && b + 1 < p.ys_stride) s[b + 1] = 0;
-      }
-    }
+    epilogue8(p, t, n, cnt, b, res, z);
   }
 }
 
@@ -248,8 +221,10 @@ int launch_stream(const LinParams& p, hipStream_t stream) {
 }
 
 int launch_linear(const LinParams& p, hipStream_t stream) {
-  if (p.T <= 32) return launch_stream<1, 1, 8, 2>(p, stream);
-  return launch_stream<2, 2, 4, 2>(p, stream);
+  if (p.T <= 64) return launch_stream<1, 1, 8, 2>(p, stream);
+  if (p.T <= 256) return launch_stream<2, 2, 4, 2>(p, stream);
+  if (p.T <= 2048) return launch_lin_tile128(p, stream);
+  return launch_lin_tile256(p, stream);
 }
 
 // Workspace: the MXFP8 form of bf16 tokens.
@@ -328,6 +303,9 @@ extern "C" int mx_linear_fused(const void* x, const void* x_s, const void* w_u8,
   p.y = static_cast<uint16_t*>(y_bf16);
   p.yq = static_cast<uint8_t*>(yq_u8);
   p.ys = static_cast<uint8_t*>(ys_u8);
+  p.vec_out = N % 8 == 0 &&
+              (reinterpret_cast<uintptr_t>(y_bf16) | reinterpret_cast<uintptr_t>(residual_bf16)) % 16 == 0;
+  p.vec_q = N % 8 == 0 && reinterpret_cast<uintptr_t>(yq_u8) % 8 == 0;
   // Outputs overlap nothing, except that y may take the residual's place.
   const uint64_t s_bytes = (uint64_t)p.s_stride, dense = (uint64_t)T * (uint64_t)N;
   const Span in[7] = {{x, (uint64_t)T * (uint64_t)K * (mx_in ? 1 : 2)},
