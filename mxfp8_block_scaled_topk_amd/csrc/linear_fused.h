@@ -22,8 +22,8 @@ struct LinParams {
   int tail_blocks;     // this many 32-element blocks (1 .. 4)
   int bias_f32;
   int act;             // mx_activation
-  int vec_out;         // rows of y and of the residual are whole 16-byte pieces
-  int vec_q;           // rows of yq are whole 8-byte pieces
+  int stream_res;      // the residual is too large to be left in the memory-side cache
+  int vec;             // rows of y and of the residual are whole 16-byte pieces, of yq 8-byte ones
 };
 
 typedef int v8i __attribute__((ext_vector_type(8)));
@@ -35,18 +35,22 @@ constexpr int kStageK = 128;   // elements (bytes) of a row per k stage
 __device__ __forceinline__ uint32_t lds_offset(const void* p) {
   return (uint32_t)(uintptr_t)(const lds_u8*)p;
 }
-// Direct global->LDS loads: lane l's bytes land at lds + l * 16 (or * 4).
+// Direct global->LDS loads: lane l's bytes land at lds + l * 16 (or * 4).  The
+// compiler keeps the wait states that a memory instruction needs after a vector
+// instruction wrote its scalar operands (5: v_readlane of a spilled base) or a
+// scalar one wrote m0 (1), but it cannot see one in inline assembly: the s_nop
+// stands for them.
 // Uniform base plus a per-lane 32-bit offset:
 __device__ __forceinline__ void load_lds16(uint32_t voff, const void* sbase, uint32_t lds) {
-  asm volatile("global_load_lds_dwordx4 %0, %1" ::"v"(voff), "s"(sbase), "{m0}"(lds) : "memory");
+  asm volatile("s_nop 4\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(voff), "s"(sbase), "{m0}"(lds) : "memory");
 }
 // Per-lane addresses:
 __device__ __forceinline__ void load_lds4(const uint8_t* p, uint32_t lds) {
-  asm volatile("global_load_lds_dword %0, off" ::"v"(p), "{m0}"(lds) : "memory");
+  asm volatile("s_nop 4\n\tglobal_load_lds_dword %0, off" ::"v"(p), "{m0}"(lds) : "memory");
 }
 // two bytes per lane, zero-extended to the lane's LDS word
 __device__ __forceinline__ void load_lds2(const uint8_t* p, uint32_t lds) {
-  asm volatile("global_load_lds_ushort %0, off" ::"v"(p), "{m0}"(lds) : "memory");
+  asm volatile("s_nop 4\n\tglobal_load_lds_ushort %0, off" ::"v"(p), "{m0}"(lds) : "memory");
 }
 template <int N>
 __device__ __forceinline__ void wait_loads() {   // at most N loads outstanding
@@ -109,6 +113,10 @@ __device__ __forceinline__ void activate(float (&z)[n], int act) {
   }
 }
 
+__device__ __forceinline__ float bias_at(const LinParams& p, int64_t n) {
+  return p.bias_f32 ? static_cast<const float*>(p.bias)[n] : bf16_to_f32(static_cast<const uint16_t*>(p.bias)[n]);
+}
+
 // ---- the epilogue of 8 consecutive features n .. of token t -------------------------
 // n is a multiple of 8; cnt (at most 8) of the features exist, none when cnt <=
 // 0.  The four lanes of a quad hold one 32-feature block of one token.
@@ -127,13 +135,14 @@ __device__ __forceinline__ void epilogue_bias(const LinParams& p, int64_t n, int
   }
 }
 
-// res: the residual's 16 bytes when p.vec_out (zeros without a residual)
+// kVec = p.vec; res: then the residual's 16 bytes (zeros without a residual)
+template <bool kVec>
 __device__ __forceinline__ void epilogue8(const LinParams& p, int64_t t, int64_t n, int cnt, const float (&b)[8],
                                           const uint4& res, float (&z)[8]) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) z[i] += b[i];
   activate(z, p.act);
-  if (p.vec_out) {
+  if (kVec) {
     float r[8];
     unpack_bf16x8(res, r);
 #pragma unroll
@@ -150,8 +159,11 @@ __device__ __forceinline__ void epilogue8(const LinParams& p, int64_t t, int64_t
     if (cnt <= 0) return;
     const uint4 o = make_uint4(bf16x2(z[0], z[1]), bf16x2(z[2], z[3]), bf16x2(z[4], z[5]), bf16x2(z[6], z[7]));
     uint16_t* y = p.y + t * p.N + n;
-    if (p.vec_out) {
-      *reinterpret_cast<uint4*>(y) = o;
+    if (kVec) {
+      // written once: past the caches, which hold the operands of the tiles to come
+      typedef unsigned int u4 __attribute__((ext_vector_type(4)));
+      const u4 oo = {o.x, o.y, o.z, o.w};
+      __builtin_nontemporal_store(oo, reinterpret_cast<u4*>(y));
     } else {
       const uint32_t w[4] = {o.x, o.y, o.z, o.w};
 #pragma unroll
@@ -172,7 +184,7 @@ __device__ __forceinline__ void epilogue8(const LinParams& p, int64_t t, int64_t
     const uint2 o = make_uint2(e4m3x4(z[0] * inv, z[1] * inv, z[2] * inv, z[3] * inv),
                                e4m3x4(z[4] * inv, z[5] * inv, z[6] * inv, z[7] * inv));
     uint8_t* q = p.yq + t * p.N + n;
-    if (p.vec_q) {
+    if (kVec) {
       *reinterpret_cast<uint2*>(q) = o;
     } else {
 #pragma unroll

@@ -28,6 +28,7 @@ int launch_mx_quantize(const uint16_t* x, int64_t rows, int64_t kd, int64_t ld, 
 
 int launch_lin_tile256(const LinParams& p, hipStream_t stream);
 int launch_lin_tile128(const LinParams& p, hipStream_t stream);
+int launch_lin_tile256x128(const LinParams& p, hipStream_t stream);
 
 namespace {
 
@@ -197,7 +198,7 @@ __global__ __launch_bounds__(64 * WV) void lin_stream_kernel(LinParams p) {
     float z[8] = {}, b[8];
     uint4 res = make_uint4(0, 0, 0, 0);
     epilogue_bias(p, n, cnt, b);
-    if (p.vec_out && p.res && cnt > 0) res = *reinterpret_cast<const uint4*>(p.res + t * p.N + n);
+    if (p.vec && p.res && cnt > 0) res = *reinterpret_cast<const uint4*>(p.res + t * p.N + n);
 #pragma unroll
     for (int w = 0; w < WV; ++w) {
       const float* src = part + (w * NF * MF + f * MF + m) * kTile + tl * kPitch + 8 * (lane & 3);
@@ -205,7 +206,8 @@ __global__ __launch_bounds__(64 * WV) void lin_stream_kernel(LinParams p) {
       z[0] += v0.x; z[1] += v0.y; z[2] += v0.z; z[3] += v0.w;
       z[4] += v1.x; z[5] += v1.y; z[6] += v1.z; z[7] += v1.w;
     }
-    epilogue8(p, t, n, cnt, b, res, z);
+    if (p.vec) epilogue8<true>(p, t, n, cnt, b, res, z);
+    else epilogue8<false>(p, t, n, cnt, b, res, z);
   }
 }
 
@@ -220,11 +222,29 @@ int launch_stream(const LinParams& p, hipStream_t stream) {
   return check_launch("mx_linear_fused");
 }
 
+// Which kernel: the one whose time, in units of 0.1 us, a line through its
+// measured times says is shortest.  Its tiles go over the CUs in rounds; a round
+// costs a part per tile and a part per k stage of a wave.  Fitted to all kernels
+// on 110 shapes (T to 16384, K and N to 8192, drawn over their logarithms), the
+// rule's choice takes 0.4 % longer than the fastest on average, 15 % at worst.
 int launch_linear(const LinParams& p, hipStream_t stream) {
-  if (p.T <= 64) return launch_stream<1, 1, 8, 2>(p, stream);
-  if (p.T <= 256) return launch_stream<2, 2, 4, 2>(p, stream);
-  if (p.T <= 2048) return launch_lin_tile128(p, stream);
-  return launch_lin_tile256(p, stream);
+  const int64_t cus = num_cus(), nk = p.nk;
+  auto tiles = [&](int64_t bn, int64_t bm) { return ((p.N + bn - 1) / bn) * ((p.T + bm - 1) / bm); };
+  auto rounds = [](int64_t n, int64_t slots) { return (n + slots - 1) / slots; };
+  const int64_t t128 = tiles(128, 128);
+  const int64_t us[5] = {
+      rounds(tiles(32, 32), cus) * (18 + 17 * ((nk + 7) / 8) / 2),          // K over 8 waves
+      rounds(tiles(64, 64), cus) * (30 + 23 * ((nk + 3) / 4) / 2),          // K over 4 waves
+      t128 <= cus ? 60 + 8 * nk : rounds(t128, 2 * cus) * (72 + 54 * nk / 5),   // two workgroups per CU
+      nk < 3 ? INT64_MAX : rounds(tiles(256, 128), cus) * (83 + 17 * nk / 2),
+      rounds(tiles(256, 256), cus) * (198 + 64 * nk / 5)};
+  switch (std::min_element(us, us + 5) - us) {
+    case 0: return launch_stream<1, 1, 8, 2>(p, stream);
+    case 1: return launch_stream<2, 2, 4, 2>(p, stream);
+    case 2: return launch_lin_tile128(p, stream);
+    case 3: return launch_lin_tile256x128(p, stream);
+    default: return launch_lin_tile256(p, stream);
+  }
 }
 
 // Workspace: the MXFP8 form of bf16 tokens.
@@ -303,9 +323,11 @@ extern "C" int mx_linear_fused(const void* x, const void* x_s, const void* w_u8,
   p.y = static_cast<uint16_t*>(y_bf16);
   p.yq = static_cast<uint8_t*>(yq_u8);
   p.ys = static_cast<uint8_t*>(ys_u8);
-  p.vec_out = N % 8 == 0 &&
-              (reinterpret_cast<uintptr_t>(y_bf16) | reinterpret_cast<uintptr_t>(residual_bf16)) % 16 == 0;
-  p.vec_q = N % 8 == 0 && reinterpret_cast<uintptr_t>(yq_u8) % 8 == 0;
+  // measured at N = 4096: non-temporal residual loads 282 -> 267 us at T = 16384
+  // (134 MB), 46 -> 49 us at T = 4096 (34 MB)
+  p.stream_res = T * N > (int64_t)48 << 20;
+  p.vec = N % 8 == 0 && reinterpret_cast<uintptr_t>(yq_u8) % 8 == 0 &&
+          (reinterpret_cast<uintptr_t>(y_bf16) | reinterpret_cast<uintptr_t>(residual_bf16)) % 16 == 0;
   // Outputs overlap nothing, except that y may take the residual's place.
   const uint64_t s_bytes = (uint64_t)p.s_stride, dense = (uint64_t)T * (uint64_t)N;
   const Span in[7] = {{x, (uint64_t)T * (uint64_t)K * (mx_in ? 1 : 2)},

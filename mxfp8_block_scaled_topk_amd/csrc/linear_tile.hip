@@ -27,6 +27,15 @@ typedef __attribute__((address_space(3))) const volatile uint8_t lds_u8_v;
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) f32x4 lds_f32x4;
 
+// at most n (wave-uniform) loads outstanding; 0 where n is not among the cases
+__device__ __forceinline__ void wait_loads_le(int n) {
+  switch (n) {
+#define MX_WAIT(N) case N: wait_loads<N>(); break;
+    MX_WAIT(16) MX_WAIT(15) MX_WAIT(14) MX_WAIT(13) MX_WAIT(12) MX_WAIT(11) MX_WAIT(10) MX_WAIT(9) MX_WAIT(8) MX_WAIT(7) MX_WAIT(6) MX_WAIT(5)
+#undef MX_WAIT
+    default: wait_loads<0>(); break;
+  }
+}
 // Workgroup barrier that first drains this wave's LDS accesses.
 __device__ __forceinline__ void drain_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
 __device__ __forceinline__ int opaque(int v) {   // keeps address arithmetic where it is used
@@ -50,19 +59,21 @@ constexpr int kBand = 8;
 // 16-byte boundaries): 16 scale bytes per row at a group's first stage, into a
 // double-buffered ring of their own.  1: the stage's 4 bytes per row.  kTail
 // (with kG = 1): K is not a multiple of 128; see lin_stream_kernel.
-template <int NA, int NB, int WN, int WM, int kG, bool kTail>
+template <int NA, int NB, int WN, int WM, int S, int kG, bool kTail, bool kVec>
 __global__ __launch_bounds__(64 * WN * WM) void lin_tile_kernel(LinParams p, int m_tiles, int n_tiles) {
   constexpr int kWaves = WN * WM;
   constexpr int BN = 32 * NA * WN, BM = 32 * NB * WM;
   constexpr int kRowsA = BN / kWaves, kRowsB = BM / kWaves;   // rows each wave fetches
   constexpr int kOpsA = kRowsA / 8, kOpsB = kRowsB / 8;
-  static_assert((BN + BM) / 64 == kWaves, "one wave, 64 scale rows");
+  constexpr int kScaleWavesA = BN / 64, kScaleWaves = (BN + BM) / 64;   // 64 scale rows per wave, weights' first
+  static_assert(kScaleWaves <= kWaves && (S == 2 || S == 3), "scale rows and ring slots");
   static_assert(kG == 1 || !kTail, "scale groups need whole stages");
   constexpr int kSlotData = (BN + BM) * kStageK;
   constexpr int kSlot = kSlotData + (kG == 1 ? (BN + BM) * (kTail ? 8 : 4) : 0);
   constexpr int kScBuf = (BN + BM) * 16;   // one group's scales
-  __shared__ __attribute__((aligned(16))) uint8_t ring[2 * kSlot];
+  __shared__ __attribute__((aligned(16))) uint8_t ring[S * kSlot];
   __shared__ __attribute__((aligned(16))) uint8_t s_sc[kG == 4 ? 2 * kScBuf : 16];
+  __shared__ __attribute__((aligned(16))) float s_bias[BN];   // the tile's, 0 where there is none
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -81,7 +92,6 @@ __global__ __launch_bounds__(64 * WN * WM) void lin_tile_kernel(LinParams p, int
   struct Tile {
     int64_t n0, t0;
     int rows_n, rows_t;   // that exist
-    int rot;              // the stage it starts with
   };
   auto tile_at = [&](int j) __attribute__((always_inline)) -> Tile {
     const int t = first_tile + j * G;
@@ -94,7 +104,6 @@ __global__ __launch_bounds__(64 * WN * WM) void lin_tile_kernel(LinParams p, int
     ti.t0 = (int64_t)mt * BM;
     ti.rows_n = uni((int)std::min<int64_t>(BN, p.N - ti.n0));
     ti.rows_t = uni((int)std::min<int64_t>(BM, p.T - ti.t0));
-    ti.rot = kTail ? 0 : nt % nk;
     return ti;
   };
 
@@ -109,9 +118,7 @@ __global__ __launch_bounds__(64 * WN * WM) void lin_tile_kernel(LinParams p, int
     const uint8_t* x;      // token row t0
     const uint8_t* sc;     // the scale rows this wave fetches (64 of them)
     int last_n, last_t, last_s;
-    int rot;
   };
-  constexpr int kScaleWavesA = BN / 64;   // waves that fetch weight scales; the others fetch tokens'
   auto src_of = [&](const Tile& ti) __attribute__((always_inline)) -> Src {
     Src s;
     s.w = uniptr(p.w + ti.n0 * K);
@@ -120,27 +127,28 @@ __global__ __launch_bounds__(64 * WN * WM) void lin_tile_kernel(LinParams p, int
     s.last_t = ti.rows_t - 1;
     s.sc = wave < kScaleWavesA ? uniptr(p.ws + ti.n0 * srow) : uniptr(p.xs + ti.t0 * srow);
     s.last_s = wave < kScaleWavesA ? s.last_n : s.last_t;
-    s.rot = ti.rot;
     return s;
   };
   const int srow_local = 64 * (wave < kScaleWavesA ? wave : wave - kScaleWavesA) + lane;
   const uint32_t row0_a = (uint32_t)((kRowsA * wave + drow) * K), row0_b = (uint32_t)((kRowsB * wave + drow) * K);
-  const int n_groups = nk / kG;
-  auto kmem = [&](int ks, int rot) __attribute__((always_inline)) -> int {
-    if constexpr (kG == 1) {
-      const int kr = ks + rot;
-      return kr >= nk ? kr - nk : kr;
-    } else {
-      int grp = (ks >> 2) + (rot >> 2);
-      grp = grp >= n_groups ? grp - n_groups : grp;
-      return 4 * grp + (((ks & 3) + rot) & 3);
-    }
-  };
   constexpr int kLoadOps = kOpsA + kOpsB + 1;
+  // S = 2: a stage's loads go out over the first MFMAs of one sub-step (5 behind
+  // the first, the rest behind the second: spread wider, the last ones are late).
+  // S = 3: half of them over that sub-step's MFMAs, half over the next one's.
+  constexpr int kFirst = S == 2 ? kLoadOps : (kLoadOps + 1) / 2;
+  constexpr int kPer = S == 2 ? 5 : (kFirst + NA * NB - 1) / (NA * NB);
+  const bool sc_wave = kScaleWaves == kWaves || wave < kScaleWaves;
+  auto slot_of = [](int gs) __attribute__((always_inline)) -> int {
+    if constexpr (S == 2) return gs & 1;
+    else return (int)((unsigned)gs % 3u);
+  };
+  // memory instructions of this wave for tile stage ks (S = 3 leaves the latest stage's in flight)
+  auto ops_of = [&](int ks) __attribute__((always_inline)) -> int {
+    return kOpsA + kOpsB + (sc_wave && (kG == 1 || (ks & 3) == 0) ? (kTail ? 2 : 1) : 0);
+  };
   auto load_part = [&](int i, const Src& s, int ks, int gs) __attribute__((always_inline)) {
-    const uint32_t base = ring0 + (uint32_t)(gs & 1) * (uint32_t)kSlot;
-    const int kr = kmem(ks, s.rot);
-    const int present = kTail && kr == nk - 1 ? 2 * p.tail_blocks : 8;   // 16-byte chunks
+    const uint32_t base = ring0 + (uint32_t)slot_of(gs) * (uint32_t)kSlot;
+    const int present = kTail && ks == nk - 1 ? 2 * p.tail_blocks : 8;   // 16-byte chunks
     if (i < kOpsA + kOpsB) {
       const bool is_w = i < kOpsA;
       const int j = is_w ? i : i - kOpsA;
@@ -149,22 +157,22 @@ __global__ __launch_bounds__(64 * WN * WM) void lin_tile_kernel(LinParams p, int
       // rows past the last repeat it
       const uint32_t row = std::min((is_w ? row0_a : row0_b) + (uint32_t)(8 * j) * (uint32_t)K,
                                     (uint32_t)(is_w ? s.last_n : s.last_t) * (uint32_t)K);
-      const uint32_t voff = row + (uint32_t)(c * 16) + (uint32_t)(kr * kStageK);
+      const uint32_t voff = row + (uint32_t)(c * 16) + (uint32_t)(ks * kStageK);
       load_lds16(voff, is_w ? s.w : s.x,
                  base + (uint32_t)((is_w ? 0 : BN * kStageK) + ((is_w ? kRowsA : kRowsB) * wave + 8 * j) * kStageK));
-    } else {
+    } else if (sc_wave) {
       const uint32_t off = (uint32_t)std::min(srow_local, s.last_s) * (uint32_t)srow;
       const uint32_t rows = (uint32_t)(wave < kScaleWavesA ? 64 * wave : BN + 64 * (wave - kScaleWavesA));
       if constexpr (kG == 4) {
         if ((ks & 3) == 0)
-          load_lds16(off + (uint32_t)((kr & ~3) * 4), s.sc, sc0 + (uint32_t)(((gs >> 2) & 1) * kScBuf) + rows * 16);
+          load_lds16(off + (uint32_t)(ks * 4), s.sc, sc0 + (uint32_t)(((gs >> 2) & 1) * kScBuf) + rows * 16);
       } else if constexpr (kTail) {
         // two pairs of scale bytes, each pair's rows together; an absent pair repeats the first
-        const uint8_t* q = s.sc + off + kr * 4;
+        const uint8_t* q = s.sc + off + ks * 4;
         load_lds2(q, base + (uint32_t)kSlotData + rows * 4);
         load_lds2(present > 4 ? q + 2 : q, base + (uint32_t)kSlotData + (uint32_t)((BN + BM) * 4) + rows * 4);
       } else {
-        load_lds4(s.sc + off + kr * 4, base + (uint32_t)kSlotData + rows * 4);
+        load_lds4(s.sc + off + ks * 4, base + (uint32_t)kSlotData + rows * 4);
       }
     }
   };
@@ -181,45 +189,54 @@ __global__ __launch_bounds__(64 * WN * WM) void lin_tile_kernel(LinParams p, int
   uint32_t chk[4];   // byte offset of chunk 2 c + lg within a row
 #pragma unroll
   for (int c = 0; c < 4; ++c) chk[c] = (uint32_t)(((2 * c + lg) ^ sw) << 4);
-  int cur_rot = 0;   // of the tile whose fragments are read
   auto slot_ptr = [&](int gs) __attribute__((always_inline)) {
-    uint32_t b = ring0 + (uint32_t)(gs & 1) * (uint32_t)kSlot;
+    uint32_t b = ring0 + (uint32_t)slot_of(gs) * (uint32_t)kSlot;
     asm("" : "+s"(b));
     return (const lds_u8*)(uintptr_t)b;
   };
   auto group_ptr = [&](int gs) __attribute__((always_inline)) {
-    uint32_t b = sc0 + (uint32_t)(((gs >> 2) & 1) * kScBuf + (((gs & 3) + cur_rot) & 3) * 4);
+    uint32_t b = sc0 + (uint32_t)(((gs >> 2) & 1) * kScBuf + (gs & 3) * 4);
     asm("" : "+s"(b));
     return (const lds_u8*)(uintptr_t)b;
   };
   auto scale_at = [&](int gs, int s, uint32_t row) __attribute__((always_inline)) -> int {
     if constexpr (kG == 4) return (int)*reinterpret_cast<lds_u8_v*>(group_ptr(gs) + row * 16 + 2 * s + lg);
-    const lds_u8* S = slot_ptr(gs) + kSlotData;
-    if constexpr (kTail) return (int)*reinterpret_cast<lds_u8_v*>(S + s * ((BN + BM) * 4) + row * 4 + lg);
-    return (int)*reinterpret_cast<lds_u8_v*>(S + row * 4 + 2 * s + lg);
+    const lds_u8* sl = slot_ptr(gs) + kSlotData;
+    if constexpr (kTail) return (int)*reinterpret_cast<lds_u8_v*>(sl + s * ((BN + BM) * 4) + row * 4 + lg);
+    return (int)*reinterpret_cast<lds_u8_v*>(sl + row * 4 + 2 * s + lg);
   };
   auto frag_at = [&](int gs, int s, uint32_t rd) __attribute__((always_inline)) -> v8i {
-    const lds_u8* S = slot_ptr(gs) + rd;
-    const u32x4 a0 = *reinterpret_cast<lds_u32x4_v*>(S + chk[2 * s]);
-    const u32x4 a1 = *reinterpret_cast<lds_u32x4_v*>(S + chk[2 * s + 1]);
+    const lds_u8* sl = slot_ptr(gs) + rd;
+    const u32x4 a0 = *reinterpret_cast<lds_u32x4_v*>(sl + chk[2 * s]);
+    const u32x4 a1 = *reinterpret_cast<lds_u32x4_v*>(sl + chk[2 * s + 1]);
     return v8i{(int)a0.x, (int)a0.y, (int)a0.z, (int)a0.w, (int)a1.x, (int)a1.y, (int)a1.z, (int)a1.w};
   };
 
-  // prologue: the first two stages
+  // prologue: the first S stages (S = 3 needs as many per tile, host)
   const Src first = src_of(tile_at(0));
   load_stage(first, 0, 0);
-  if (nk > 1) load_stage(first, 1, 1);
-  else if (my_tiles > 1) load_stage(src_of(tile_at(1)), 0, 1);
-  wait_loads<0>();
+  if constexpr (S == 3) {
+    int later = 0;
+#pragma unroll
+    for (int i = 1; i < S; ++i) {
+      load_stage(first, i, i);
+      later += ops_of(i);
+    }
+    wait_loads_le(later);
+  } else {
+    if (nk > 1) load_stage(first, 1, 1);
+    else if (my_tiles > 1) load_stage(src_of(tile_at(1)), 0, 1);
+    wait_loads<0>();
+  }
   drain_barrier();
 
-  int g = 0;   // stages so far: stage g is in slot g % 2
+  int g = 0;   // stages so far: stage g is in slot g % S
+  int latest = S == 3 ? ops_of(S - 1) : 0;   // S = 3: memory instructions of the latest stage's loads, at a tile's start
   for (int cj = 0; cj < my_tiles; ++cj) {
     const Tile cur = tile_at(cj);
     const Src csrc = src_of(cur);
     const bool has_next = cj + 1 < my_tiles;
     const Src nsrc = has_next ? src_of(tile_at(cj + 1)) : csrc;
-    cur_rot = cur.rot & 3;
     // waves with no row that exists compute nothing, but load their share and meet the barriers
     const bool active = 32 * NA * wn < cur.rows_n && 32 * NB * wm < cur.rows_t;
     v8i fa[NA], fb[NB];
@@ -250,7 +267,10 @@ __global__ __launch_bounds__(64 * WN * WM) void lin_tile_kernel(LinParams p, int
         const int fm = m / NA, fn = m % NA;
         acc[fn][fm] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fa[fn], fb[fm], acc[fn][fm], 0, 0, 0, sa[fn], 0,
                                                                       sb[fm]);
-        asm volatile("" : "+v"(acc[fn][fm]));   // keeps the MFMA here, among the loads it overlaps
+        // keeps the MFMA here, among the loads it overlaps; with 512 registers a
+        // wave (4 waves) the accumulators live in the upper half
+        if constexpr (kWaves > 4) asm volatile("" : "+v"(acc[fn][fm]));
+        else asm volatile("" : "+a"(acc[fn][fm]));
         __builtin_amdgcn_sched_barrier(0);
         if constexpr (decltype(kReload)::value) {
           if (fm == NB - 1) load_a(gs, ns, fn);
@@ -272,33 +292,42 @@ __global__ __launch_bounds__(64 * WN * WM) void lin_tile_kernel(LinParams p, int
 #pragma unroll
       for (int f = 0; f < NB; ++f) load_b(g, 0, f, 0);
     }
+    // the loads that stage ks of this tile starts: stage ks + S of the tile, else
+    // of the next one, else a repeat of the last that is never read
+    auto target = [&](int ks, Src& t) __attribute__((always_inline)) -> int {
+      const bool in_tile = ks + S < nk;
+      t.w = in_tile ? csrc.w : nsrc.w;
+      t.x = in_tile ? csrc.x : nsrc.x;
+      t.sc = in_tile ? csrc.sc : nsrc.sc;
+      t.last_n = in_tile ? csrc.last_n : nsrc.last_n;
+      t.last_t = in_tile ? csrc.last_t : nsrc.last_t;
+      t.last_s = in_tile ? csrc.last_s : nsrc.last_s;
+      return in_tile ? ks + S : (has_next ? (S == 2 ? 0 : ks + S - nk) : nk - 1);
+    };
     auto stage = [&](int ks, auto kLoad) __attribute__((always_inline)) {
       __builtin_amdgcn_sched_barrier(0);
-      substep(g, 1, ks, std::true_type{}, [&](int) {});
-      wait_loads<0>();    // this wave's part of stage g + 1 has landed
-      drain_barrier();    // every wave's has, and nobody reads slot g % 2 any more
+      Src pt;
+      const int ptks = S == 3 && ks > 0 ? target(ks - 1, pt) : 0;
+      substep(g, 1, ks, std::true_type{}, [&](int m) __attribute__((always_inline)) {
+        if constexpr (S == 3) {
+          if (ks > 0) {
+#pragma unroll
+            for (int i = kFirst + kPer * m; i < kFirst + kPer * m + kPer; ++i)
+              if (i < kLoadOps) load_part(i, pt, ptks, g - 1 + S);
+          }
+        }
+      });
+      // this wave's part of stage g + 1 has landed (S = 3: stage g + 2 may be in flight)
+      if constexpr (S == 2) wait_loads<0>();
+      else wait_loads_le(ks > 0 ? ops_of(ptks) : latest);
+      drain_barrier();    // every wave's has, and nobody reads slot g % S any more
       if constexpr (decltype(kLoad)::value) {
-        // stage ks + 2 of this tile, else the next tile's first, else a repeat never read
-        const bool in_tile = ks + 2 < nk;
         Src t;
-        t.w = in_tile ? csrc.w : nsrc.w;
-        t.x = in_tile ? csrc.x : nsrc.x;
-        t.sc = in_tile ? csrc.sc : nsrc.sc;
-        t.last_n = in_tile ? csrc.last_n : nsrc.last_n;
-        t.last_t = in_tile ? csrc.last_t : nsrc.last_t;
-        t.last_s = in_tile ? csrc.last_s : nsrc.last_s;
-        t.rot = in_tile ? csrc.rot : nsrc.rot;
-        const int tks = in_tile ? ks + 2 : (has_next ? 0 : nk - 1);
-        constexpr int kHalf = (kLoadOps + 1) / 2;
+        const int tks = target(ks, t);
         substep(g + 1, 0, ks + 1, std::true_type{}, [&](int m) __attribute__((always_inline)) {
-          if (m == 0) {
 #pragma unroll
-            for (int i = 0; i < kHalf; ++i) load_part(i, t, tks, g + 2);
-          }
-          if (m == 1) {
-#pragma unroll
-            for (int i = kHalf; i < kLoadOps; ++i) load_part(i, t, tks, g + 2);
-          }
+          for (int i = kPer * m; i < kPer * m + kPer; ++i)
+            if (i < kFirst) load_part(i, t, tks, g + S);
         });
       } else {
         substep(g + 1, 0, 0, std::false_type{}, [&](int) {});
@@ -306,56 +335,73 @@ __global__ __launch_bounds__(64 * WN * WM) void lin_tile_kernel(LinParams p, int
       __builtin_amdgcn_sched_barrier(0);
       ++g;
     };
+    // the tile's bias, a value per thread, goes to LDS before the last stage's
+    // barrier; the epilogue reads it after that, and the tile's closing barrier
+    // comes before the next tile's
+    float bias = 0.0f;
+    if (p.bias && tid < cur.rows_n) bias = bias_at(p, cur.n0 + tid);
     for (int ks = 0; ks + 1 < nk; ++ks) stage(ks, std::true_type{});
+    static_assert(BN <= 64 * kWaves, "a thread per feature");
+    if (tid < BN) s_bias[tid] = bias;
     stage(nk - 1, std::false_type{});
 
     // ---- epilogue ---------------------------------------------------------------------
     // The slot of the last stage is free until the barrier below.  A wave stages
-    // 32 tokens x 64 features at a time as fp32 rows of 256 bytes, 16-byte chunk
-    // c of row r at c ^ (r % 16): the writes (16 rows, one chunk) and the reads
-    // (8 lanes of a row) hit distinct banks.  Read back, a lane holds 8
-    // consecutive features of a token, so the residual comes in and the output
-    // leaves 128 bytes of a row at a time, and a quad holds an MX block.
+    // 16 tokens x 64 features at a time as fp32 rows of 256 bytes, 16-byte chunk
+    // c of row r at c ^ r: the writes (16 rows, one chunk) and the reads (8 lanes
+    // of a row) hit distinct banks.  Read back, a lane holds 8 consecutive
+    // features of a token, so the residual comes in and the output leaves 128
+    // bytes of a row at a time, and a quad holds an MX block.  A wave's memory
+    // operations complete in order and a wait behind a conditional store waits
+    // for it: the residual comes 64 tokens x 64 features (4 passes) at a time, so
+    // that only the group's first pass waits for memory.
     if (active) {
       const int li = opaque(lane & 31), lg = opaque(lane >> 5), lane_e = opaque(lane);
-      static_assert(kWaves * 8192 <= kSlotData && NA % 2 == 0, "staging fits the slot");
-      lds_u8* stg = (lds_u8*)(uintptr_t)(ring0 + (uint32_t)((g - 1) & 1) * (uint32_t)kSlot + (uint32_t)(wave * 8192));
+      static_assert(kWaves * 4096 <= kSlotData && NA % 2 == 0 && NB == 2, "staging fits the slot");
+      lds_u8* stg = (lds_u8*)(uintptr_t)(ring0 + (uint32_t)slot_of(g - 1) * (uint32_t)kSlot + (uint32_t)(wave * 4096));
       const int rr = lane_e >> 3, rc = lane_e & 7;
+      const int64_t t = cur.t0 + 32 * NB * wm + rr;   // the lane's first token; the others 8 apart
 #pragma unroll
-      for (int fm = 0; fm < NB; ++fm) {
-        const int64_t tb = cur.t0 + 32 * (NB * wm + fm);   // first token
-        const int t_left = (int)std::min<int64_t>(p.T - tb, 32);
+      for (int h = 0; h < NA / 2; ++h) {
+        const int f = 32 * NA * wn + 64 * h + 8 * rc;   // the lane's features in the tile
+        const int64_t n = cur.n0 + f;
+        const int cnt = (int)std::min<int64_t>(p.N - n, 8);
+        __builtin_amdgcn_sched_barrier(0);
+        uint4 res[8];
+        if (kVec) {
 #pragma unroll
-        for (int h = 0; h < NA / 2; ++h) {
-          const int64_t n = cur.n0 + 32 * NA * wn + 64 * h + 8 * rc;   // the lane's features
-          const int cnt = (int)std::min<int64_t>(p.N - n, 8);
-          __builtin_amdgcn_sched_barrier(0);
-          float b[8];
-          uint4 res[4];
-          epilogue_bias(p, n, cnt, b);
-          if (p.vec_out)
+          for (int i = 0; i < 8; ++i) res[i] = make_uint4(0, 0, 0, 0);
+          if (p.res)
 #pragma unroll
-            for (int it = 0; it < 4; ++it) {
-              const int r = 8 * it + rr;
-              res[it] = make_uint4(0, 0, 0, 0);
-              if (p.res && r < t_left && cnt > 0) res[it] = *reinterpret_cast<const uint4*>(p.res + (tb + r) * p.N + n);
-            }
+            for (int i = 0; i < 8; ++i)
+              if (t + 8 * i < p.T && cnt > 0) {
+                const u32x4* src = reinterpret_cast<const u32x4*>(p.res + (t + 8 * i) * p.N + n);
+                const u32x4 v = p.stream_res ? __builtin_nontemporal_load(src) : *src;
+                res[i] = make_uint4(v.x, v.y, v.z, v.w);
+              }
+        }
 #pragma unroll
-          for (int f = 0; f < 2; ++f)
+        for (int pass = 0; pass < 4; ++pass) {   // tokens 16 pass ..
+          if ((li >> 4) == (pass & 1)) {
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              const v16f& c = acc[2 * h + f][fm];
-              const f32x4 o = {c[4 * q], c[4 * q + 1], c[4 * q + 2], c[4 * q + 3]};
-              *reinterpret_cast<lds_f32x4*>(stg + li * 256 + (((8 * f + 2 * q + lg) ^ (li & 15)) << 4)) = o;
-            }
+            for (int ff = 0; ff < 2; ++ff)
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
+                const v16f& c = acc[2 * h + ff][pass >> 1];
+                const f32x4 o = {c[4 * q], c[4 * q + 1], c[4 * q + 2], c[4 * q + 3]};
+                *reinterpret_cast<lds_f32x4*>(stg + (li & 15) * 256 + (((8 * ff + 2 * q + lg) ^ (li & 15)) << 4)) = o;
+              }
+          }
           asm volatile("" ::: "memory");   // a wave's LDS accesses execute in issue order
+          const f32x4 b0 = *reinterpret_cast<const f32x4*>(s_bias + f), b1 = *reinterpret_cast<const f32x4*>(s_bias + f + 4);
+          const float b[8] = {b0.x, b0.y, b0.z, b0.w, b1.x, b1.y, b1.z, b1.w};
 #pragma unroll
-          for (int it = 0; it < 4; ++it) {
-            const int r = 8 * it + rr;
-            const f32x4 z0 = *reinterpret_cast<const lds_f32x4*>(stg + r * 256 + (((2 * rc) ^ (r & 15)) << 4));
-            const f32x4 z1 = *reinterpret_cast<const lds_f32x4*>(stg + r * 256 + (((2 * rc + 1) ^ (r & 15)) << 4));
+          for (int it = 0; it < 2; ++it) {
+            const int r = 8 * it + rr, i = 2 * pass + it;
+            const f32x4 z0 = *reinterpret_cast<const lds_f32x4*>(stg + r * 256 + (((2 * rc) ^ r) << 4));
+            const f32x4 z1 = *reinterpret_cast<const lds_f32x4*>(stg + r * 256 + (((2 * rc + 1) ^ r) << 4));
             float z[8] = {z0.x, z0.y, z0.z, z0.w, z1.x, z1.y, z1.z, z1.w};
-            epilogue8(p, tb + r, n, r < t_left ? cnt : 0, b, res[it], z);
+            epilogue8<kVec>(p, t + 8 * i, n, t + 8 * i < p.T ? cnt : 0, b, res[i], z);
             __builtin_amdgcn_sched_barrier(0);   // one row at a time
           }
           asm volatile("" ::: "memory");
@@ -364,7 +410,12 @@ __global__ __launch_bounds__(64 * WN * WM) void lin_tile_kernel(LinParams p, int
     }
     // the staging slot is done with: the loads that the last stage left out
     drain_barrier();
-    if (nk > 1) {
+    if constexpr (S == 3) {
+      if (has_next) {
+        load_stage(nsrc, S - 1, g + S - 1);
+        latest = ops_of(S - 1);
+      }
+    } else if (nk > 1) {
       if (has_next) load_stage(nsrc, 1, g + 1);
     } else if (cj + 2 < my_tiles) {
       load_stage(src_of(tile_at(cj + 2)), 0, g + 1);
@@ -373,7 +424,7 @@ __global__ __launch_bounds__(64 * WN * WM) void lin_tile_kernel(LinParams p, int
   wait_loads<0>();   // nothing may land in LDS that is no longer ours
 }
 
-template <int NA, int NB, int WN, int WM>
+template <int NA, int NB, int WN, int WM, int S>
 int launch_tiles(const LinParams& p, int per_cu, hipStream_t stream) {
   constexpr int BN = 32 * NA * WN, BM = 32 * NB * WM;
   const int64_t m_tiles = (p.T + BM - 1) / BM, n_tiles = (p.N + BN - 1) / BN;
@@ -384,18 +435,24 @@ int launch_tiles(const LinParams& p, int per_cu, hipStream_t stream) {
   const dim3 grid((unsigned)std::min(full, (total + 7) / 8 * 8)), block(64 * WN * WM);
   const bool groups = p.K % (4 * kStageK) == 0 && reinterpret_cast<uintptr_t>(p.xs) % 16 == 0 &&
                       reinterpret_cast<uintptr_t>(p.ws) % 16 == 0;
-  if (p.K % kStageK)
-    lin_tile_kernel<NA, NB, WN, WM, 1, true><<<grid, block, 0, stream>>>(p, (int)m_tiles, (int)n_tiles);
-  else if (groups)
-    lin_tile_kernel<NA, NB, WN, WM, 4, false><<<grid, block, 0, stream>>>(p, (int)m_tiles, (int)n_tiles);
-  else
-    lin_tile_kernel<NA, NB, WN, WM, 1, false><<<grid, block, 0, stream>>>(p, (int)m_tiles, (int)n_tiles);
+#define MX_TILE_LAUNCH(kG, kTail)                                                                          \
+  do {                                                                                                     \
+    if (p.vec)                                                                                             \
+      lin_tile_kernel<NA, NB, WN, WM, S, kG, kTail, true><<<grid, block, 0, stream>>>(p, (int)m_tiles, (int)n_tiles);  \
+    else                                                                                                   \
+      lin_tile_kernel<NA, NB, WN, WM, S, kG, kTail, false><<<grid, block, 0, stream>>>(p, (int)m_tiles, (int)n_tiles); \
+  } while (0)
+  if (p.K % kStageK) MX_TILE_LAUNCH(1, true);
+  else if (groups) MX_TILE_LAUNCH(4, false);
+  else MX_TILE_LAUNCH(1, false);
+#undef MX_TILE_LAUNCH
   return check_launch("mx_linear_fused");
 }
 
 }  // namespace
 
-int launch_lin_tile256(const LinParams& p, hipStream_t stream) { return launch_tiles<4, 2, 2, 4>(p, 1, stream); }
-int launch_lin_tile128(const LinParams& p, hipStream_t stream) { return launch_tiles<2, 2, 2, 2>(p, 2, stream); }
+int launch_lin_tile256(const LinParams& p, hipStream_t stream) { return launch_tiles<4, 2, 2, 4, 2>(p, 1, stream); }
+int launch_lin_tile128(const LinParams& p, hipStream_t stream) { return launch_tiles<2, 2, 2, 2, 2>(p, 2, stream); }
+int launch_lin_tile256x128(const LinParams& p, hipStream_t stream) { return launch_tiles<2, 2, 4, 2, 3>(p, 1, stream); }
 
 }  // namespace mxmoe
