@@ -2,6 +2,8 @@
 // global->LDS loads and the epilogue's arithmetic.
 #pragma once
 
+#include <type_traits>
+
 #include "fused.h"
 
 namespace mxmoe {
@@ -117,7 +119,7 @@ __device__ __forceinline__ float bias_at(const LinParams& p, int64_t n) {
   return p.bias_f32 ? static_cast<const float*>(p.bias)[n] : bf16_to_f32(static_cast<const uint16_t*>(p.bias)[n]);
 }
 
-// ---- the epilogue of 8 consecutive features n .. of token t -------------------------
+// ---- the epilogue of 8 consecutive features n .. of a token -------------------------
 // n is a multiple of 8; cnt (at most 8) of the features exist, none when cnt <=
 // 0.  The four lanes of a quad hold one 32-feature block of one token.
 
@@ -135,9 +137,22 @@ __device__ __forceinline__ void epilogue_bias(const LinParams& p, int64_t n, int
   }
 }
 
+// Where they lie: element el + lane_el of y, yq and the residual, scale byte s
+// + lane_s of ys.  With el and s uniform over the wave the addresses take a
+// scalar base and one 32-bit register.
+struct Place {
+  int64_t el, s;
+  uint32_t lane_el, lane_s;
+};
+template <class T>
+__device__ __forceinline__ T* at(T* base, int64_t el, uint32_t lane_el) {
+  return reinterpret_cast<T*>(reinterpret_cast<char*>(const_cast<typename std::remove_const<T>::type*>(base + el)) +
+                              (uint32_t)(lane_el * (uint32_t)sizeof(T)));
+}
+
 // kVec = p.vec; res: then the residual's 16 bytes (zeros without a residual)
 template <bool kVec>
-__device__ __forceinline__ void epilogue8(const LinParams& p, int64_t t, int64_t n, int cnt, const float (&b)[8],
+__device__ __forceinline__ void epilogue8(const LinParams& p, const Place& pl, int64_t n, int cnt, const float (&b)[8],
                                           const uint4& res, float (&z)[8]) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) z[i] += b[i];
@@ -148,7 +163,7 @@ __device__ __forceinline__ void epilogue8(const LinParams& p, int64_t t, int64_t
 #pragma unroll
     for (int i = 0; i < 8; ++i) z[i] += r[i];
   } else if (p.res && cnt > 0) {
-    const uint16_t* row = p.res + t * p.N + n;
+    const uint16_t* row = at(p.res, pl.el, pl.lane_el);
     uint16_t r[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) r[i] = row[i < cnt ? i : 0];
@@ -158,7 +173,7 @@ __device__ __forceinline__ void epilogue8(const LinParams& p, int64_t t, int64_t
   if (p.y) {
     if (cnt <= 0) return;
     const uint4 o = make_uint4(bf16x2(z[0], z[1]), bf16x2(z[2], z[3]), bf16x2(z[4], z[5]), bf16x2(z[6], z[7]));
-    uint16_t* y = p.y + t * p.N + n;
+    uint16_t* y = at(p.y, pl.el, pl.lane_el);
     if (kVec) {
       // written once: past the caches, which hold the operands of the tiles to come
       typedef unsigned int u4 __attribute__((ext_vector_type(4)));
@@ -183,7 +198,7 @@ __device__ __forceinline__ void epilogue8(const LinParams& p, int64_t t, int64_t
     const float inv = e8m0_inverse(sb);
     const uint2 o = make_uint2(e4m3x4(z[0] * inv, z[1] * inv, z[2] * inv, z[3] * inv),
                                e4m3x4(z[4] * inv, z[5] * inv, z[6] * inv, z[7] * inv));
-    uint8_t* q = p.yq + t * p.N + n;
+    uint8_t* q = at(p.yq, pl.el, pl.lane_el);
     if (kVec) {
       *reinterpret_cast<uint2*>(q) = o;
     } else {
@@ -192,10 +207,9 @@ __device__ __forceinline__ void epilogue8(const LinParams& p, int64_t t, int64_t
         if (i < cnt) q[i] = static_cast<uint8_t>((i < 4 ? o.x : o.y) >> (8 * (i & 3)));
     }
     if ((n & 31) == 0) {
-      const int64_t blk = n >> 5;
-      uint8_t* s = p.ys + t * p.ys_stride;
-      s[blk] = static_cast<uint8_t>(sb);
-      if (blk == (p.N - 1) >> 5 && blk + 1 < p.ys_stride) s[blk + 1] = 0;
+      uint8_t* s = at(p.ys, pl.s, pl.lane_s);
+      s[0] = static_cast<uint8_t>(sb);
+      if (n + 32 >= p.N && (n & 32) == 0) s[1] = 0;   // the last of an odd count: its pair's padding
     }
   }
 }

@@ -206,8 +206,9 @@ __global__ __launch_bounds__(64 * WV) void lin_stream_kernel(LinParams p) {
       z[0] += v0.x; z[1] += v0.y; z[2] += v0.z; z[3] += v0.w;
       z[4] += v1.x; z[5] += v1.y; z[6] += v1.z; z[7] += v1.w;
     }
-    if (p.vec) epilogue8<true>(p, t, n, cnt, b, res, z);
-    else epilogue8<false>(p, t, n, cnt, b, res, z);
+    const Place pl{t * p.N + n, t * p.ys_stride + (n >> 5), 0, 0};
+    if (p.vec) epilogue8<true>(p, pl, n, cnt, b, res, z);
+    else epilogue8<false>(p, pl, n, cnt, b, res, z);
   }
 }
 
@@ -232,12 +233,13 @@ int launch_linear(const LinParams& p, hipStream_t stream) {
   auto tiles = [&](int64_t bn, int64_t bm) { return ((p.N + bn - 1) / bn) * ((p.T + bm - 1) / bm); };
   auto rounds = [](int64_t n, int64_t slots) { return (n + slots - 1) / slots; };
   const int64_t t128 = tiles(128, 128);
+  const bool big = p.N >= (int64_t)1 << 27;   // the tile kernels' 32-bit offsets within 8 rows
   const int64_t us[5] = {
       rounds(tiles(32, 32), cus) * (18 + 17 * ((nk + 7) / 8) / 2),          // K over 8 waves
       rounds(tiles(64, 64), cus) * (30 + 23 * ((nk + 3) / 4) / 2),          // K over 4 waves
-      t128 <= cus ? 60 + 8 * nk : rounds(t128, 2 * cus) * (72 + 54 * nk / 5),   // two workgroups per CU
-      nk < 3 ? INT64_MAX : rounds(tiles(256, 128), cus) * (83 + 17 * nk / 2),
-      rounds(tiles(256, 256), cus) * (198 + 64 * nk / 5)};
+      big ? INT64_MAX : t128 <= cus ? 60 + 8 * nk : rounds(t128, 2 * cus) * (72 + 54 * nk / 5),   // two workgroups per CU
+      big || nk < 3 ? INT64_MAX : rounds(tiles(256, 128), cus) * (83 + 17 * nk / 2),
+      big ? INT64_MAX : rounds(tiles(256, 256), cus) * (198 + 64 * nk / 5)};
   switch (std::min_element(us, us + 5) - us) {
     case 0: return launch_stream<1, 1, 8, 2>(p, stream);
     case 1: return launch_stream<2, 2, 4, 2>(p, stream);

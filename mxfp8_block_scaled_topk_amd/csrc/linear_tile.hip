@@ -347,61 +347,79 @@ __global__ __launch_bounds__(64 * WN * WM) void lin_tile_kernel(LinParams p, int
 
     // ---- epilogue ---------------------------------------------------------------------
     // The slot of the last stage is free until the barrier below.  A wave stages
-    // 16 tokens x 64 features at a time as fp32 rows of 256 bytes, 16-byte chunk
-    // c of row r at c ^ r: the writes (16 rows, one chunk) and the reads (8 lanes
-    // of a row) hit distinct banks.  Read back, a lane holds 8 consecutive
+    // 16 or 32 tokens x 64 features at a time as fp32 rows of 256 bytes, 16-byte
+    // chunk c of row r at c ^ (r % 16): the writes (16 rows, one chunk) and the
+    // reads (8 lanes of a row) hit distinct banks.  Read back, a lane holds 8 consecutive
     // features of a token, so the residual comes in and the output leaves 128
     // bytes of a row at a time, and a quad holds an MX block.  A wave's memory
     // operations complete in order and a wait behind a conditional store waits
-    // for it: the residual comes 64 tokens x 64 features (4 passes) at a time, so
-    // that only the group's first pass waits for memory.
+    // for it: the residual comes 64 tokens x 64 features at a time, so that only
+    // the first of their rows waits for memory.
     if (active) {
       const int li = opaque(lane & 31), lg = opaque(lane >> 5), lane_e = opaque(lane);
-      static_assert(kWaves * 4096 <= kSlotData && NA % 2 == 0 && NB == 2, "staging fits the slot");
-      lds_u8* stg = (lds_u8*)(uintptr_t)(ring0 + (uint32_t)slot_of(g - 1) * (uint32_t)kSlot + (uint32_t)(wave * 4096));
+      constexpr int kTok = kWaves * 8192 <= kSlotData ? 32 : 16;   // tokens staged at a time
+      static_assert(kWaves * kTok * 256 <= kSlotData && NA % 2 == 0 && NB == 2, "staging fits the slot");
+      lds_u8* stg = (lds_u8*)(uintptr_t)(ring0 + (uint32_t)slot_of(g - 1) * (uint32_t)kSlot +
+                                         (uint32_t)(wave * kTok * 256));
       const int rr = lane_e >> 3, rc = lane_e & 7;
-      const int64_t t = cur.t0 + 32 * NB * wm + rr;   // the lane's first token; the others 8 apart
+      const int64_t t_w = cur.t0 + 32 * NB * wm, n_w = cur.n0 + 32 * NA * wn;   // the wave's first token and feature
+      const int t_left = (int)std::min<int64_t>(p.T - t_w, 32 * NB);
+      const uint32_t lane_el = (uint32_t)rr * (uint32_t)p.N + (uint32_t)(8 * rc);
+      const uint32_t lane_s = (uint32_t)rr * (uint32_t)p.ys_stride + (uint32_t)(rc >> 2);
 #pragma unroll
       for (int h = 0; h < NA / 2; ++h) {
         const int f = 32 * NA * wn + 64 * h + 8 * rc;   // the lane's features in the tile
         const int64_t n = cur.n0 + f;
         const int cnt = (int)std::min<int64_t>(p.N - n, 8);
         __builtin_amdgcn_sched_barrier(0);
+        // the lane's tokens are rr + 8 i
+        auto el_of = [&](int i) __attribute__((always_inline)) -> int64_t { return (t_w + 8 * i) * p.N + n_w + 64 * h; };
         uint4 res[8];
-        if (kVec) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) res[i] = make_uint4(0, 0, 0, 0);
-          if (p.res)
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-              if (t + 8 * i < p.T && cnt > 0) {
-                const u32x4* src = reinterpret_cast<const u32x4*>(p.res + (t + 8 * i) * p.N + n);
-                const u32x4 v = p.stream_res ? __builtin_nontemporal_load(src) : *src;
-                res[i] = make_uint4(v.x, v.y, v.z, v.w);
-              }
-        }
-#pragma unroll
-        for (int pass = 0; pass < 4; ++pass) {   // tokens 16 pass ..
-          if ((li >> 4) == (pass & 1)) {
+        for (int pass = 0; pass < 64 / kTok; ++pass) {   // tokens kTok pass ..
+          const int fm = pass * kTok / 32;
+          if (kTok == 32 || (li >> 4) == (pass & 1)) {
 #pragma unroll
             for (int ff = 0; ff < 2; ++ff)
 #pragma unroll
               for (int q = 0; q < 4; ++q) {
-                const v16f& c = acc[2 * h + ff][pass >> 1];
+                const v16f& c = acc[2 * h + ff][fm];
                 const f32x4 o = {c[4 * q], c[4 * q + 1], c[4 * q + 2], c[4 * q + 3]};
-                *reinterpret_cast<lds_f32x4*>(stg + (li & 15) * 256 + (((8 * ff + 2 * q + lg) ^ (li & 15)) << 4)) = o;
+                *reinterpret_cast<lds_f32x4*>(stg + (li % kTok) * 256 + (((8 * ff + 2 * q + lg) ^ (li & 15)) << 4)) = o;
               }
           }
           asm volatile("" ::: "memory");   // a wave's LDS accesses execute in issue order
+          if (pass == 0 && kVec) {
+            // after the first accumulators left their registers
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) res[i] = make_uint4(0, 0, 0, 0);
+            if (p.res && cnt > 0) {
+              if (p.stream_res) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                  if (rr + 8 * i < t_left) {
+                    const u32x4 v =
+                        __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(at(p.res, el_of(i), lane_el)));
+                    res[i] = make_uint4(v.x, v.y, v.z, v.w);
+                  }
+              } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                  if (rr + 8 * i < t_left) res[i] = *reinterpret_cast<const uint4*>(at(p.res, el_of(i), lane_el));
+              }
+            }
+          }
           const f32x4 b0 = *reinterpret_cast<const f32x4*>(s_bias + f), b1 = *reinterpret_cast<const f32x4*>(s_bias + f + 4);
           const float b[8] = {b0.x, b0.y, b0.z, b0.w, b1.x, b1.y, b1.z, b1.w};
 #pragma unroll
-          for (int it = 0; it < 2; ++it) {
-            const int r = 8 * it + rr, i = 2 * pass + it;
-            const f32x4 z0 = *reinterpret_cast<const lds_f32x4*>(stg + r * 256 + (((2 * rc) ^ r) << 4));
-            const f32x4 z1 = *reinterpret_cast<const lds_f32x4*>(stg + r * 256 + (((2 * rc + 1) ^ r) << 4));
+          for (int it = 0; it < kTok / 8; ++it) {
+            const int r = 8 * it + rr, i = kTok / 8 * pass + it;
+            const f32x4 z0 = *reinterpret_cast<const lds_f32x4*>(stg + r * 256 + (((2 * rc) ^ (r & 15)) << 4));
+            const f32x4 z1 = *reinterpret_cast<const lds_f32x4*>(stg + r * 256 + (((2 * rc + 1) ^ (r & 15)) << 4));
             float z[8] = {z0.x, z0.y, z0.z, z0.w, z1.x, z1.y, z1.z, z1.w};
-            epilogue8<kVec>(p, t + 8 * i, n, t + 8 * i < p.T ? cnt : 0, b, res[i], z);
+            const Place pl{el_of(i), (t_w + 8 * i) * p.ys_stride + ((n_w + 64 * h) >> 5), lane_el, lane_s};
+            epilogue8<kVec>(p, pl, n, rr + 8 * i < t_left ? cnt : 0, b, res[i], z);
             __builtin_amdgcn_sched_barrier(0);   // one row at a time
           }
           asm volatile("" ::: "memory");
