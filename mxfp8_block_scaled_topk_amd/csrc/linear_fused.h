@@ -25,7 +25,6 @@ struct LinParams {
   int bias_f32;
   int act;             // mx_activation
   int stream_res;      // the residual is too large to be left in the memory-side cache
-  int vec;             // rows of y and of the residual are whole 16-byte pieces, of yq 8-byte ones
 };
 
 typedef int v8i __attribute__((ext_vector_type(8)));
@@ -125,15 +124,23 @@ __device__ __forceinline__ float bias_at(const LinParams& p, int64_t n) {
 
 // their bias (0 where there is none)
 __device__ __forceinline__ void epilogue_bias(const LinParams& p, int64_t n, int cnt, float (&b)[8]) {
-  if (!p.bias || cnt <= 0) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) b[i] = 0.0f;
-  } else if (p.bias_f32) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) b[i] = static_cast<const float*>(p.bias)[n + (i < cnt ? i : 0)];
+  for (int i = 0; i < 8; ++i) b[i] = 0.0f;
+  if (!p.bias || cnt <= 0) return;
+  if (cnt >= 8) {
+    if (p.bias_f32) {
+      __builtin_memcpy(b, static_cast<const float*>(p.bias) + n, 32);
+    } else {
+      uint4 u;
+      __builtin_memcpy(&u, static_cast<const uint16_t*>(p.bias) + n, 16);
+      unpack_bf16x8(u, b);
+    }
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) b[i] = bf16_to_f32(static_cast<const uint16_t*>(p.bias)[n + (i < cnt ? i : 0)]);
+    for (int i = 0; i < 7; ++i) {
+      const float v = bias_at(p, n + (i < cnt ? i : 0));
+      b[i] = i < cnt ? v : 0.0f;
+    }
   }
 }
 
@@ -150,39 +157,54 @@ __device__ __forceinline__ T* at(T* base, int64_t el, uint32_t lane_el) {
                               (uint32_t)(lane_el * (uint32_t)sizeof(T)));
 }
 
-// kVec = p.vec; res: then the residual's 16 bytes (zeros without a residual)
-template <bool kVec>
+// 16 and 8 bytes on a boundary of their elements only: gfx950 loads and stores
+// them in one instruction all the same (rows of any width, measured within 5 %
+// of aligned ones).
+typedef unsigned int u32x4_any __attribute__((ext_vector_type(4), aligned(2)));
+typedef unsigned int u32x2_any __attribute__((ext_vector_type(2), aligned(1)));
+
+// The residual of the 8 features as 16 bytes (zeros past cnt).
+template <bool kStream>
+__device__ __forceinline__ uint4 load_res8(const uint16_t* r, int cnt) {
+  uint4 u;
+  if (cnt >= 8) {
+    const u32x4_any* src = reinterpret_cast<const u32x4_any*>(r);
+    const u32x4_any v = kStream ? __builtin_nontemporal_load(src) : *src;
+    u = make_uint4(v.x, v.y, v.z, v.w);
+  } else {
+    uint16_t e[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) e[i] = r[i < cnt ? i : 0];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) e[i] = i < cnt ? e[i] : 0;
+    u = make_uint4(e[0] | (uint32_t)e[1] << 16, e[2] | (uint32_t)e[3] << 16, e[4] | (uint32_t)e[5] << 16,
+                   e[6] | (uint32_t)e[7] << 16);
+  }
+  return u;
+}
+
+// res: load_res8's (zeros without a residual)
 __device__ __forceinline__ void epilogue8(const LinParams& p, const Place& pl, int64_t n, int cnt, const float (&b)[8],
                                           const uint4& res, float (&z)[8]) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) z[i] += b[i];
   activate(z, p.act);
-  if (kVec) {
-    float r[8];
-    unpack_bf16x8(res, r);
+  float r[8];
+  unpack_bf16x8(res, r);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) z[i] += r[i];
-  } else if (p.res && cnt > 0) {
-    const uint16_t* row = at(p.res, pl.el, pl.lane_el);
-    uint16_t r[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) r[i] = row[i < cnt ? i : 0];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) z[i] += bf16_to_f32(r[i]);
-  }
+  for (int i = 0; i < 8; ++i) z[i] += r[i];
   if (p.y) {
     if (cnt <= 0) return;
     const uint4 o = make_uint4(bf16x2(z[0], z[1]), bf16x2(z[2], z[3]), bf16x2(z[4], z[5]), bf16x2(z[6], z[7]));
     uint16_t* y = at(p.y, pl.el, pl.lane_el);
-    if (kVec) {
+    if (cnt >= 8) {
       // written once: past the caches, which hold the operands of the tiles to come
-      typedef unsigned int u4 __attribute__((ext_vector_type(4)));
-      const u4 oo = {o.x, o.y, o.z, o.w};
-      __builtin_nontemporal_store(oo, reinterpret_cast<u4*>(y));
+      const u32x4_any v = {o.x, o.y, o.z, o.w};
+      __builtin_nontemporal_store(v, reinterpret_cast<u32x4_any*>(y));
     } else {
       const uint32_t w[4] = {o.x, o.y, o.z, o.w};
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
+      for (int i = 0; i < 7; ++i)
         if (i < cnt) y[i] = static_cast<uint16_t>(w[i >> 1] >> (16 * (i & 1)));
     }
   } else {
@@ -199,11 +221,12 @@ __device__ __forceinline__ void epilogue8(const LinParams& p, const Place& pl, i
     const uint2 o = make_uint2(e4m3x4(z[0] * inv, z[1] * inv, z[2] * inv, z[3] * inv),
                                e4m3x4(z[4] * inv, z[5] * inv, z[6] * inv, z[7] * inv));
     uint8_t* q = at(p.yq, pl.el, pl.lane_el);
-    if (kVec) {
-      *reinterpret_cast<uint2*>(q) = o;
+    if (cnt >= 8) {
+      const u32x2_any v = {o.x, o.y};
+      *reinterpret_cast<u32x2_any*>(q) = v;
     } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
+      for (int i = 0; i < 7; ++i)
         if (i < cnt) q[i] = static_cast<uint8_t>((i < 4 ? o.x : o.y) >> (8 * (i & 3)));
     }
     if ((n & 31) == 0) {

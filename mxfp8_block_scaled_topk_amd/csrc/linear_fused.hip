@@ -198,7 +198,7 @@ __global__ __launch_bounds__(64 * WV) void lin_stream_kernel(LinParams p) {
     float z[8] = {}, b[8];
     uint4 res = make_uint4(0, 0, 0, 0);
     epilogue_bias(p, n, cnt, b);
-    if (p.vec && p.res && cnt > 0) res = *reinterpret_cast<const uint4*>(p.res + t * p.N + n);
+    if (p.res && cnt > 0) res = load_res8<false>(p.res + t * p.N + n, cnt);
 #pragma unroll
     for (int w = 0; w < WV; ++w) {
       const float* src = part + (w * NF * MF + f * MF + m) * kTile + tl * kPitch + 8 * (lane & 3);
@@ -207,8 +207,7 @@ __global__ __launch_bounds__(64 * WV) void lin_stream_kernel(LinParams p) {
       z[4] += v1.x; z[5] += v1.y; z[6] += v1.z; z[7] += v1.w;
     }
     const Place pl{t * p.N + n, t * p.ys_stride + (n >> 5), 0, 0};
-    if (p.vec) epilogue8<true>(p, pl, n, cnt, b, res, z);
-    else epilogue8<false>(p, pl, n, cnt, b, res, z);
+    epilogue8(p, pl, n, cnt, b, res, z);
   }
 }
 
@@ -328,8 +327,6 @@ extern "C" int mx_linear_fused(const void* x, const void* x_s, const void* w_u8,
   // measured at N = 4096: non-temporal residual loads 282 -> 267 us at T = 16384
   // (134 MB), 46 -> 49 us at T = 4096 (34 MB)
   p.stream_res = T * N > (int64_t)48 << 20;
-  p.vec = N % 8 == 0 && reinterpret_cast<uintptr_t>(yq_u8) % 8 == 0 &&
-          (reinterpret_cast<uintptr_t>(y_bf16) | reinterpret_cast<uintptr_t>(residual_bf16)) % 16 == 0;
   // Outputs overlap nothing, except that y may take the residual's place.
   const uint64_t s_bytes = (uint64_t)p.s_stride, dense = (uint64_t)T * (uint64_t)N;
   const Span in[7] = {{x, (uint64_t)T * (uint64_t)K * (mx_in ? 1 : 2)},

@@ -59,7 +59,7 @@ constexpr int kBand = 8;
 // 16-byte boundaries): 16 scale bytes per row at a group's first stage, into a
 // double-buffered ring of their own.  1: the stage's 4 bytes per row.  kTail
 // (with kG = 1): K is not a multiple of 128; see lin_stream_kernel.
-template <int NA, int NB, int WN, int WM, int S, int kG, bool kTail, bool kVec>
+template <int NA, int NB, int WN, int WM, int S, int kG, bool kTail>
 __global__ __launch_bounds__(64 * WN * WM) void lin_tile_kernel(LinParams p, int m_tiles, int n_tiles) {
   constexpr int kWaves = WN * WM;
   constexpr int BN = 32 * NA * WN, BM = 32 * NB * WM;
@@ -389,7 +389,7 @@ __global__ __launch_bounds__(64 * WN * WM) void lin_tile_kernel(LinParams p, int
               }
           }
           asm volatile("" ::: "memory");   // a wave's LDS accesses execute in issue order
-          if (pass == 0 && kVec) {
+          if (pass == 0) {
             // after the first accumulators left their registers
             __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
@@ -398,15 +398,11 @@ __global__ __launch_bounds__(64 * WN * WM) void lin_tile_kernel(LinParams p, int
               if (p.stream_res) {
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
-                  if (rr + 8 * i < t_left) {
-                    const u32x4 v =
-                        __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(at(p.res, el_of(i), lane_el)));
-                    res[i] = make_uint4(v.x, v.y, v.z, v.w);
-                  }
+                  if (rr + 8 * i < t_left) res[i] = load_res8<true>(at(p.res, el_of(i), lane_el), cnt);
               } else {
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
-                  if (rr + 8 * i < t_left) res[i] = *reinterpret_cast<const uint4*>(at(p.res, el_of(i), lane_el));
+                  if (rr + 8 * i < t_left) res[i] = load_res8<false>(at(p.res, el_of(i), lane_el), cnt);
               }
             }
           }
@@ -419,7 +415,7 @@ __global__ __launch_bounds__(64 * WN * WM) void lin_tile_kernel(LinParams p, int
             const f32x4 z1 = *reinterpret_cast<const lds_f32x4*>(stg + r * 256 + (((2 * rc + 1) ^ (r & 15)) << 4));
             float z[8] = {z0.x, z0.y, z0.z, z0.w, z1.x, z1.y, z1.z, z1.w};
             const Place pl{el_of(i), (t_w + 8 * i) * p.ys_stride + ((n_w + 64 * h) >> 5), lane_el, lane_s};
-            epilogue8<kVec>(p, pl, n, rr + 8 * i < t_left ? cnt : 0, b, res[i], z);
+            epilogue8(p, pl, n, rr + 8 * i < t_left ? cnt : 0, b, res[i], z);
             __builtin_amdgcn_sched_barrier(0);   // one row at a time
           }
           asm volatile("" ::: "memory");
@@ -453,17 +449,10 @@ int launch_tiles(const LinParams& p, int per_cu, hipStream_t stream) {
   const dim3 grid((unsigned)std::min(full, (total + 7) / 8 * 8)), block(64 * WN * WM);
   const bool groups = p.K % (4 * kStageK) == 0 && reinterpret_cast<uintptr_t>(p.xs) % 16 == 0 &&
                       reinterpret_cast<uintptr_t>(p.ws) % 16 == 0;
-#define MX_TILE_LAUNCH(kG, kTail)                                                                          \
-  do {                                                                                                     \
-    if (p.vec)                                                                                             \
-      lin_tile_kernel<NA, NB, WN, WM, S, kG, kTail, true><<<grid, block, 0, stream>>>(p, (int)m_tiles, (int)n_tiles);  \
-    else                                                                                                   \
-      lin_tile_kernel<NA, NB, WN, WM, S, kG, kTail, false><<<grid, block, 0, stream>>>(p, (int)m_tiles, (int)n_tiles); \
-  } while (0)
-  if (p.K % kStageK) MX_TILE_LAUNCH(1, true);
-  else if (groups) MX_TILE_LAUNCH(4, false);
-  else MX_TILE_LAUNCH(1, false);
-#undef MX_TILE_LAUNCH
+  const int mt = (int)m_tiles, nt = (int)n_tiles;
+  if (p.K % kStageK) lin_tile_kernel<NA, NB, WN, WM, S, 1, true><<<grid, block, 0, stream>>>(p, mt, nt);
+  else if (groups) lin_tile_kernel<NA, NB, WN, WM, S, 4, false><<<grid, block, 0, stream>>>(p, mt, nt);
+  else lin_tile_kernel<NA, NB, WN, WM, S, 1, false><<<grid, block, 0, stream>>>(p, mt, nt);
   return check_launch("mx_linear_fused");
 }
 
