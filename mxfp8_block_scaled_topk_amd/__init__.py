@@ -825,7 +825,7 @@ def mx_linear_fused(x, w, w_s, x_s=None, bias=None, act="none", residual=None, q
         y = out
         _need_like(y, (T, N), "out", torch.bfloat16, dev)
     lib = load()
-    need = lib.mx_linear_fused_workspace_size(T, K, N, mx_in)
+    need = 0 if mx_in else lib.mx_linear_fused_workspace_size(T, K, N, 0)
     if workspace is not None:
         _need_workspace(workspace, need, dev)
     _need_gpu(x, "x")

@@ -16,7 +16,9 @@
 // 128-element stages w, w + WV, ...), so the waves of a workgroup read whole
 // kilobytes of a weight row together.  Each wave streams its stages through an
 // LDS ring of its own by direct global->LDS loads, S stages ahead, with no
-// barrier in the loop; the accumulators meet in LDS at the end.
+// barrier in the loop; the accumulators meet in LDS at the end.  Few bf16 tokens
+// (a decode step) skip the quantiser's launch: every workgroup quantises them
+// into LDS itself while its first weights are on their way.
 #include <algorithm>
 
 #include "linear_fused.h"
@@ -42,9 +44,17 @@ __device__ __forceinline__ int swz(int r, int c) { return r * kStageK + ((c ^ ((
 // bytes of the row's first present ones (nothing past a row is read), and the
 // token operand's are zeroed, so they add nothing; scale rows are then only
 // 2-byte aligned and come two bytes at a time.
-template <int NF, int MF, int WV, int S, bool kTail>
+//
+// kX16: p.x is bf16 [T, K], T <= 32 and T K <= kMaxResident (host).  The tokens
+// stay in LDS as MXFP8 rows of nk stages, swizzled like a slot's, each row an
+// odd number of 128-byte stages long so that 16 rows' chunks hit distinct banks;
+// only the weights go through the rings.
+constexpr int kMaxResident = 65536;
+
+template <int NF, int MF, int WV, int S, bool kTail, bool kX16>
 __global__ __launch_bounds__(64 * WV) void lin_stream_kernel(LinParams p) {
-  constexpr int kRows = 32 * (NF + MF);              // LDS rows per slot: weights, then tokens
+  static_assert(!kX16 || MF == 1, "one fragment of resident tokens");
+  constexpr int kRows = 32 * (NF + (kX16 ? 0 : MF));   // LDS rows per slot: weights, then tokens
   constexpr int kScaleOps = (kRows + 63) / 64;       // 64 rows per scale load
   constexpr int kScaleBytes = kScaleOps * 256 * (kTail ? 2 : 1);
   constexpr int kSlot = kRows * kStageK + kScaleBytes;
@@ -54,6 +64,9 @@ __global__ __launch_bounds__(64 * WV) void lin_stream_kernel(LinParams p) {
   static_assert(S >= 2 && S <= 3 && (S - 1) * kOps < 64, "vmcnt range");
   static_assert(WV * NF * MF * 32 * kPitch * 4 <= kRing, "the partial tiles reuse the ring");
   __shared__ __attribute__((aligned(16))) uint8_t ring[kRing];
+  // kX16: at most T (nk + 1) stages of 128 bytes and T nk scale words; T (K + 256) and T (K + 128) / 32 bound them
+  __shared__ __attribute__((aligned(16))) uint8_t xres[kX16 ? kMaxResident + 32 * 256 : 16];
+  __shared__ uint32_t xsc[kX16 ? (kMaxResident + 32 * 128) / 128 : 1];
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -73,7 +86,7 @@ __global__ __launch_bounds__(64 * WV) void lin_stream_kernel(LinParams p) {
   const uint8_t* sptr[kScaleOps];
 #pragma unroll
   for (int j = 0; j < kScaleOps; ++j) {
-    const int r = 64 * j + lane;
+    const int r = kX16 ? (64 * j + lane) & (32 * NF - 1) : 64 * j + lane;   // (a spare half repeats the weights')
     sptr[j] = r < 32 * NF ? p.ws + (n0 + std::min(r, n_last)) * p.s_stride
                           : p.xs + (t0 + std::min(r - 32 * NF, t_last)) * p.s_stride;
   }
@@ -111,11 +124,59 @@ __global__ __launch_bounds__(64 * WV) void lin_stream_kernel(LinParams p) {
 #pragma unroll
       for (int v = 0; v < 16; ++v) acc[f][m][v] = 0.0f;
 
+  // ---- kX16: the tokens, quantised by the workgroup ----------------------------------
+  const int xstages = p.nk | 1;   // per row
+  constexpr int kBlk = 2;         // blocks whose loads a thread has in flight
+  const int nblk = (int)p.T * p.nk * 4;   // blocks past K are zeros
+  u32x4_any xin[kX16 ? kBlk : 1][4];
+  auto load_blocks = [&](int u0) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < kBlk; ++i) {
+      const int u = u0 + i * 64 * WV;
+      const int r = u / (p.nk * 4), b = u - r * (p.nk * 4);
+#pragma unroll
+      for (int v = 0; v < 4; ++v) xin[i][v] = u32x4_any{0, 0, 0, 0};
+      if (u < nblk && 32 * b < p.K) {
+        const u32x4_any* src = reinterpret_cast<const u32x4_any*>(reinterpret_cast<const uint16_t*>(p.x) + r * p.K + 32 * b);
+#pragma unroll
+        for (int v = 0; v < 4; ++v) xin[i][v] = src[v];
+      }
+    }
+  };
+  auto store_blocks = [&](int u0) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < kBlk; ++i) {
+      const int u = u0 + i * 64 * WV;
+      if (u >= nblk) continue;
+      const int r = u / (p.nk * 4), b = u - r * (p.nk * 4);
+      float v[32];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        unpack_bf16x8(make_uint4(xin[i][j].x, xin[i][j].y, xin[i][j].z, xin[i][j].w), v + 8 * j);
+      uint32_t q[8];
+      reinterpret_cast<uint8_t*>(xsc)[r * p.nk * 4 + b] = static_cast<uint8_t>(mx_block32(v, q));
+      uint8_t* dst = xres + (r * xstages + (b >> 2)) * kStageK;
+      const int c = 2 * (b & 3), sw = (r >> 1) & 7;
+      *reinterpret_cast<uint4*>(dst + ((c ^ sw) << 4)) = make_uint4(q[0], q[1], q[2], q[3]);
+      *reinterpret_cast<uint4*>(dst + (((c + 1) ^ sw) << 4)) = make_uint4(q[4], q[5], q[6], q[7]);
+    }
+  };
+  if constexpr (kX16) load_blocks(tid);
+
   const int li = lane & 31, lg = lane >> 5;
   const int cnt = wave < p.nk ? (p.nk - wave + WV - 1) / WV : 0;   // this wave's stages
 #pragma unroll
   for (int i = 0; i < S; ++i)
     if (i < cnt) issue(wave + i * WV, i);
+  if constexpr (kX16) {
+    store_blocks(tid);
+    for (int u = tid + kBlk * 64 * WV; u < nblk; u += kBlk * 64 * WV) {
+      load_blocks(u);
+      store_blocks(u);
+    }
+    __syncthreads();
+  }
+  const int xrow = std::min(li, t_last);
   int slot = 0;
   for (int i = 0; i < cnt; ++i) {
     const int ks = wave + i * WV;
@@ -148,13 +209,22 @@ __global__ __launch_bounds__(64 * WV) void lin_stream_kernel(LinParams p) {
       }
 #pragma unroll
       for (int m = 0; m < MF; ++m) {
-        fb[s][m] = frag(32 * (NF + m) + li, s);
-        sb[s][m] = scale(32 * (NF + m) + li, s);
+        if constexpr (kX16) {
+          const uint8_t* xr = xres + (xrow * xstages + ks) * kStageK;
+          const int sw = (xrow >> 1) & 7;
+          const uint4 u0 = *reinterpret_cast<const uint4*>(xr + (((4 * s + lg) ^ sw) << 4));
+          const uint4 u1 = *reinterpret_cast<const uint4*>(xr + (((4 * s + 2 + lg) ^ sw) << 4));
+          fb[s][m] = v8i{(int)u0.x, (int)u0.y, (int)u0.z, (int)u0.w, (int)u1.x, (int)u1.y, (int)u1.z, (int)u1.w};
+          sb[s][m] = reinterpret_cast<const uint8_t*>(xsc)[(xrow * p.nk + ks) * 4 + 2 * s + lg];
+        } else {
+          fb[s][m] = frag(32 * (NF + m) + li, s);
+          sb[s][m] = scale(32 * (NF + m) + li, s);
+        }
       }
     }
     wait_lds();   // the slot is read: refill it
     if (i + S < cnt) issue(ks + S * WV, slot);
-    if (kTail && ks == p.nk - 1) {
+    if (kTail && !kX16 && ks == p.nk - 1) {
 #pragma unroll
       for (int s = 0; s < 2; ++s)
 #pragma unroll
@@ -211,14 +281,14 @@ __global__ __launch_bounds__(64 * WV) void lin_stream_kernel(LinParams p) {
   }
 }
 
-template <int NF, int MF, int WV, int S>
+template <int NF, int MF, int WV, int S, bool kX16>
 int launch_stream(const LinParams& p, hipStream_t stream) {
   const int64_t grid = ((p.N + 32 * NF - 1) / (32 * NF)) * ((p.T + 32 * MF - 1) / (32 * MF));
   if (grid * 64 * WV >= (int64_t)1 << 32) return fail(MX_ERR_UNSUPPORTED, "mx_linear_fused: too many tiles");
   if (p.K % kStageK)
-    lin_stream_kernel<NF, MF, WV, S, true><<<dim3((unsigned)grid), dim3(64 * WV), 0, stream>>>(p);
+    lin_stream_kernel<NF, MF, WV, S, true, kX16><<<dim3((unsigned)grid), dim3(64 * WV), 0, stream>>>(p);
   else
-    lin_stream_kernel<NF, MF, WV, S, false><<<dim3((unsigned)grid), dim3(64 * WV), 0, stream>>>(p);
+    lin_stream_kernel<NF, MF, WV, S, false, kX16><<<dim3((unsigned)grid), dim3(64 * WV), 0, stream>>>(p);
   return check_launch("mx_linear_fused");
 }
 
@@ -240,13 +310,16 @@ int launch_linear(const LinParams& p, hipStream_t stream) {
       big || nk < 3 ? INT64_MAX : rounds(tiles(256, 128), cus) * (83 + 17 * nk / 2),
       big ? INT64_MAX : rounds(tiles(256, 256), cus) * (198 + 64 * nk / 5)};
   switch (std::min_element(us, us + 5) - us) {
-    case 0: return launch_stream<1, 1, 8, 2>(p, stream);
-    case 1: return launch_stream<2, 2, 4, 2>(p, stream);
+    case 0: return launch_stream<1, 1, 8, 2, false>(p, stream);
+    case 1: return launch_stream<2, 2, 4, 2, false>(p, stream);
     case 2: return launch_lin_tile128(p, stream);
     case 3: return launch_lin_tile256x128(p, stream);
     default: return launch_lin_tile256(p, stream);
   }
 }
+
+// bf16 tokens that every workgroup quantises for itself (no workspace).
+bool resident(int64_t T, int64_t K) { return T <= 32 && T * K <= kMaxResident; }
 
 // Workspace: the MXFP8 form of bf16 tokens.
 struct FusedLayout {
@@ -254,7 +327,7 @@ struct FusedLayout {
 };
 FusedLayout fused_layout(int64_t T, int64_t K, int x_is_mx) {
   FusedLayout L{0, 0, 0};
-  if (x_is_mx) return L;
+  if (x_is_mx || resident(T, K)) return L;
   L.xs = align_up((size_t)(T * K), 256);
   L.total = L.xs + align_up((size_t)(T * 2 * ((K + 63) / 64)), 256);
   return L;
@@ -346,6 +419,9 @@ extern "C" int mx_linear_fused(const void* x, const void* x_s, const void* w_u8,
   if (mx_in) {
     p.x = static_cast<const uint8_t*>(x);
     p.xs = static_cast<const uint8_t*>(x_s);
+  } else if (resident(T, K)) {
+    p.x = static_cast<const uint8_t*>(x);
+    return launch_stream<1, 1, 8, 2, true>(p, s);
   } else {
     uint8_t* xq = static_cast<uint8_t*>(workspace);
     uint8_t* xs = xq + L.xs;

@@ -270,3 +270,24 @@ def test_linear_fused_stream_and_graph(T):
             eager = mx.mx_linear_fused(bufs[j], w, ws, act="gelu")
             torch.cuda.synchronize()
             assert torch.equal(outs[j], eager), (i, j)
+
+
+@pytest.mark.parametrize("T,K,N,act", [
+    (32, 2048, 96, "none"), (16, 4096, 130, "silu"), (1, 65536, 33, "none"), (31, 2080, 64, "gelu"),
+    (32, 2080, 64, "none"), (7, 96, 1000, "relu"), (2, 32736, 40, "none"), (32, 32, 32, "gelu_tanh"),
+])
+def test_linear_fused_few_bf16_tokens(T, K, N, act):
+    """bf16 tokens on both sides of the size that workgroups quantise for
+    themselves (T <= 32, T K <= 65536, no workspace): the bytes of the MXFP8 call
+    on mx_quantize's output wherever the same kernel runs, and the definition's."""
+    assert (mx.linear_fused_workspace_size(T, K, N, False) == 0) == (T * K <= 65536)
+    run_case(T, K, N, T + K, False, "f32", act, True, False, "few bf16")
+    run_case(T, K, N, T + K + 1, False, "none", act, False, True, "few bf16")
+    xb, _, wq = draw(T, K, N, 3)
+    x = bf16_dev(xb)
+    raw = torch.zeros(T * K + 1, dtype=torch.bfloat16, device="cuda")[1:].view(T, K)   # an odd address
+    raw.copy_(x)
+    a = mx.mx_linear_fused(x, u8_dev(wq[0]), u8_dev(wq[1]), act=act)
+    b = mx.mx_linear_fused(raw, u8_dev(wq[0]), u8_dev(wq[1]), act=act)
+    torch.cuda.synchronize()
+    assert torch.equal(a, b)
