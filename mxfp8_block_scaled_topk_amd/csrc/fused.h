@@ -56,6 +56,21 @@ __device__ __forceinline__ float wave_sum(float x) {
   return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(x), 63));
 }
 
+// 16 and 8 bytes on a boundary of their elements only: gfx950 loads and stores
+// them in one instruction all the same.
+typedef unsigned int u32x4_any __attribute__((ext_vector_type(4), aligned(2)));
+typedef unsigned int u32x2_any __attribute__((ext_vector_type(2), aligned(1)));
+
+// e4m3x4 with its saturation in one instruction per value (finite inputs).
+__device__ __forceinline__ uint32_t e4m3x4_sat(float a, float b, float c, float d) {
+  a = __builtin_amdgcn_fmed3f(a, -448.0f, 448.0f);
+  b = __builtin_amdgcn_fmed3f(b, -448.0f, 448.0f);
+  c = __builtin_amdgcn_fmed3f(c, -448.0f, 448.0f);
+  d = __builtin_amdgcn_fmed3f(d, -448.0f, 448.0f);
+  const int lo = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
+  return static_cast<uint32_t>(__builtin_amdgcn_cvt_pk_fp8_f32(c, d, lo, true));
+}
+
 // Maximum over a quad of lanes (quad_perm [1, 0, 3, 2], then [2, 3, 0, 1]).
 __device__ __forceinline__ float quad_max(float x) {
   x = fmaxf(x, dpp_f32<0xb1>(x, x));

@@ -157,12 +157,6 @@ __device__ __forceinline__ T* at(T* base, int64_t el, uint32_t lane_el) {
                               (uint32_t)(lane_el * (uint32_t)sizeof(T)));
 }
 
-// 16 and 8 bytes on a boundary of their elements only: gfx950 loads and stores
-// them in one instruction all the same (rows of any width, measured within 5 %
-// of aligned ones).
-typedef unsigned int u32x4_any __attribute__((ext_vector_type(4), aligned(2)));
-typedef unsigned int u32x2_any __attribute__((ext_vector_type(2), aligned(1)));
-
 // The residual of the 8 features as 16 bytes (zeros past cnt).
 template <bool kStream>
 __device__ __forceinline__ uint4 load_res8(const uint16_t* r, int cnt) {
@@ -218,8 +212,8 @@ __device__ __forceinline__ void epilogue8(const LinParams& p, const Place& pl, i
     if (cnt <= 0) return;
     const uint32_t sb = e8m0_from_amax(a);
     const float inv = e8m0_inverse(sb);
-    const uint2 o = make_uint2(e4m3x4(z[0] * inv, z[1] * inv, z[2] * inv, z[3] * inv),
-                               e4m3x4(z[4] * inv, z[5] * inv, z[6] * inv, z[7] * inv));
+    const uint2 o = make_uint2(e4m3x4_sat(z[0] * inv, z[1] * inv, z[2] * inv, z[3] * inv),
+                               e4m3x4_sat(z[4] * inv, z[5] * inv, z[6] * inv, z[7] * inv));
     uint8_t* q = at(p.yq, pl.el, pl.lane_el);
     if (cnt >= 8) {
       const u32x2_any v = {o.x, o.y};

@@ -12,13 +12,12 @@
 // of lanes owns one 32-element MX block and its amax is two DPP exchanges.  W
 // waves share a row, chunk c of lane t covering elements 8 (64 W c + t) .. + 8:
 // the loads and stores of a wave are contiguous.  The row stays in registers
-// between the sum of squares and the outputs (up to 64 elements a lane);
+// between the sum of squares and the outputs (up to 32 elements a lane);
 // the sum is a tree over the lane's elements, the wave (DPP) and the W waves
-// (LDS).  Rows longer than 65536 are read twice (add_rmsnorm_long).
+// (LDS).  Rows longer than 32768 (16384 when they are not aligned) are read twice
+// (add_rmsnorm_long).
 // HBM-bound: 2 bytes per element in (4 with a residual), 1 + 1/32 out (2 more
 // for each of residual_out and y).
-#include <string.h>
-
 #include <algorithm>
 #include <cfloat>
 #include <cmath>
@@ -44,69 +43,89 @@ struct NormParams {
   float eps;
 };
 
-// Eight bf16 at p as floats, the n first of them (the rest 0).  kVec: p is
-// 16-byte aligned and n = 8.
-template <bool kVec>
+// The first n (1 .. 7) of the 16-byte window's 8 elements that ends n elements
+// into the window (elements before a row's last chunk are readable): moved to
+// the front, zeros behind them.
+__device__ __forceinline__ uint4 window8(const u32x4_any& u, int n) {
+  const uint64_t lo = (uint64_t)u.y << 32 | u.x, hi = (uint64_t)u.w << 32 | u.z;
+  const int s = 16 * (8 - n);
+  const uint64_t a = s < 64 ? lo >> s | hi << (64 - s) : hi >> (s - 64);
+  const uint64_t b = s < 64 ? hi >> s : 0;
+  return make_uint4((uint32_t)a, (uint32_t)(a >> 32), (uint32_t)b, (uint32_t)(b >> 32));
+}
+
+// Eight bf16 at p as floats, the n first of them (the rest 0).  kVec: n = 8.
+// kTiny: the row may be shorter than 8 elements.
+template <bool kVec, bool kTiny>
 __device__ __forceinline__ void load8(const uint16_t* p, int n, float (&v)[8]) {
   if (kVec || n >= 8) {
-    uint4 u;
-    if constexpr (kVec)
-      u = *reinterpret_cast<const uint4*>(p);
-    else
-      memcpy(&u, p, 16);   // any alignment: gfx950 loads take one instruction all the same
-    unpack_bf16x8(u, v);
-  } else {
-    uint16_t t[8];   // eight loads in flight, none behind a branch
+    const u32x4_any u = *reinterpret_cast<const u32x4_any*>(p);
+    unpack_bf16x8(make_uint4(u.x, u.y, u.z, u.w), v);
+  } else if constexpr (kTiny) {
+    uint16_t t[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) t[i] = p[i < n ? i : 0];
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = i < n ? bf16_to_f32(t[i]) : 0.0f;
+  } else {
+    unpack_bf16x8(window8(*reinterpret_cast<const u32x4_any*>(p + n - 8), n), v);
   }
 }
 
-template <bool kVec>
+template <bool kVec, bool kTiny>
 __device__ __forceinline__ void load_weight8(const NormParams& p, int64_t e, int n, float (&w)[8]) {
   if (p.w_f32) {
     const float* f = static_cast<const float*>(p.weight) + e;
     if (kVec || n >= 8) {
-      float4 a, b;
-      if constexpr (kVec) {
-        a = reinterpret_cast<const float4*>(f)[0];
-        b = reinterpret_cast<const float4*>(f)[1];
-      } else {
-        memcpy(&a, f, 16);
-        memcpy(&b, f + 4, 16);
+      const u32x4_any a = *reinterpret_cast<const u32x4_any*>(f), b = *reinterpret_cast<const u32x4_any*>(f + 4);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        w[i] = __uint_as_float(a[i]);
+        w[4 + i] = __uint_as_float(b[i]);
       }
-      w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
-      w[4] = b.x; w[5] = b.y; w[6] = b.z; w[7] = b.w;
     } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) w[i] = f[i < n ? i : 0];
+      for (int i = 0; i < 7; ++i) w[i] = f[i < n ? i : 0];
 #pragma unroll
       for (int i = 0; i < 8; ++i) w[i] = i < n ? w[i] : 0.0f;
     }
   } else {
-    load8<kVec>(static_cast<const uint16_t*>(p.weight) + e, n, w);
+    load8<kVec, kTiny>(static_cast<const uint16_t*>(p.weight) + e, n, w);
   }
 }
 
+// The first `bytes` (1 .. 15) of the 16 in (lo, hi).
+__device__ __forceinline__ void store_part(uint8_t* p, uint64_t lo, uint64_t hi, int bytes) {
+  if (bytes & 8) {
+    __builtin_memcpy(p, &lo, 8);
+    p += 8;
+    lo = hi;
+  }
+  if (bytes & 4) {
+    const uint32_t v = (uint32_t)lo;
+    __builtin_memcpy(p, &v, 4);
+    p += 4;
+    lo >>= 32;
+  }
+  if (bytes & 2) {
+    const uint16_t v = (uint16_t)lo;
+    __builtin_memcpy(p, &v, 2);
+    p += 2;
+    lo >>= 16;
+  }
+  if (bytes & 1) *p = (uint8_t)lo;
+}
+
+// Whole pieces of an output go past this XCD's L2: they are written once, for a
+// kernel on any XCD (16384 x 2048 with three outputs 71 -> 61 us, rows of 1001
+// 52 -> 35).
 template <bool kVec>
 __device__ __forceinline__ void store_bf16x8(uint16_t* p, int n, const float (&v)[8]) {
-  uint4 u;
-  u.x = bf16x2(v[0], v[1]);
-  u.y = bf16x2(v[2], v[3]);
-  u.z = bf16x2(v[4], v[5]);
-  u.w = bf16x2(v[6], v[7]);
-  if constexpr (kVec) {
-    *reinterpret_cast<uint4*>(p) = u;
-  } else if (n >= 8) {
-    memcpy(p, &u, 16);
-  } else {
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int i = 0; i < 7; ++i)
-      if (i < n) p[i] = static_cast<uint16_t>(w[i >> 1] >> (16 * (i & 1)));
-  }
+  const u32x4_any u = {bf16x2(v[0], v[1]), bf16x2(v[2], v[3]), bf16x2(v[4], v[5]), bf16x2(v[6], v[7])};
+  if (kVec || n >= 8)
+    __builtin_nontemporal_store(u, reinterpret_cast<u32x4_any*>(p));
+  else
+    store_part(reinterpret_cast<uint8_t*>(p), (uint64_t)u.y << 32 | u.x, (uint64_t)u.w << 32 | u.z, 2 * n);
 }
 
 // The outputs of 8 elements e .. of row r from h and rstd (n of them exist;
@@ -128,19 +147,14 @@ __device__ __forceinline__ void emit8(const NormParams& p, int64_t r, int64_t e,
   if (n <= 0) return;
   const uint32_t sb = e8m0_from_amax(amax);
   const float inv = e8m0_inverse(sb);
-  const uint32_t lo = e4m3x4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv);
-  const uint32_t hi = e4m3x4(v[4] * inv, v[5] * inv, v[6] * inv, v[7] * inv);
+  const uint32_t lo = e4m3x4_sat(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv);
+  const uint32_t hi = e4m3x4_sat(v[4] * inv, v[5] * inv, v[6] * inv, v[7] * inv);
   uint8_t* d = p.q + r * p.K + e;
-  const uint2 u = make_uint2(lo, hi);
-  if constexpr (kVec) {
-    *reinterpret_cast<uint2*>(d) = u;
-  } else if (n >= 8) {
-    memcpy(d, &u, 8);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 7; ++i)
-      if (i < n) d[i] = static_cast<uint8_t>((i < 4 ? lo : hi) >> (8 * (i & 3)));
-  }
+  const u32x2_any u = {lo, hi};
+  if (kVec || n >= 8)
+    __builtin_nontemporal_store(u, reinterpret_cast<u32x2_any*>(d));
+  else
+    store_part(d, (uint64_t)hi << 32 | lo, 0, n);
   if ((threadIdx.x & 3) == 0) {
     const int b = static_cast<int>(e >> 5);
     uint8_t* sr = p.s + r * p.s_stride;
@@ -170,7 +184,8 @@ __device__ __forceinline__ float rstd_of(float sum, const NormParams& p) {
 }
 
 // W waves per row (kR = max(1, 4 / W) rows per workgroup), C chunks per lane.
-template <int W, int C, bool kVec>
+// kTiny: rows of fewer than 8 elements.
+template <int W, int C, bool kVec, bool kTiny>
 __global__ __launch_bounds__(64 * (W < 4 ? 4 : W)) void add_rmsnorm_kernel(NormParams p) {
   constexpr int kRows = W < 4 ? 4 / W : 1;
   static_assert(W == 1 || W >= 4, "one wave per row, or the workgroup's waves share one");
@@ -185,7 +200,7 @@ __global__ __launch_bounds__(64 * (W < 4 ? 4 : W)) void add_rmsnorm_kernel(NormP
       const int64_t e = 8 * (int64_t)(64 * W * c + lane);
       const int n = static_cast<int>(std::min<int64_t>(p.K - e, 8));
       if (n > 0) {
-        load8<kVec>(p.x + r * p.ldx + e, n, h[c]);
+        load8<kVec, kTiny>(p.x + r * p.ldx + e, n, h[c]);
       } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i) h[c][i] = 0.0f;
@@ -198,7 +213,7 @@ __global__ __launch_bounds__(64 * (W < 4 ? 4 : W)) void add_rmsnorm_kernel(NormP
         const int n = static_cast<int>(std::min<int64_t>(p.K - e, 8));
         if (n > 0) {
           float a[8];
-          load8<kVec>(p.res + r * p.ldr + e, n, a);
+          load8<kVec, kTiny>(p.res + r * p.ldr + e, n, a);
 #pragma unroll
           for (int i = 0; i < 8; ++i) h[c][i] += a[i];
         }
@@ -211,14 +226,26 @@ __global__ __launch_bounds__(64 * (W < 4 ? 4 : W)) void add_rmsnorm_kernel(NormP
       for (int i = 0; i < 4; ++i) t[i] = h[c][2 * i] * h[c][2 * i] + h[c][2 * i + 1] * h[c][2 * i + 1];
       sum += (t[0] + t[1]) + (t[2] + t[3]);
     }
+    // the weight: with few chunks per lane (few or short rows, where latency
+    // counts) requested before the sum's exchange
+    constexpr bool kEarly = C <= 2;
+    float w[kEarly ? C : 1][8] = {};
+    auto load_w = [&](int c, float (&v)[8]) __attribute__((always_inline)) {
+      const int64_t e = 8 * (int64_t)(64 * W * c + lane);
+      const int n = static_cast<int>(std::min<int64_t>(p.K - e, 8));
+      if (n > 0) load_weight8<kVec, kTiny>(p, e, n, v);
+    };
+    if constexpr (kEarly) {
+#pragma unroll
+      for (int c = 0; c < C; ++c) load_w(c, w[c]);
+    }
     const float rstd = rstd_of(row_sum<W>(sum, part), p);
 #pragma unroll
     for (int c = 0; c < C; ++c) {
       const int64_t e = 8 * (int64_t)(64 * W * c + lane);
       const int n = static_cast<int>(std::min<int64_t>(p.K - e, 8));
-      float w[8] = {};
-      if (n > 0) load_weight8<kVec>(p, e, n, w);
-      emit8<kVec>(p, r, e, n, h[c], w, rstd);
+      if constexpr (!kEarly) load_w(c, w[0]);
+      emit8<kVec>(p, r, e, n, h[c], w[kEarly ? c : 0], rstd);
     }
   }
 }
@@ -238,10 +265,10 @@ __global__ __launch_bounds__(64 * kLongWaves) void add_rmsnorm_long(NormParams p
 #pragma unroll
       for (int i = 0; i < 8; ++i) h[i] = 0.0f;
       if (n <= 0) return;
-      load8<kVec>(p.x + r * p.ldx + e, n, h);
+      load8<kVec, false>(p.x + r * p.ldx + e, n, h);
       if (p.res) {
         float a[8];
-        load8<kVec>(p.res + r * p.ldr + e, n, a);
+        load8<kVec, false>(p.res + r * p.ldr + e, n, a);
 #pragma unroll
         for (int i = 0; i < 8; ++i) h[i] += a[i];
       }
@@ -263,7 +290,7 @@ __global__ __launch_bounds__(64 * kLongWaves) void add_rmsnorm_long(NormParams p
       const int n = static_cast<int>(std::min<int64_t>(p.K - e, 8));
       float h[8], w[8] = {};
       load_h(e, n, h);
-      if (n > 0) load_weight8<kVec>(p, e, n, w);
+      if (n > 0) load_weight8<kVec, false>(p, e, n, w);
       emit8<kVec>(p, r, e, n, h, w, rstd);
     }
   }
@@ -273,24 +300,39 @@ template <bool kVec>
 void launch_norm(const NormParams& p, hipStream_t stream) {
   const int64_t cap = (int64_t)num_cus() * 32;
   const int64_t chunks = (p.K + 7) / 8;   // of a row
-#define MX_NORM_LAUNCH(W, C)                                                                               \
-  do {                                                                                                     \
-    const int64_t per = W < 4 ? 4 / W : 1;                                                                 \
-    const int64_t grid = std::min(cap, (p.rows + per - 1) / per);                                          \
-    add_rmsnorm_kernel<W, C, kVec><<<dim3((unsigned)grid), dim3(64 * (W < 4 ? 4 : W)), 0, stream>>>(p);    \
+#define MX_NORM_LAUNCH_T(W, C, kTiny)                                                                          \
+  do {                                                                                                         \
+    const int64_t per = W < 4 ? 4 / W : 1;                                                                     \
+    const int64_t grid = std::min(cap, (p.rows + per - 1) / per);                                              \
+    add_rmsnorm_kernel<W, C, kVec, kTiny><<<dim3((unsigned)grid), dim3(64 * (W < 4 ? 4 : W)), 0, stream>>>(p); \
   } while (0)
-  if (chunks <= 64) MX_NORM_LAUNCH(1, 1);
+#define MX_NORM_LAUNCH(W, C) MX_NORM_LAUNCH_T(W, C, false)
+#define MX_NORM_LONG()                                                                         \
+  add_rmsnorm_long<kVec><<<dim3((unsigned)std::min<int64_t>((int64_t)num_cus() * 2, p.rows)), \
+                           dim3(64 * kLongWaves), 0, stream>>>(p)
+  if (p.K < 8) {
+    if constexpr (!kVec) MX_NORM_LAUNCH_T(1, 1, true);
+  } else if (p.rows <= num_cus()) {
+    // a row's latency counts, not the waves it takes (1 row of 2048: 4.8 us with
+    // one wave of 4 chunks a lane, 2.7 with 4 waves)
+    if (chunks <= 64) MX_NORM_LAUNCH(1, 1);
+    else if (chunks <= 256) MX_NORM_LAUNCH(4, 1);
+    else if (chunks <= 512) MX_NORM_LAUNCH(8, 1);
+    else if (chunks <= 1024) MX_NORM_LAUNCH(16, 1);
+    else if (chunks <= 2048) MX_NORM_LAUNCH(16, 2);
+    else if (kVec && chunks <= 4096) MX_NORM_LAUNCH(16, 4);
+    else MX_NORM_LONG();
+  } else if (chunks <= 64) MX_NORM_LAUNCH(1, 1);
   else if (chunks <= 128) MX_NORM_LAUNCH(1, 2);
   else if (chunks <= 256) MX_NORM_LAUNCH(1, 4);
   else if (chunks <= 512) MX_NORM_LAUNCH(4, 2);
   else if (chunks <= 1024) MX_NORM_LAUNCH(4, 4);
   else if (chunks <= 2048) MX_NORM_LAUNCH(8, 4);
-  else if (chunks <= 4096) MX_NORM_LAUNCH(16, 4);
-  else if (chunks <= 8192) MX_NORM_LAUNCH(16, 8);
-  else
-    add_rmsnorm_long<kVec><<<dim3((unsigned)std::min<int64_t>((int64_t)num_cus() * 2, p.rows)),
-                             dim3(64 * kLongWaves), 0, stream>>>(p);
+  else if (kVec && chunks <= 4096) MX_NORM_LAUNCH(16, 4);
+  else MX_NORM_LONG();
+#undef MX_NORM_LONG
 #undef MX_NORM_LAUNCH
+#undef MX_NORM_LAUNCH_T
 }
 
 }  // namespace
