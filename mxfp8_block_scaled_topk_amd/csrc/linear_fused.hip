@@ -295,25 +295,34 @@ int launch_stream(const LinParams& p, hipStream_t stream) {
 // Which kernel: the one whose time, in units of 0.1 us, a line through its
 // measured times says is shortest.  Its tiles go over the CUs in rounds; a round
 // costs a part per tile and a part per k stage of a wave.  Fitted to all kernels
-// on 110 shapes (T to 16384, K and N to 8192, drawn over their logarithms), the
-// rule's choice takes 0.4 % longer than the fastest on average, 15 % at worst.
+// on 220 shapes (T to 16384, K and N to 8192, drawn over their logarithms), the
+// rule's choice takes 0.5 % longer than the fastest on average, 30 % at worst.
+// The smaller kernels differ only in how the tiles fill the rounds (32 x 32, 64 x
+// 64 and the tile kernels alone: 5 % longer on average, up to 46 %): T = 203, K =
+// 2080, N = 4099 takes 20.8 us in 260 tiles of 64 x 64, 18.9 us in 455 of 64 x 32.
 int launch_linear(const LinParams& p, hipStream_t stream) {
   const int64_t cus = num_cus(), nk = p.nk;
   auto tiles = [&](int64_t bn, int64_t bm) { return ((p.N + bn - 1) / bn) * ((p.T + bm - 1) / bm); };
-  auto rounds = [](int64_t n, int64_t slots) { return (n + slots - 1) / slots; };
+  auto up = [](int64_t n, int64_t d) { return (n + d - 1) / d; };
   const int64_t t128 = tiles(128, 128);
   const bool big = p.N >= (int64_t)1 << 27;   // the tile kernels' 32-bit offsets within 8 rows
-  const int64_t us[5] = {
-      rounds(tiles(32, 32), cus) * (18 + 17 * ((nk + 7) / 8) / 2),          // K over 8 waves
-      rounds(tiles(64, 64), cus) * (30 + 23 * ((nk + 3) / 4) / 2),          // K over 4 waves
-      big ? INT64_MAX : t128 <= cus ? 60 + 8 * nk : rounds(t128, 2 * cus) * (72 + 54 * nk / 5),   // two workgroups per CU
-      big || nk < 3 ? INT64_MAX : rounds(tiles(256, 128), cus) * (83 + 17 * nk / 2),
-      big ? INT64_MAX : rounds(tiles(256, 256), cus) * (198 + 64 * nk / 5)};
-  switch (std::min_element(us, us + 5) - us) {
+  const int64_t us[8] = {
+      up(tiles(32, 32), cus) * (30 + 21 * up(nk, 8) / 2),       // K over 8 waves
+      up(tiles(64, 32), cus) * (33 + 13 * up(nk, 6)),           // over 6
+      up(tiles(64, 64), cus) * (43 + 25 * up(nk, 4) / 2),       // over 4
+      up(tiles(64, 96), cus) * (67 + 13 * up(nk, 3)),           // over 3
+      up(tiles(64, 64), 2 * cus) * (66 + 10 * up(nk, 2)),       // over 2, two workgroups per CU
+      big ? INT64_MAX : t128 <= cus ? 83 + 17 * nk / 2 : up(t128, 2 * cus) * (82 + 11 * nk),   // two per CU
+      big || nk < 3 ? INT64_MAX : up(tiles(256, 128), cus) * (102 + 9 * nk),
+      big ? INT64_MAX : up(tiles(256, 256), cus) * (171 + 14 * nk)};
+  switch (std::min_element(us, us + 8) - us) {
     case 0: return launch_stream<1, 1, 8, 2, false>(p, stream);
-    case 1: return launch_stream<2, 2, 4, 2, false>(p, stream);
-    case 2: return launch_lin_tile128(p, stream);
-    case 3: return launch_lin_tile256x128(p, stream);
+    case 1: return launch_stream<2, 1, 6, 2, false>(p, stream);
+    case 2: return launch_stream<2, 2, 4, 2, false>(p, stream);
+    case 3: return launch_stream<2, 3, 3, 2, false>(p, stream);
+    case 4: return launch_stream<2, 2, 2, 2, false>(p, stream);
+    case 5: return launch_lin_tile128(p, stream);
+    case 6: return launch_lin_tile256x128(p, stream);
     default: return launch_lin_tile256(p, stream);
   }
 }

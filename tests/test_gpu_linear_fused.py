@@ -51,15 +51,15 @@ def group_maxima(xq, wq):
         K = q.shape[1]
         pay = np.maximum(np.abs(mx_ref.e4m3_decode(q)), 2.0 ** -6)
         e = mx_ref.scales_flat(s, K).astype(np.float64) - 127
-        return torch.from_numpy((pay * np.repeat(np.exp2(e), 32, axis=1)[:, :K]).astype(np.float32))
+        return torch.from_numpy((pay * np.repeat(np.exp2(e), 32, axis=1)[:, :K]).astype(np.float32)).cuda()
     px, pw = p_of(*xq), p_of(*wq)
-    total = torch.zeros(px.shape[0], pw.shape[0])
+    total = torch.zeros(px.shape[0], pw.shape[0], device="cuda")
     for g in range(0, px.shape[1], 8):
         best = px[:, g, None] * pw[None, :, g]
         for k in range(g + 1, g + 8):
             torch.maximum(best, px[:, k, None] * pw[None, :, k], out=best)
         total += best
-    return total.double().numpy() * (1 + 2.0 ** -12)   # these sums are float32
+    return total.double().cpu().numpy() * (1 + 2.0 ** -12)   # these sums are float32
 
 
 def reference(xq, wq, bias, act, res):
@@ -128,6 +128,27 @@ def test_linear_fused(i):
                  residual=c % 4 < 2, mx_out=j == 1, what=f"case {c}")
 
 
+# two sizes, one with an incomplete last k stage, for each tile shape that only
+# wide outputs reach: weight rows x tokens
+WIDE = [
+    (45, 96, 4225), (128, 640, 4096),        # 64 x 32
+    (100, 1056, 4099), (150, 512, 5440),     # 64 x 64
+    (131, 992, 5505), (129, 896, 5633),      # 64 x 96
+    (199, 160, 4130), (330, 384, 4810),      # 64 x 64, two workgroups per CU
+    (450, 416, 4100), (600, 768, 4500),      # 128 x 128
+    (1030, 1696, 4099), (1030, 1664, 4096),  # 256 x 128
+    (1440, 672, 5633), (1500, 1280, 5633),   # 256 x 256
+]
+
+
+@pytest.mark.parametrize("i", range(len(WIDE)))
+def test_linear_fused_wide(i):
+    T, K, N = WIDE[i]
+    run_case(T, K, N, 200 + i, mx_in=i % 3 != 0, bias=["none", "bf16", "f32"][i % 3], act=ACTS[i % 5],
+             residual=i % 4 < 2, mx_out=i % 7 == 3, what=f"wide {i}")
+    exact_case(T, K, N)
+
+
 @pytest.mark.parametrize("T", [5, 200, 600])
 @pytest.mark.parametrize("act", ACTS)
 @pytest.mark.parametrize("mx_out", [False, True])
@@ -135,27 +156,31 @@ def test_linear_fused_epilogues(T, act, mx_out):
     run_case(T, 256, 320, T, True, "f32", act, True, mx_out, "epilogue")
 
 
-def test_linear_fused_exact():
+def exact_case(T, K, N):
     """Small integers with power-of-two scales: every sum is exact in float32,
     so the bf16 output is the correctly rounded one, at every tile position."""
-    for T, K, N in [(1, 128, 96), (29, 416, 131), (64, 1024, 256), (300, 640, 520), (1030, 256, 1030)]:
-        rng = np.random.default_rng(T)
-        # one nonzero block scale pair per row keeps every product a small integer times 2^-6
-        xi = rng.integers(-15, 16, (T, K)).astype(np.float64)
-        wi = rng.integers(-15, 16, (N, K)).astype(np.float64)
-        xq, wq = mx_ref.e4m3_encode(xi), mx_ref.e4m3_encode(wi)
-        nb = -(-K // 32)
-        pad = -(-K // 64) * 2
-        xs, ws = np.zeros((T, pad), np.uint8), np.zeros((N, pad), np.uint8)
-        xs[:, :nb] = rng.integers(125, 129, (T, nb))
-        ws[:, :nb] = rng.integers(126, 129, (N, nb))
-        xs, ws = xs.reshape(T, -1, 2), ws.reshape(N, -1, 2)
-        say(f"mx_linear_fused exact T={T} K={K} N={N}")
-        y = mx.mx_linear_fused(u8_dev(xq), u8_dev(wq), u8_dev(ws), x_s=u8_dev(xs))
-        torch.cuda.synchronize()
-        z = mx_ref.mx_dequantize_ref(xq, xs) @ mx_ref.mx_dequantize_ref(wq, ws).T
-        assert np.abs(z).max() < 2 ** 19   # 24 bits from the unit 2^-3
-        assert np.array_equal(bf16_host(y), mx_ref.f32_to_bf16(z.astype(np.float32)))
+    rng = np.random.default_rng(T)
+    # scales near 1 keep every product a small integer times 2^-3
+    xi = rng.integers(-15, 16, (T, K)).astype(np.float64)
+    wi = rng.integers(-15, 16, (N, K)).astype(np.float64)
+    xq, wq = mx_ref.e4m3_encode(xi), mx_ref.e4m3_encode(wi)
+    nb = -(-K // 32)
+    pad = -(-K // 64) * 2
+    xs, ws = np.zeros((T, pad), np.uint8), np.zeros((N, pad), np.uint8)
+    xs[:, :nb] = rng.integers(125, 129, (T, nb))
+    ws[:, :nb] = rng.integers(126, 129, (N, nb))
+    xs, ws = xs.reshape(T, -1, 2), ws.reshape(N, -1, 2)
+    say(f"mx_linear_fused exact T={T} K={K} N={N}")
+    y = mx.mx_linear_fused(u8_dev(xq), u8_dev(wq), u8_dev(ws), x_s=u8_dev(xs))
+    torch.cuda.synchronize()
+    z = mx_ref.mx_dequantize_ref(xq, xs) @ mx_ref.mx_dequantize_ref(wq, ws).T
+    assert np.abs(z).max() < 2 ** 19   # 24 bits from the unit 2^-3
+    assert np.array_equal(bf16_host(y), mx_ref.f32_to_bf16(z.astype(np.float32)))
+
+
+@pytest.mark.parametrize("T,K,N", [(1, 128, 96), (29, 416, 131), (64, 1024, 256), (300, 640, 520), (1030, 256, 1030)])
+def test_linear_fused_exact(T, K, N):
+    exact_case(T, K, N)
 
 
 def test_linear_fused_quantised_input_is_mx_quantize():
