@@ -584,6 +584,8 @@ TYPE_F32 = 1
 # the current stream's handle on a device, without a Stream object around it
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
+# the current device's index; only called once a tensor is known to be on a GPU
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _need_like(t, shape, name, dtype, device):
@@ -601,7 +603,7 @@ def _elsewhere(device, stream):
     stream is given.  With a stream, what the call allocates comes from that
     stream's pool (see _stream_scoped)."""
     if stream is None:
-        return None if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+        return None if device.index == _current_device() else torch.cuda.device(device)
     if stream.device != device:
         raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
     return torch.cuda.stream(stream)
@@ -613,6 +615,8 @@ def _addr(t):
 
 def _rows(t, name):
     """t [..., K] as (a 2-D view or copy, row stride) with unit inner stride."""
+    if t.dim() == 2 and t.is_contiguous():
+        return t, t.shape[1]
     t2 = t if t.dim() == 2 else t.reshape(-1, t.shape[-1])
     rows, k = t2.shape
     if k > 1 and t2.stride(1) != 1:

@@ -24,6 +24,7 @@ struct LinParams {
   int tail_blocks;     // this many 32-element blocks (1 .. 4)
   int bias_f32;
   int act;             // mx_activation
+  uint32_t n_tiles, t_tiles;   // lin_stream_kernel's tiles along N and T
   int stream_res;      // the residual is too large to be left in the memory-side cache
 };
 

@@ -70,9 +70,16 @@ __global__ __launch_bounds__(64 * WV) void lin_stream_kernel(LinParams p) {
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int64_t n_tiles = (p.N + 32 * NF - 1) / (32 * NF);
-  const int64_t tt = blockIdx.x / n_tiles;
-  const int64_t n0 = (blockIdx.x - tt * n_tiles) * (32 * NF), t0 = tt * (32 * MF);
+  // Workgroups go over the XCDs in turn: XCD b % 8 takes a contiguous share of
+  // the tiles, cut along the longer side, so that one L2 sees an operand row.
+  const uint32_t share = (p.n_tiles * p.t_tiles) >> 3, spare = (p.n_tiles * p.t_tiles) & 7;
+  const uint32_t xcd = blockIdx.x & 7;
+  const uint32_t id = xcd * share + std::min(xcd, spare) + (blockIdx.x >> 3);
+  const bool by_rows = p.N >= p.T;
+  const uint32_t inner = by_rows ? p.t_tiles : p.n_tiles;
+  const uint32_t outer_i = id / inner, inner_i = id - outer_i * inner;
+  const int64_t n0 = (int64_t)(by_rows ? outer_i : inner_i) * (32 * NF);
+  const int64_t t0 = (int64_t)(by_rows ? inner_i : outer_i) * (32 * MF);
   const int n_last = (int)std::min<int64_t>(p.N - 1 - n0, 32 * NF - 1);   // last row that exists
   const int t_last = (int)std::min<int64_t>(p.T - 1 - t0, 32 * MF - 1);
 
@@ -282,8 +289,10 @@ __global__ __launch_bounds__(64 * WV) void lin_stream_kernel(LinParams p) {
 }
 
 template <int NF, int MF, int WV, int S, bool kX16>
-int launch_stream(const LinParams& p, hipStream_t stream) {
-  const int64_t grid = ((p.N + 32 * NF - 1) / (32 * NF)) * ((p.T + 32 * MF - 1) / (32 * MF));
+int launch_stream(LinParams p, hipStream_t stream) {
+  p.n_tiles = (uint32_t)((p.N + 32 * NF - 1) / (32 * NF));
+  p.t_tiles = (uint32_t)((p.T + 32 * MF - 1) / (32 * MF));
+  const int64_t grid = (int64_t)p.n_tiles * p.t_tiles;
   if (grid * 64 * WV >= (int64_t)1 << 32) return fail(MX_ERR_UNSUPPORTED, "mx_linear_fused: too many tiles");
   if (p.K % kStageK)
     lin_stream_kernel<NF, MF, WV, S, true, kX16><<<dim3((unsigned)grid), dim3(64 * WV), 0, stream>>>(p);
@@ -296,10 +305,10 @@ int launch_stream(const LinParams& p, hipStream_t stream) {
 // measured times says is shortest.  Its tiles go over the CUs in rounds; a round
 // costs a part per tile and a part per k stage of a wave.  Fitted to all kernels
 // on 220 shapes (T to 16384, K and N to 8192, drawn over their logarithms), the
-// rule's choice takes 0.5 % longer than the fastest on average, 30 % at worst.
+// rule's choice takes 0.3 % longer than the fastest on average, 30 % at worst.
 // The smaller kernels differ only in how the tiles fill the rounds (32 x 32, 64 x
 // 64 and the tile kernels alone: 5 % longer on average, up to 46 %): T = 203, K =
-// 2080, N = 4099 takes 20.8 us in 260 tiles of 64 x 64, 18.9 us in 455 of 64 x 32.
+// 2080, N = 4099 takes 19.3 us in 260 tiles of 64 x 64, 14.8 us in 455 of 64 x 32.
 int launch_linear(const LinParams& p, hipStream_t stream) {
   const int64_t cus = num_cus(), nk = p.nk;
   auto tiles = [&](int64_t bn, int64_t bm) { return ((p.N + bn - 1) / bn) * ((p.T + bm - 1) / bm); };
@@ -307,13 +316,13 @@ int launch_linear(const LinParams& p, hipStream_t stream) {
   const int64_t t128 = tiles(128, 128);
   const bool big = p.N >= (int64_t)1 << 27;   // the tile kernels' 32-bit offsets within 8 rows
   const int64_t us[8] = {
-      up(tiles(32, 32), cus) * (30 + 21 * up(nk, 8) / 2),       // K over 8 waves
-      up(tiles(64, 32), cus) * (33 + 13 * up(nk, 6)),           // over 6
-      up(tiles(64, 64), cus) * (43 + 25 * up(nk, 4) / 2),       // over 4
-      up(tiles(64, 96), cus) * (67 + 13 * up(nk, 3)),           // over 3
-      up(tiles(64, 64), 2 * cus) * (66 + 10 * up(nk, 2)),       // over 2, two workgroups per CU
-      big ? INT64_MAX : t128 <= cus ? 83 + 17 * nk / 2 : up(t128, 2 * cus) * (82 + 11 * nk),   // two per CU
-      big || nk < 3 ? INT64_MAX : up(tiles(256, 128), cus) * (102 + 9 * nk),
+      up(tiles(32, 32), cus) * (32 + 17 * up(nk, 8) / 2),       // K over 8 waves
+      up(tiles(64, 32), cus) * (34 + 11 * up(nk, 6)),           // over 6
+      up(tiles(64, 64), cus) * (44 + 11 * up(nk, 4)),           // over 4
+      up(tiles(64, 96), cus) * (64 + 25 * up(nk, 3) / 2),       // over 3
+      up(tiles(64, 64), 2 * cus) * (64 + 10 * up(nk, 2)),       // over 2, two workgroups per CU
+      big ? INT64_MAX : t128 <= cus ? 82 + 17 * nk / 2 : up(t128, 2 * cus) * (82 + 11 * nk),   // two per CU
+      big || nk < 3 ? INT64_MAX : up(tiles(256, 128), cus) * (100 + 9 * nk),
       big ? INT64_MAX : up(tiles(256, 256), cus) * (171 + 14 * nk)};
   switch (std::min_element(us, us + 8) - us) {
     case 0: return launch_stream<1, 1, 8, 2, false>(p, stream);
