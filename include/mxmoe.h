@@ -429,7 +429,8 @@ int mx_add_rmsnorm(const void* x_bf16, int64_t ldx, const void* residual_bf16,
  * s uint8 [T, K/64, 2] are sent to their experts' rows as they are (xq, xs);
  * the maps, the group list, the workspace (moe_route_quant_workspace_size,
  * on an 8-byte boundary), the limits and the bounded waits are those of
- * moe_route_quant.  q needs 16-byte alignment; s any.
+ * moe_route_quant.  q needs 16-byte alignment; s any.  An output that overlaps
+ * an input, another output or the workspace is MX_ERR_INVALID_ARG.
  */
 int moe_route_mx(const void* q_u8, const void* s_u8, const int32_t* topk_ids,
                  int64_t T, int64_t K, int64_t k, int64_t E, void* xq_u8,
@@ -471,15 +472,15 @@ size_t mx_linear_fused_workspace_size(int64_t T, int64_t K, int64_t N, int x_is_
  * in fp32, rounded once: to bf16 (y), or along n to MXFP8 (yq, ys: the x of
  * the next linear, or the rows of moe_route_mx).
  *   x         uint8 [T, K] e4m3 with x_s uint8 [T, ceil(K/64), 2], or with a
- *             NULL x_s bf16 [T, K], quantised first (as mx_quantize) into
- *             the workspace
+ *             NULL x_s bf16 [T, K], quantised first (the bytes are those of
+ *             mx_quantize; few tokens need no workspace for it)
  *   w, w_s    uint8 [N, K], [N, ceil(K/64), 2]
  *   bias      [N] bf16 or fp32 (bias_type), or NULL
  *   residual  bf16 [T, N] or NULL
  *   y         bf16 [T, N], or yq uint8 [T, N] and ys uint8 [T, ceil(N/64), 2]
  *             (an odd count of scales padded with a zero byte)
  * y may be the residual itself (the same address); any other overlap of an
- * output with another buffer of the call is MX_ERR_INVALID_ARG.  Limits:
+ * output or of the workspace is MX_ERR_INVALID_ARG.  Limits:
  * K % 32 == 0, K <= 2^20; T and N as they are.  Alignment: MXFP8 payloads that
  * are read on 16-byte boundaries, their scales on 4, the workspace on 256.
  */

@@ -433,6 +433,9 @@ extern "C" int mx_linear_fused(const void* x, const void* x_s, const void* w_u8,
       if (overlaps(out[o], in[i]) && !(o == 0 && i == 6 && y_bf16 == residual_bf16))
         return fail(MX_ERR_INVALID_ARG, "mx_linear_fused: an output overlaps an input or the workspace");
   if (overlaps(out[1], out[2])) return fail(MX_ERR_INVALID_ARG, "mx_linear_fused: two outputs overlap");
+  for (int i = 0; i < 7; ++i)
+    if (i != 5 && overlaps(in[5], in[i]))
+      return fail(MX_ERR_INVALID_ARG, "mx_linear_fused: the workspace overlaps an input");
   hipStream_t s = as_stream(stream);
   if (mx_in) {
     p.x = static_cast<const uint8_t*>(x);

@@ -56,7 +56,7 @@
 
 #include <unistd.h>
 
-#include "common.h"
+#include "fused.h"
 
 namespace mxmoe {
 
@@ -799,6 +799,17 @@ extern "C" int moe_route_mx(const void* q_u8, const void* s_u8, const int32_t* t
   if (reinterpret_cast<uintptr_t>(q_u8) % 16 || reinterpret_cast<uintptr_t>(xq_u8) % 16 ||
       reinterpret_cast<uintptr_t>(workspace) % 8)
     return fail(MX_ERR_UNSUPPORTED, "moe_route_mx: q and xq must be 16-byte aligned, the workspace 8-byte");
+  // every row is read while others are being written: no output may lie over an input
+  const uint64_t M = (uint64_t)(T * k), s_bytes = 2 * (((uint64_t)K + 63) / 64);
+  const Span in[3] = {{q_u8, (uint64_t)T * (uint64_t)K}, {s_u8, (uint64_t)T * s_bytes}, {topk_ids, M * 4}};
+  const Span out[6] = {{xq_u8, M * (uint64_t)K}, {xs_u8, M * s_bytes}, {sorted_row, M * 4}, {expanded_row_idx, M * 4},
+                       {group_list, (uint64_t)E * 8}, {workspace, need}};
+  for (int o = 0; o < 6; ++o) {
+    for (int i = 0; i < 3; ++i)
+      if (overlaps(out[o], in[i])) return fail(MX_ERR_INVALID_ARG, "moe_route_mx: an output overlaps an input");
+    for (int i = o + 1; i < 6; ++i)
+      if (overlaps(out[o], out[i])) return fail(MX_ERR_INVALID_ARG, "moe_route_mx: two outputs overlap");
+  }
   return launch_route_mx(static_cast<const uint8_t*>(q_u8), static_cast<const uint8_t*>(s_u8), topk_ids, T, K, k, E,
                          static_cast<uint8_t*>(xq_u8), static_cast<uint8_t*>(xs_u8), sorted_row, expanded_row_idx,
                          group_list, workspace, as_stream(stream));

@@ -100,6 +100,9 @@ def test_linear_fused_overlap(lib):
     assert lin(lib, y=a((6 << 40) + 2)) == INVALID                         # y into the residual, shifted
     assert lin(lib, y=None, r=None, yq=at(0), ys=at(8)) == INVALID         # yq over x
     assert lin(lib, y=None, r=None, yq=at(7), ys=a((8 << 40) + 16)) == INVALID   # ys inside yq
+    # the workspace, where bf16 tokens are quantised to, over them or over the weights
+    for other in (dict(x=at(7)), dict(w=at(7)), dict(b=at(7)), dict(r=at(7)), dict(y=at(7))):
+        assert lin(lib, T=64, xs=None, wsp=at(7), wsb=1 << 20, **other) == INVALID, other
     assert "overlap" in mx.last_error()
 
 
@@ -112,6 +115,14 @@ def test_route_mx_and_forward_mx_validation(lib):
     assert route(64, 256, 2, 8, s=None) == INVALID
     assert route(64, 256, 2, 8, q=ctypes.c_void_p(0x1008)) == UNSUPPORTED
     assert route(300, 256, 2, 8, wsp=ctypes.c_void_p(0x1004)) == UNSUPPORTED
+
+    bufs = [at(i) for i in range(8)] + [at(9)]   # q s ids xq xs sorted_row expanded_row_idx group_list workspace
+    for i in range(9):
+        for o in range(max(i + 1, 3), 9):
+            b = list(bufs)
+            b[o] = b[i]
+            rc = lib.moe_route_mx(*b[:3], 300, 256, 2, 8, *b[3:], 1 << 30, None)
+            assert rc == INVALID and "overlap" in mx.last_error(), (i, o)
 
     def fwd(fmt, T, K, I, E, k, ws=1 << 40, s=at(1)):
         return lib.moe_mxfp8_forward_mx(at(0), s, at(2), at(3), fmt, at(4), at(5), at(6), at(7), T, K, I, E, k, at(8),

@@ -131,3 +131,37 @@ def test_two_streams_at_once():
                 got.append(block(x, r, d, k)[-1])
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("T", [4, 40, 300, 700])
+def test_rows_behind_a_batch(T):
+    """Rows of NaN and infinities behind a batch (a padded one's unwritten
+    rows) leave the other rows' bytes as they are, in every operator."""
+    K, N, E, k, pad = 512, 640, 16, 4, 37
+    rng = np.random.default_rng(T)
+    xb = to_bf16_bits(rng.standard_normal((T + pad, K)).astype(np.float32))
+    bad = xb.copy()
+    bad[T:] = rng.choice(np.array([0x7FC0, 0x7F80, 0xFF80, 0x3F80], np.uint16), (pad, K))
+    g = bf16_dev(to_bf16_bits(rng.standard_normal(K).astype(np.float32)))
+    wq, ws = mx.mx_quantize(bf16_dev(to_bf16_bits((0.05 * rng.standard_normal((N, K))).astype(np.float32))))
+    ids = u8_dev(rng.permuted(np.tile(np.arange(E), (T + pad, 1)), axis=1)[:, :k].copy()).int()
+    ids_bad = ids.clone()
+    ids_bad[T:] = -1   # no expert
+    say(f"rows behind a batch T={T}")
+    got = []
+    for bits, i in ((xb, ids), (bad, ids_bad)):
+        x = bf16_dev(bits)
+        q, s, h, y = mx.mx_add_rmsnorm(x, g, x, norm_out=True)
+        rows = [q, s, h, y, mx.mx_linear_fused(x, wq, ws, act="gelu", residual=x.repeat(1, 2)[:, :N].contiguous()),
+                mx.mx_linear_fused(q, wq, ws, x_s=s, act="silu"),
+                *mx.mx_linear_fused(q, wq, ws, x_s=s, quantize_out=True)]
+        payload = q.clone()
+        if bits is bad:
+            payload[T:] = 0x7F   # NaN
+        rows.append(mx.mx_linear_fused(payload, wq, ws, x_s=s))
+        xq, xs, _, eri, _ = mx.moe_route_mx(q, s, i, E)
+        at = eri[:T * k].long()
+        torch.cuda.synchronize()
+        assert int(at.min()) >= 0
+        got.append([r[:T] for r in rows] + [xq[at], xs[at]])
+    assert all(torch.equal(a, b) for a, b in zip(*got))
