@@ -316,3 +316,43 @@ def test_linear_fused_few_bf16_tokens(T, K, N, act):
     b = mx.mx_linear_fused(raw, u8_dev(wq[0]), u8_dev(wq[1]), act=act)
     torch.cuda.synchronize()
     assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("T,K,N", [(600000, 32, 4104), (300, 32768, 140000), (2, 32768, 140003), ((1 << 26) + 32, 64, 3)])
+def test_linear_fused_offsets_past_32_bits(T, K, N):
+    """The last rows and features of operands and outputs over 4 GiB, against
+    the same ones in a call of their own: sums of small integers, exact in
+    float32 in any order."""
+    say(f"mx_linear_fused past 32 bits T={T} K={K} N={N}")
+    gen = torch.Generator(device="cuda").manual_seed(T)
+    codes = torch.tensor([0, 0x38, 0xB8, 0x40, 0xC0], dtype=torch.uint8, device="cuda")   # 0, 1, -1, 2, -2
+
+    def rows(n):
+        q = torch.empty((n, K), dtype=torch.uint8, device="cuda")
+        step = max(1, (1 << 27) // K)
+        for i in range(0, n, step):
+            part = q[i:i + step]
+            part.copy_(codes[torch.randint(0, 5, part.shape, dtype=torch.int32, device="cuda", generator=gen)])
+        s = torch.full((n, -(-K // 64), 2), 127, dtype=torch.uint8, device="cuda")
+        if K % 64:
+            s[:, -1, 1] = 0
+        return q, s
+    x, xs = rows(T)
+    w, ws = rows(N)
+    t, n = min(T, 200), min(N, 192 + N % 32)
+    n0 = N - n
+    assert n0 % 32 == 0   # whole blocks of the MXFP8 output
+    res = torch.empty((T, N), dtype=torch.bfloat16, device="cuda")
+    for i in range(0, T, 1 << 14):
+        part = res[i:i + (1 << 14)]
+        part.copy_(torch.randint(-8, 9, part.shape, dtype=torch.int8, device="cuda", generator=gen))
+    y = mx.mx_linear_fused(x, w, ws, x_s=xs, residual=res)
+    part = mx.mx_linear_fused(x[-t:], w[n0:], ws[n0:], x_s=xs[-t:], residual=res[-t:, n0:].contiguous())
+    torch.cuda.synchronize()
+    assert torch.equal(y[-t:, n0:], part)
+    del res, y
+    yq, ys = mx.mx_linear_fused(x, w, ws, x_s=xs, act="relu", quantize_out=True)
+    pq, ps = mx.mx_linear_fused(x[-t:], w[n0:], ws[n0:], x_s=xs[-t:], act="relu", quantize_out=True)
+    torch.cuda.synchronize()
+    assert torch.equal(yq[-t:, n0:], pq) and torch.equal(ys[-t:].flatten(1)[:, n0 // 32:-(-N // 32)],
+                                                       ps.flatten(1)[:, :-(-n // 32)])
