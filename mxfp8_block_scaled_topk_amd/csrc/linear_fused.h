@@ -84,7 +84,8 @@ __device__ __forceinline__ float half_erfc(float x) {
 
 // The activation of n values (act is uniform over the launch).  The hardware
 // exp and reciprocal are good to about 1 ulp; every form below is a product
-// whose factors keep their relative accuracy over the whole range.
+// whose factors keep their relative accuracy until the exponential leaves the
+// normal floats (results below about 1e-36 become 0).
 template <int n>
 __device__ __forceinline__ void activate(float (&z)[n], int act) {
   switch (act) {
@@ -106,8 +107,9 @@ __device__ __forceinline__ void activate(float (&z)[n], int act) {
     case MX_ACT_GELU_TANH:   // (z / 2)(1 + tanh u) = z / (1 + e^-2u)
 #pragma unroll
       for (int i = 0; i < n; ++i) {
-        const float u2 = z[i] * fmaf(z[i] * z[i], 2.0f * 0.79788456080286536f * 0.044715f, 2.0f * 0.79788456080286536f);
-        z[i] *= __builtin_amdgcn_rcpf(1.0f + __expf(-u2));
+        constexpr float c = -2.0f * 0.79788456080286536f * 1.4426950408889634f;   // exponents of 2
+        const float u2 = z[i] * fmaf(z[i] * z[i], c * 0.044715f, c);
+        z[i] *= __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(u2));
       }
       break;
     default:
@@ -203,12 +205,13 @@ __device__ __forceinline__ void epilogue8(const LinParams& p, const Place& pl, i
         if (i < cnt) y[i] = static_cast<uint16_t>(w[i >> 1] >> (16 * (i & 1)));
     }
   } else {
+    if (cnt < 8) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) z[i] = i < cnt ? z[i] : 0.0f;
+    }
     float a = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      if (i >= cnt) z[i] = 0.0f;
-      a = fmaxf(a, fabsf(z[i]));
-    }
+    for (int i = 0; i < 8; ++i) a = fmaxf(a, fabsf(z[i]));
     a = quad_max(a);
     if (cnt <= 0) return;
     const uint32_t sb = e8m0_from_amax(a);
@@ -218,7 +221,7 @@ __device__ __forceinline__ void epilogue8(const LinParams& p, const Place& pl, i
     uint8_t* q = at(p.yq, pl.el, pl.lane_el);
     if (cnt >= 8) {
       const u32x2_any v = {o.x, o.y};
-      *reinterpret_cast<u32x2_any*>(q) = v;
+      __builtin_nontemporal_store(v, reinterpret_cast<u32x2_any*>(q));
     } else {
 #pragma unroll
       for (int i = 0; i < 7; ++i)

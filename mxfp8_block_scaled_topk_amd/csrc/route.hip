@@ -367,14 +367,15 @@ __global__ __launch_bounds__(kThreads) void route_quant_kernel(RouteParams p) {
   constexpr int kLd = 4;          // half-blocks whose loads a lane has in flight at once
   if constexpr (kMx) {
     // a payload row is hpr 16-byte pieces
+    typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));   // (an array of uint4 would go to scratch)
     for (int it0 = tid; it0 < n_it; it0 += kLd * kThreads) {
-      uint4 u[kLd];
+      u32x4 u[kLd];
 #pragma unroll
       for (int i = 0; i < kLd; ++i) {
         const int it = it0 + i * kThreads;
         if (it < n_it) {
           const int tl = it / hpr, hb = it - tl * hpr;
-          u[i] = *reinterpret_cast<const uint4*>(p.mxq + (t0 + tb + tl) * p.K + hb * 16);
+          u[i] = *reinterpret_cast<const u32x4*>(p.mxq + (t0 + tb + tl) * p.K + hb * 16);
         }
       }
 #pragma unroll
@@ -382,7 +383,7 @@ __global__ __launch_bounds__(kThreads) void route_quant_kernel(RouteParams p) {
         const int it = it0 + i * kThreads;
         if (it < n_it) {
           const int tl = it / hpr, hb = it - tl * hpr;
-          *reinterpret_cast<uint4*>(xbuf + tl * rowb + hb * 16) = u[i];
+          *reinterpret_cast<u32x4*>(xbuf + tl * rowb + hb * 16) = u[i];
         }
       }
     }
