@@ -13,16 +13,17 @@
 // tile's first stage is already in LDS.
 //
 // Three shapes, by how much of the card the tiles fill and what a stage costs:
-//   256 x 256, two slots    1.4 us a stage (3.0 PFLOP/s at full clock), the least
-//                           operand traffic; 8 waves, all 256 registers
+//   256 x 256, two slots    1.4 us a stage (3.0 PFLOP/s), the least operand
+//                           traffic; 8 waves, all 256 registers
 //   256 x 128, three slots  0.9 us a stage (2.4 PFLOP/s), half the epilogue
 //   128 x 128, two slots    two workgroups per CU, so that one's epilogue and
 //                           first loads run beside the other's products
 // Measured: T = 16384, K = N = 4096 with bias and residual 254 - 263 us, 2.1 -
 // 2.2 PFLOP/s (the same product in 256 x 256 tiles without a residual 235 us,
 // 2.34; the library's fp8 product without any epilogue 224 us).  What bounds it:
-// the matrix units while K runs (under load their clock falls), then the
-// residual and the output of all CUs in one burst per tile.  T = 2048, K = 2048,
+// operands arriving in LDS, 64 KB a stage at about 47 GB/s per CU (the matrix
+// units are busy half of the time, at 2.1 GHz), then the residual and the output
+// of all CUs in one burst per tile.  T = 2048, K = 2048,
 // N = 4096 to MXFP8 with gelu_tanh 27 us: 15 us of stages, the rest one tile's
 // launch, first loads and epilogue with nothing beside them.
 #include <algorithm>
@@ -429,7 +430,7 @@ __global__ __launch_bounds__(64 * WN * WM) void lin_tile_kernel(LinParams p, int
             float z[8] = {z0.x, z0.y, z0.z, z0.w, z1.x, z1.y, z1.z, z1.w};
             const Place pl{el_of(i), (t_w + 8 * i) * p.ys_stride + ((n_w + 64 * h) >> 5), lane_el, lane_s};
             epilogue8(p, pl, n, rr + 8 * i < t_left ? cnt : 0, b, res[i], z);
-            __builtin_amdgcn_sched_barrier(0);   // one row at a time
+            __builtin_amdgcn_sched_barrier(0);   // one row at a time (reading the next one ahead gains nothing)
           }
           asm volatile("" ::: "memory");
         }
