@@ -59,16 +59,21 @@ __device__ __forceinline__ int swz(int r, int c) { return r * kStageK + ((c ^ ((
 // token operand's are zeroed, so they add nothing; scale rows are then only
 // 2-byte aligned and come two bytes at a time.
 //
-// kX16: p.x is bf16 [T, K], T <= 32 and T K <= kMaxResident (host).  The tokens
+// XR: token rows a slot holds.  8 or 16 where no more tokens exist (T <= XR,
+// host): the lanes of the tokens beyond repeat them, and the ring is deeper (T =
+// 1, K = N = 4096: 6.3 -> 6.0 us; K = 8192, N = 512: 7.4 -> 6.5).
+//
+// XR = 0 (kX16): p.x is bf16 [T, K], T <= 32 and T K <= kMaxResident (host).  The tokens
 // stay in LDS as MXFP8 rows of nk stages, swizzled like a slot's, each row an
 // odd number of 128-byte stages long so that 16 rows' chunks hit distinct banks;
 // only the weights go through the rings.
 constexpr int kMaxResident = 65536;
 
-template <int NF, int MF, int WV, int S, bool kTail, bool kX16>
+template <int NF, int MF, int WV, int S, bool kTail, int XR>
 __global__ __launch_bounds__(64 * WV) void lin_stream_kernel(LinParams p) {
-  static_assert(!kX16 || MF == 1, "one fragment of resident tokens");
-  constexpr int kRows = 32 * (NF + (kX16 ? 0 : MF));   // LDS rows per slot: weights, then tokens
+  constexpr bool kX16 = XR == 0;
+  static_assert(XR == 32 * MF || (MF == 1 && (XR == 0 || XR == 8 || XR == 16)), "token rows per slot");
+  constexpr int kRows = 32 * NF + XR;   // LDS rows per slot: weights, then tokens
   constexpr int kScaleOps = (kRows + 63) / 64;       // 64 rows per scale load
   constexpr int kScaleBytes = kScaleOps * 256 * (kTail ? 2 : 1);
   constexpr int kSlot = kRows * kStageK + kScaleBytes;
@@ -107,7 +112,8 @@ __global__ __launch_bounds__(64 * WV) void lin_stream_kernel(LinParams p) {
   const uint8_t* sptr[kScaleOps];
 #pragma unroll
   for (int j = 0; j < kScaleOps; ++j) {
-    const int r = kX16 ? (64 * j + lane) & (32 * NF - 1) : 64 * j + lane;   // (a spare half repeats the weights')
+    // (lanes past the last row repeat others)
+    const int r = kX16 ? (64 * j + lane) & (32 * NF - 1) : 64 * j + lane;
     sptr[j] = r < 32 * NF ? p.ws + (n0 + std::min(r, n_last)) * p.s_stride
                           : p.xs + (t0 + std::min(r - 32 * NF, t_last)) * p.s_stride;
   }
@@ -238,8 +244,9 @@ __global__ __launch_bounds__(64 * WV) void lin_stream_kernel(LinParams p) {
           fb[s][m] = v8i{(int)u0.x, (int)u0.y, (int)u0.z, (int)u0.w, (int)u1.x, (int)u1.y, (int)u1.z, (int)u1.w};
           sb[s][m] = reinterpret_cast<const uint8_t*>(xsc)[(xrow * p.nk + ks) * 4 + 2 * s + lg];
         } else {
-          fb[s][m] = frag(32 * (NF + m) + li, s);
-          sb[s][m] = scale(32 * (NF + m) + li, s);
+          const int r = 32 * (NF + m) + (XR < 32 ? li & (XR - 1) : li);
+          fb[s][m] = frag(r, s);
+          sb[s][m] = scale(r, s);
         }
       }
     }
@@ -302,16 +309,16 @@ __global__ __launch_bounds__(64 * WV) void lin_stream_kernel(LinParams p) {
   }
 }
 
-template <int NF, int MF, int WV, int S, bool kX16>
+template <int NF, int MF, int WV, int S, int XR = 32 * MF>
 int launch_stream(LinParams p, hipStream_t stream) {
   p.n_tiles = (uint32_t)((p.N + 32 * NF - 1) / (32 * NF));
   p.t_tiles = (uint32_t)((p.T + 32 * MF - 1) / (32 * MF));
   const int64_t grid = (int64_t)p.n_tiles * p.t_tiles;
   if (grid * 64 * WV >= (int64_t)1 << 32) return fail(MX_ERR_UNSUPPORTED, "mx_linear_fused: too many tiles");
   if (p.K % kStageK)
-    lin_stream_kernel<NF, MF, WV, S, true, kX16><<<dim3((unsigned)grid), dim3(64 * WV), 0, stream>>>(p);
+    lin_stream_kernel<NF, MF, WV, S, true, XR><<<dim3((unsigned)grid), dim3(64 * WV), 0, stream>>>(p);
   else
-    lin_stream_kernel<NF, MF, WV, S, false, kX16><<<dim3((unsigned)grid), dim3(64 * WV), 0, stream>>>(p);
+    lin_stream_kernel<NF, MF, WV, S, false, XR><<<dim3((unsigned)grid), dim3(64 * WV), 0, stream>>>(p);
   return check_launch("mx_linear_fused");
 }
 
@@ -339,11 +346,14 @@ int launch_linear(const LinParams& p, hipStream_t stream) {
       big || nk < 3 ? INT64_MAX : up(tiles(256, 128), cus) * (100 + 9 * nk),
       big ? INT64_MAX : up(tiles(256, 256), cus) * (171 + 14 * nk)};
   switch (std::min_element(us, us + 8) - us) {
-    case 0: return launch_stream<1, 1, 8, 2, false>(p, stream);
-    case 1: return launch_stream<2, 1, 6, 2, false>(p, stream);
-    case 2: return launch_stream<2, 2, 4, 2, false>(p, stream);
-    case 3: return launch_stream<2, 3, 3, 2, false>(p, stream);
-    case 4: return launch_stream<2, 2, 2, 2, false>(p, stream);
+    case 0:
+      if (p.T <= 8) return launch_stream<1, 1, 8, 3, 8>(p, stream);
+      if (p.T <= 16) return launch_stream<1, 1, 8, 3, 16>(p, stream);
+      return launch_stream<1, 1, 8, 2>(p, stream);
+    case 1: return launch_stream<2, 1, 6, 2>(p, stream);
+    case 2: return launch_stream<2, 2, 4, 2>(p, stream);
+    case 3: return launch_stream<2, 3, 3, 2>(p, stream);
+    case 4: return launch_stream<2, 2, 2, 2>(p, stream);
     case 5: return launch_lin_tile128(p, stream);
     case 6: return launch_lin_tile256x128(p, stream);
     default: return launch_lin_tile256(p, stream);
@@ -456,7 +466,7 @@ extern "C" int mx_linear_fused(const void* x, const void* x_s, const void* w_u8,
     p.xs = static_cast<const uint8_t*>(x_s);
   } else if (resident(T, K)) {
     p.x = static_cast<const uint8_t*>(x);
-    return launch_stream<1, 1, 8, 2, true>(p, s);
+    return launch_stream<1, 1, 8, 2, 0>(p, s);
   } else {
     uint8_t* xq = static_cast<uint8_t*>(workspace);
     uint8_t* xs = xq + L.xs;
