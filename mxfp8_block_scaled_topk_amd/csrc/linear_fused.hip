@@ -360,7 +360,10 @@ int launch_linear(const LinParams& p, hipStream_t stream) {
   }
 }
 
-// bf16 tokens that every workgroup quantises for itself (no workspace).
+// bf16 tokens that every workgroup quantises for itself (no workspace).  One
+// launch in the place of two: 4 us of host work less.  On the GPU alone (K = N =
+// 2048; quantiser 2.3 us + product) 4.6 against 6.3 us at T = 1, 6.2 against 6.4
+// at T = 16, 8.3 against 6.8 at T = 32, where the workgroup's arithmetic shows.
 bool resident(int64_t T, int64_t K) { return T <= 32 && T * K <= kMaxResident; }
 
 // Workspace: the MXFP8 form of bf16 tokens.
