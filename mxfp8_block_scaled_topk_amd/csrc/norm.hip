@@ -182,7 +182,10 @@ __device__ __forceinline__ float row_sum(float x, float* part) {
 }
 
 __device__ __forceinline__ float rstd_of(float sum, const NormParams& p) {
-  return rsqrtf(sum / static_cast<float>(p.K) + p.eps);
+  // the hardware's root is good to 1 ulp; a Newton step takes it to about half
+  const float m = sum / static_cast<float>(p.K) + p.eps;
+  const float r = rsqrtf(m);
+  return r > 0.0f ? fmaf(0.5f * r, fmaf(-m * r, r, 1.0f), r) : r;   // (a mean square past fp32 gives 0)
 }
 
 // W waves per row (kR = max(1, 4 / W) rows per workgroup), C chunks per lane.
