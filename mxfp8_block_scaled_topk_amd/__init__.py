@@ -588,14 +588,13 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
 _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
+_Tensor, _U8, _BF16, _F32 = torch.Tensor, torch.uint8, torch.bfloat16, torch.float32   # (quicker names)
+
+
 def _need_like(t, shape, name, dtype, device):
     """_need_shape, quick for a right tensor."""
-    try:
-        if t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.device == device:
-            return
-    except AttributeError:
-        pass
-    _need_shape(t, shape, name, dtype, device)
+    if not (type(t) is _Tensor and t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.device == device):
+        _need_shape(t, shape, name, dtype, device)
 
 
 def _elsewhere(device, stream):
@@ -637,7 +636,8 @@ def mx_add_rmsnorm(x, weight, residual=None, eps=1e-6, quantize=True, norm_out=F
     residual) and bf16(n) (None without ``norm_out``).  ``out`` gives the four
     buffers instead, None for an output that is not wanted; its residual_out
     or y may be x or residual itself."""
-    _need(x, torch.bfloat16, "x")
+    if type(x) is not _Tensor or x.dtype is not _BF16:
+        _need(x, _BF16, "x")
     shape, dev = x.shape, x.device
     if not shape or shape[-1] == 0:
         raise ValueError("x must have at least one element per row")
@@ -645,35 +645,36 @@ def mx_add_rmsnorm(x, weight, residual=None, eps=1e-6, quantize=True, norm_out=F
     x2, ldx = _rows(x, "x")
     r2, ldr = None, 0
     if residual is not None:
-        _need(residual, torch.bfloat16, "residual")
+        if type(residual) is not _Tensor or residual.dtype is not _BF16:
+            _need(residual, _BF16, "residual")
         if residual.shape != shape:
             raise ValueError(f"residual must have shape {tuple(shape)}, got {tuple(residual.shape)}")
         if residual.device != dev:
             raise ValueError(f"residual must be on {dev}, got {residual.device}")
         r2, ldr = _rows(residual, "residual")
-    wtype = TYPE_F32 if isinstance(weight, torch.Tensor) and weight.dtype is torch.float32 else TYPE_BF16
-    _need_like(weight, (K,), "weight", torch.float32 if wtype else torch.bfloat16, dev)
-    s_shape = shape[:-1] + (_pairs(K), 2)
+    wtype = TYPE_F32 if isinstance(weight, _Tensor) and weight.dtype is _F32 else TYPE_BF16
+    _need_like(weight, (K,), "weight", _F32 if wtype else _BF16, dev)
+    s_shape = (*shape[:-1], -(-K // 64), 2)
     if out is not None:
         q, s, r_out, y = out
         if q is not None:
-            _need_like(q, shape, "q", torch.uint8, dev)
+            _need_like(q, shape, "q", _U8, dev)
         if s is not None:
-            _need_like(s, s_shape, "s", torch.uint8, dev)
+            _need_like(s, s_shape, "s", _U8, dev)
         if r_out is not None:
-            _need_like(r_out, shape, "residual_out", torch.bfloat16, dev)
+            _need_like(r_out, shape, "residual_out", _BF16, dev)
         if y is not None:
-            _need_like(y, shape, "y", torch.bfloat16, dev)
+            _need_like(y, shape, "y", _BF16, dev)
     _need_gpu(x, "x")
     there = _elsewhere(dev, stream)
     if there is not None:
         with there:
             return mx_add_rmsnorm(x, weight, residual, eps, quantize, norm_out, out)
     if out is None:
-        q = torch.empty(shape, dtype=torch.uint8, device=dev) if quantize else None
-        s = torch.empty(s_shape, dtype=torch.uint8, device=dev) if quantize else None
-        r_out = torch.empty(shape, dtype=torch.bfloat16, device=dev) if residual is not None else None
-        y = torch.empty(shape, dtype=torch.bfloat16, device=dev) if norm_out else None
+        q = torch.empty(shape, dtype=_U8, device=dev) if quantize else None
+        s = torch.empty(s_shape, dtype=_U8, device=dev) if quantize else None
+        r_out = torch.empty(shape, dtype=_BF16, device=dev) if residual is not None else None
+        y = torch.empty(shape, dtype=_BF16, device=dev) if norm_out else None
     rc = load().mx_add_rmsnorm(x2.data_ptr(), ldx, _addr(r2), ldr, weight.data_ptr(), wtype, eps, x2.shape[0], K,
                                _addr(r_out), _addr(y), _addr(q), _addr(s), _raw_stream(dev.index))
     if rc:
@@ -685,19 +686,22 @@ def moe_route_mx(q, s, topk_ids, E, out=None, workspace=None, stream=None):
     """moe_route_quant for rows that are MXFP8 already: q uint8 [T, K] and
     s uint8 [T, K/64, 2] (as mx_add_rmsnorm or mx_quantize make them).
     Returns (xq, xs, sorted_row, expanded_row_idx, group_list)."""
-    _need(q, torch.uint8, "q", 2); _need(topk_ids, torch.int32, "topk_ids", 2)
+    _need(q, _U8, "q", 2)
+    if type(topk_ids) is not _Tensor or topk_ids.dim() != 2:
+        _need(topk_ids, torch.int32, "topk_ids", 2)
     T, K = q.shape
     k = topk_ids.shape[1]
     M = T * k
     dev = q.device
     P = _pairs(K)
-    _need_like(q, (T, K), "q", torch.uint8, dev)
-    _need_like(s, (T, P, 2), "s", torch.uint8, dev)
+    if not q.is_contiguous():
+        raise ValueError("q must be contiguous")
+    _need_like(s, (T, P, 2), "s", _U8, dev)
     _need_like(topk_ids, (T, k), "topk_ids", torch.int32, dev)
     if out is not None:
         xq, xs, sr, eri, gl = out
-        _need_like(xq, (M, K), "xq", torch.uint8, dev)
-        _need_like(xs, (M, P, 2), "xs", torch.uint8, dev)
+        _need_like(xq, (M, K), "xq", _U8, dev)
+        _need_like(xs, (M, P, 2), "xs", _U8, dev)
         _need_like(sr, (M,), "sorted_row", torch.int32, dev)
         _need_like(eri, (M,), "expanded_row_idx", torch.int32, dev)
         _need_like(gl, (E,), "group_list", torch.int64, dev)
@@ -711,13 +715,13 @@ def moe_route_mx(q, s, topk_ids, E, out=None, workspace=None, stream=None):
         with there:
             return moe_route_mx(q, s, topk_ids, E, out, workspace)
     if out is None:
-        xq = torch.empty((M, K), dtype=torch.uint8, device=dev)
-        xs = torch.empty((M, P, 2), dtype=torch.uint8, device=dev)
+        xq = torch.empty((M, K), dtype=_U8, device=dev)
+        xs = torch.empty((M, P, 2), dtype=_U8, device=dev)
         sr = torch.empty(M, dtype=torch.int32, device=dev)
         eri = torch.empty(M, dtype=torch.int32, device=dev)
         gl = torch.empty(E, dtype=torch.int64, device=dev)
     if workspace is None and need:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        workspace = torch.empty(need, dtype=_U8, device=dev)
     rc = lib.moe_route_mx(q.data_ptr(), s.data_ptr(), topk_ids.data_ptr(), T, K, k, E, xq.data_ptr(), xs.data_ptr(),
                           sr.data_ptr(), eri.data_ptr(), gl.data_ptr(), _addr(workspace),
                           0 if workspace is None else workspace.numel(), _raw_stream(dev.index))
@@ -799,35 +803,38 @@ def mx_linear_fused(x, w, w_s, x_s=None, bias=None, act="none", residual=None, q
     ys uint8 [T, ceil(N/64), 2]).  ``out`` gives that tensor or pair instead
     (y may be the residual)."""
     mx_in = x_s is not None
-    _need(x, torch.uint8 if mx_in else torch.bfloat16, "x", 2); _need(w, torch.uint8, "w", 2)
+    _need(x, _U8 if mx_in else _BF16, "x", 2)
+    if type(w) is not _Tensor or w.dim() != 2:
+        _need(w, _U8, "w", 2)
     T, K = x.shape
     N = w.shape[0]
     dev = x.device
-    _need_like(x, (T, K), "x", x.dtype, dev)
+    if not x.is_contiguous():
+        raise ValueError("x must be contiguous")
     if mx_in:
-        _need_like(x_s, (T, _pairs(K), 2), "x_s", torch.uint8, dev)
-    _need_like(w, (N, K), "w", torch.uint8, dev)
-    _need_like(w_s, (N, _pairs(K), 2), "w_s", torch.uint8, dev)
+        _need_like(x_s, (T, _pairs(K), 2), "x_s", _U8, dev)
+    _need_like(w, (N, K), "w", _U8, dev)
+    _need_like(w_s, (N, _pairs(K), 2), "w_s", _U8, dev)
     btype = TYPE_BF16
     if bias is not None:
-        if isinstance(bias, torch.Tensor) and bias.dtype is torch.float32:
+        if isinstance(bias, _Tensor) and bias.dtype is _F32:
             btype = TYPE_F32
-        _need_like(bias, (N,), "bias", torch.float32 if btype else torch.bfloat16, dev)
+        _need_like(bias, (N,), "bias", _F32 if btype else _BF16, dev)
     if act not in ACTIVATIONS:
         raise ValueError(f"act must be one of {', '.join(ACTIVATIONS)}, got {act!r}")
     if residual is not None:
-        _need_like(residual, (T, N), "residual", torch.bfloat16, dev)
+        _need_like(residual, (T, N), "residual", _BF16, dev)
     if out is not None:
         quantize_out = isinstance(out, (tuple, list))
     y = yq = ys = None
     if quantize_out:
         yq, ys = out if out is not None else (None, None)
         if out is not None:
-            _need_like(yq, (T, N), "yq", torch.uint8, dev)
-            _need_like(ys, (T, _pairs(N), 2), "ys", torch.uint8, dev)
+            _need_like(yq, (T, N), "yq", _U8, dev)
+            _need_like(ys, (T, _pairs(N), 2), "ys", _U8, dev)
     elif out is not None:
         y = out
-        _need_like(y, (T, N), "out", torch.bfloat16, dev)
+        _need_like(y, (T, N), "out", _BF16, dev)
     lib = load()
     need = 0 if mx_in else lib.mx_linear_fused_workspace_size(T, K, N, 0)
     if workspace is not None:
@@ -838,13 +845,13 @@ def mx_linear_fused(x, w, w_s, x_s=None, bias=None, act="none", residual=None, q
         with there:
             return mx_linear_fused(x, w, w_s, x_s, bias, act, residual, quantize_out, out, workspace)
     if workspace is None and need:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        workspace = torch.empty(need, dtype=_U8, device=dev)
     if out is None:
         if quantize_out:
-            yq = torch.empty((T, N), dtype=torch.uint8, device=dev)
-            ys = torch.empty((T, _pairs(N), 2), dtype=torch.uint8, device=dev)
+            yq = torch.empty((T, N), dtype=_U8, device=dev)
+            ys = torch.empty((T, _pairs(N), 2), dtype=_U8, device=dev)
         else:
-            y = torch.empty((T, N), dtype=torch.bfloat16, device=dev)
+            y = torch.empty((T, N), dtype=_BF16, device=dev)
     rc = lib.mx_linear_fused(x.data_ptr(), _addr(x_s), w.data_ptr(), w_s.data_ptr(), _addr(bias), btype,
                              ACTIVATIONS[act], _addr(residual), T, K, N, _addr(y), _addr(yq), _addr(ys),
                              _addr(workspace), 0 if workspace is None else workspace.numel(),

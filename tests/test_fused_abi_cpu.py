@@ -153,6 +153,9 @@ def test_binding_norm_checks(lib):
     _raises(lambda: mx.mx_add_rmsnorm(x, w.double()), "weight must be torch.bfloat16")
     _raises(lambda: mx.mx_add_rmsnorm(x, _bf(99)), "weight must have shape")
     _raises(lambda: mx.mx_add_rmsnorm(x, None), "weight must be a torch.Tensor")
+    _raises(lambda: mx.mx_add_rmsnorm(None, w), "x must be a torch.Tensor")
+    _raises(lambda: mx.mx_add_rmsnorm(x, w, x.float()), "residual must be torch.bfloat16")
+    _raises(lambda: mx.mx_add_rmsnorm(torch.nn.Parameter(x), torch.nn.Parameter(w)), "on the GPU")   # as tensors
     _raises(lambda: mx.mx_add_rmsnorm(x, w, _bf(4, 99)), "residual must have shape")
     _raises(lambda: mx.mx_add_rmsnorm(_bf(100, 4).t(), w), "unit stride")
     _raises(lambda: mx.mx_add_rmsnorm(_bf(1, 100).expand(4, 100), w), "repeat its rows")
@@ -177,6 +180,10 @@ def test_binding_linear_fused_checks(lib):
     _raises(lambda: mx.mx_linear_fused(x, w, ws, out=_bf(10, 32)), "out must have shape")
     _raises(lambda: mx.mx_linear_fused(x, w, ws, out=(_u8(10, 33), _u8(10, 2, 2))), "ys must have shape")
     _raises(lambda: mx.mx_linear_fused(_bf(96, 10).t(), w, ws), "x must be contiguous")
+    _raises(lambda: mx.mx_linear_fused(x, w[0], ws), "w must have 2 dims")
+    _raises(lambda: mx.mx_linear_fused(x, None, ws), "w must be a torch.Tensor")
+    _raises(lambda: mx.mx_linear_fused(x, w.int(), ws), "w must be torch.uint8")
+    _raises(lambda: mx.mx_linear_fused(x, torch.nn.Parameter(w, requires_grad=False), ws), "on the GPU")   # as a tensor
     _raises(lambda: mx.mx_linear_fused(_bf(100, 96), w, ws, workspace=_u8(16)), "workspace has 16 bytes")
 
 
@@ -186,6 +193,9 @@ def test_binding_route_mx_and_forward_mx_checks(lib):
     _raises(lambda: mx.moe_route_mx(q, _u8(8, 3, 2), ids, 4), "s must have shape")
     _raises(lambda: mx.moe_route_mx(q, s, ids[:7], 4), "topk_ids must have shape")
     _raises(lambda: mx.moe_route_mx(q, s, ids.long(), 4), "topk_ids must be torch.int32")
+    _raises(lambda: mx.moe_route_mx(q, s, ids[0], 4), "topk_ids must have 2 dims")
+    _raises(lambda: mx.moe_route_mx(q, s, None, 4), "topk_ids must be a torch.Tensor")
+    _raises(lambda: mx.moe_route_mx(_u8(256, 8).t(), s, ids, 4), "q must be contiguous")
     E, I = 4, 128
     args = (q, s, ids, torch.zeros(8, 2), _u8(E, 2 * I, 256), _u8(E, 2 * I, 4, 2), _u8(E, 256, I), _u8(E, 256, 2, 2))
     _raises(lambda: mx.moe_mxfp8_forward_mx(*args), "on the GPU")
