@@ -30,9 +30,9 @@
 //
 // Bounded by what a CU can take in, about 60 GB/s (26 bytes a cycle) of weights
 // and tokens together, behind 3 us of launch and first loads: T = 32, K = N =
-// 4096 takes 7.3 us (17 MB of weights at 2.3 TB/s); T = 1, K = N = 2048 from bf16
-// 4.6 us.  The tile is a choice between re-reading the tokens (few rows) and few
-// workgroups (many rows).
+// 4096 takes 7.0 us (17 MB of weights at 2.4 TB/s), T = 1 5.7 us; K = N = 8192 at T =
+// 1 12.3 us (67 MB, 5.5 TB/s); T = 1, K = N = 2048 from bf16 4.6 us.  The tile is a
+// choice between re-reading the tokens (few rows) and few workgroups (many rows).
 #include <algorithm>
 
 #include "linear_fused.h"
@@ -61,7 +61,7 @@ __device__ __forceinline__ int swz(int r, int c) { return r * kStageK + ((c ^ ((
 //
 // XR: token rows a slot holds.  8 or 16 where no more tokens exist (T <= XR,
 // host): the lanes of the tokens beyond repeat them, and the ring is deeper (T =
-// 1, K = N = 4096: 6.3 -> 6.0 us; K = 8192, N = 512: 7.4 -> 6.5).
+// 1, K = N = 4096: 6.1 -> 5.7 us; K = 8192, N = 512: 7.6 -> 7.1).
 //
 // XR = 0 (kX16): p.x is bf16 [T, K], T <= 32 and T K <= kMaxResident (host).  The tokens
 // stay in LDS as MXFP8 rows of nk stages, swizzled like a slot's, each row an
@@ -326,36 +326,36 @@ int launch_stream(LinParams p, hipStream_t stream) {
 // measured times says is shortest.  Its tiles go over the CUs in rounds; a round
 // costs a part per tile and a part per k stage of a wave.  Fitted to all kernels
 // on 220 shapes (T to 16384, K and N to 8192, drawn over their logarithms), the
-// rule's choice takes 0.3 % longer than the fastest on average, 30 % at worst.
-// The smaller kernels differ only in how the tiles fill the rounds (32 x 32, 64 x
-// 64 and the tile kernels alone: 5 % longer on average, up to 46 %): T = 203, K =
-// 2080, N = 4099 takes 19.3 us in 260 tiles of 64 x 64, 14.8 us in 455 of 64 x 32.
+// rule's choice takes 0.3 % longer than the fastest on average, 13 % at worst.
+// The smaller kernels differ only in how the tiles fill the rounds: T = 203, K =
+// 2080, N = 4099 takes 19.3 us in 260 tiles of 64 x 64, 13.7 us in 903 of 32 x
+// 32.  (Also measured: 32 x 32 over 8 waves, one per CU, and 64 x 32 over 6 or
+// 3; they win by 0.5 % on average.)
 int launch_linear(const LinParams& p, hipStream_t stream) {
   const int64_t cus = num_cus(), nk = p.nk;
   auto tiles = [&](int64_t bn, int64_t bm) { return ((p.N + bn - 1) / bn) * ((p.T + bm - 1) / bm); };
   auto up = [](int64_t n, int64_t d) { return (n + d - 1) / d; };
-  const int64_t t128 = tiles(128, 128);
+  const int64_t t32 = tiles(32, 32), t128 = tiles(128, 128);
   const bool big = p.N >= (int64_t)1 << 27;   // the tile kernels' 32-bit offsets within 8 rows
-  const int64_t us[8] = {
-      up(tiles(32, 32), cus) * (32 + 17 * up(nk, 8) / 2),       // K over 8 waves
-      up(tiles(64, 32), cus) * (34 + 11 * up(nk, 6)),           // over 6
+  const int64_t us[7] = {
+      // K over 4 waves, two workgroups per CU
+      t32 <= cus ? 35 + 5 * up(nk, 4) : up(t32, 2 * cus) * (33 + 7 * up(nk, 4)),
       up(tiles(64, 64), cus) * (44 + 11 * up(nk, 4)),           // over 4
       up(tiles(64, 96), cus) * (64 + 25 * up(nk, 3) / 2),       // over 3
       up(tiles(64, 64), 2 * cus) * (64 + 10 * up(nk, 2)),       // over 2, two workgroups per CU
       big ? INT64_MAX : t128 <= cus ? 82 + 17 * nk / 2 : up(t128, 2 * cus) * (82 + 11 * nk),   // two per CU
       big || nk < 3 ? INT64_MAX : up(tiles(256, 128), cus) * (100 + 9 * nk),
-      big ? INT64_MAX : up(tiles(256, 256), cus) * (171 + 14 * nk)};
-  switch (std::min_element(us, us + 8) - us) {
+      big ? INT64_MAX : up(tiles(256, 256), cus) * (174 + 14 * nk)};
+  switch (std::min_element(us, us + 7) - us) {
     case 0:
-      if (p.T <= 8) return launch_stream<1, 1, 8, 3, 8>(p, stream);
-      if (p.T <= 16) return launch_stream<1, 1, 8, 3, 16>(p, stream);
-      return launch_stream<1, 1, 8, 2>(p, stream);
-    case 1: return launch_stream<2, 1, 6, 2>(p, stream);
-    case 2: return launch_stream<2, 2, 4, 2>(p, stream);
-    case 3: return launch_stream<2, 3, 3, 2>(p, stream);
-    case 4: return launch_stream<2, 2, 2, 2>(p, stream);
-    case 5: return launch_lin_tile128(p, stream);
-    case 6: return launch_lin_tile256x128(p, stream);
+      if (p.T <= 8) return launch_stream<1, 1, 4, 3, 8>(p, stream);
+      if (p.T <= 16) return launch_stream<1, 1, 4, 3, 16>(p, stream);
+      return launch_stream<1, 1, 4, 2>(p, stream);
+    case 1: return launch_stream<2, 2, 4, 2>(p, stream);
+    case 2: return launch_stream<2, 3, 3, 2>(p, stream);
+    case 3: return launch_stream<2, 2, 2, 2>(p, stream);
+    case 4: return launch_lin_tile128(p, stream);
+    case 5: return launch_lin_tile256x128(p, stream);
     default: return launch_lin_tile256(p, stream);
   }
 }

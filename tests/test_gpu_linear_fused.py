@@ -128,12 +128,15 @@ def test_linear_fused(i):
                  residual=c % 4 < 2, mx_out=j == 1, what=f"case {c}")
 
 
-# two sizes, one with an incomplete last k stage, for each tile shape that only
-# wide outputs reach: weight rows x tokens
+# two sizes or more, with an incomplete last k stage and without, for each tile
+# shape that only wide outputs reach (weight rows x tokens), and for 32 x 32
+# tiles over more than one round
 WIDE = [
-    (45, 96, 4225), (128, 640, 4096),        # 64 x 32
+    (45, 96, 4225), (128, 640, 4096),        # 32 x 32
+    (7, 160, 8300), (13, 512, 9000),         # 32 x 32, few tokens
+    (131, 992, 5505), (129, 896, 5633),      # 32 x 32, two rounds
     (100, 1056, 4099), (150, 512, 5440),     # 64 x 64
-    (131, 992, 5505), (129, 896, 5633),      # 64 x 96
+    (161, 1056, 5700), (288, 640, 5400),     # 64 x 96
     (199, 160, 4130), (330, 384, 4810),      # 64 x 64, two workgroups per CU
     (450, 416, 4100), (600, 768, 4500),      # 128 x 128
     (1030, 1696, 4099), (1030, 1664, 4096),  # 256 x 128
