@@ -141,13 +141,20 @@ __device__ __forceinline__ uint32_t lds_addr(const void* p) {
 }
 
 // 64 lanes x 16 B from global (uniform base + per-lane 32-bit offset) to LDS
-// [m0, m0 + 1024).
+// [m0, m0 + 1024).  A load needs one wait state after a write of m0 and five
+// after a vector instruction's write of its scalar base (v_readlane of a spilled
+// one).  The compiler keeps them for its own loads but does not see one inside
+// inline assembly, and the hardware does not check these two.  The move of the
+// base to itself stands for both: it is a wait state for m0, and the hardware
+// does hold a scalar instruction until a vector one's scalar result is there,
+// and a load until a scalar one's is.  It costs nothing; s_nop 4 in its place
+// takes the dense linear from 262 to 266 us (T = 16384, K = N = 4096).
 __device__ __forceinline__ void dma16(uint32_t voff, const void* sbase, uint32_t lds) {
-  asm volatile("global_load_lds_dwordx4 %0, %1" ::"v"(voff), "s"(sbase), "{m0}"(lds) : "memory");
+  asm volatile("s_mov_b64 %1, %1\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(voff), "s"(sbase), "{m0}"(lds) : "memory");
 }
 // 64 lanes x 4 B to LDS [m0, m0 + 256).
 __device__ __forceinline__ void dma4(uint32_t voff, const void* sbase, uint32_t lds) {
-  asm volatile("global_load_lds_dword %0, %1" ::"v"(voff), "s"(sbase), "{m0}"(lds) : "memory");
+  asm volatile("s_mov_b64 %1, %1\n\tglobal_load_lds_dword %0, %1" ::"v"(voff), "s"(sbase), "{m0}"(lds) : "memory");
 }
 __device__ __forceinline__ void wait_vmcnt0() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 // s_waitcnt vmcnt(n) for a wave-uniform n (vmcnt(0) above 7): every VMEM
