@@ -416,8 +416,7 @@ typedef enum mx_type { MX_TYPE_BF16 = 0, MX_TYPE_F32 = 1 } mx_type;
  * rows); any other overlap of an output is MX_ERR_INVALID_ARG.  eps is a
  * positive normal float.  Any kd from 1 to 2^24 and any alignment of whole
  * elements (rows of a multiple of 8 elements on 16-byte boundaries, q on 8,
- * take the fast path).  A row's mean square has to stay within fp32 (|h|
- * below about 1e18).
+ * take the fast path).  h has to be finite in fp32; a row's squares need not.
  */
 int mx_add_rmsnorm(const void* x_bf16, int64_t ldx, const void* residual_bf16,
                    int64_t ldr, const void* weight, int weight_type, float eps,

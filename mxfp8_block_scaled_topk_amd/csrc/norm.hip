@@ -17,8 +17,8 @@
 // (LDS).  Rows longer than 32768 (16384 when they are not aligned) are read twice
 // (add_rmsnorm_long).
 // HBM-bound: 2 bytes per element in (4 with a residual), 1 + 1/32 out (2 more
-// for each of residual_out and y).  16384 x 2048 with all of them takes 62 us,
-// 303 MB at 4.9 TB/s (a copy of 256 MB: 5.5); 1031 x 4304 6.6 us; one row of 2048
+// for each of residual_out and y).  16384 x 2048 with all of them takes 58 us,
+// 303 MB at 5.2 TB/s (a copy of 256 MB: 5.5); 1031 x 4304 6.8 us; one row of 2048
 // 2.7 us, of which the launch is 1.7.
 #include <algorithm>
 #include <cfloat>
@@ -130,7 +130,7 @@ __device__ __forceinline__ void store_bf16x8(uint16_t* p, int n, const float (&v
     store_part(reinterpret_cast<uint8_t*>(p), (uint64_t)u.y << 32 | u.x, (uint64_t)u.w << 32 | u.z, 2 * n);
 }
 
-// The outputs of 8 elements e .. of row r from h and rstd (n of them exist;
+// y, q and s of 8 elements e .. of row r from h and rstd (n of them exist;
 // lanes with n <= 0 only take part in the quad's exchange).
 template <bool kVec>
 __device__ __forceinline__ void emit8(const NormParams& p, int64_t r, int64_t e, int n, const float (&h)[8],
@@ -142,7 +142,6 @@ __device__ __forceinline__ void emit8(const NormParams& p, int64_t r, int64_t e,
     v[i] = h[i] * rstd * w[i];
     amax = fmaxf(amax, fabsf(v[i]));
   }
-  if (p.res_out && n > 0) store_bf16x8<kVec>(p.res_out + r * p.K + e, n, h);
   if (p.y && n > 0) store_bf16x8<kVec>(p.y + r * p.K + e, n, v);
   if (!p.q) return;
   amax = quad_max(amax);
@@ -181,11 +180,39 @@ __device__ __forceinline__ float row_sum(float x, float* part) {
   return x;
 }
 
-__device__ __forceinline__ float rstd_of(float sum, const NormParams& p) {
-  // the hardware's root is good to 1 ulp; a Newton step takes it to about half
-  const float m = sum / static_cast<float>(p.K) + p.eps;
+// 1 / sqrt(m).  The hardware's root is good to 1 ulp; a Newton step takes it to
+// about half.
+__device__ __forceinline__ float recip_root(float m) {
   const float r = rsqrtf(m);
-  return r > 0.0f ? fmaf(0.5f * r, fmaf(-m * r, r, 1.0f), r) : r;   // (a mean square past fp32 gives 0)
+  return r > 0.0f ? fmaf(0.5f * r, fmaf(-m * r, r, 1.0f), r) : r;   // (an infinite element gives 0)
+}
+
+// Squares of a row can add up past fp32 (elements over 1.8e19 / sqrt K).  The row
+// then comes again, scaled by kFar: its sum of squares lies between 2^-64 and
+// 2^89, and elements whose scaled square underflows are below 2^-85 of it.  The
+// branch is taken by whole rows; residual_out is stored ahead of it (behind it,
+// one row of 2048 takes 2.8 us instead of 2.7 and 16384 x 2048 62 instead of 58).
+constexpr float kFar = 0x1p-96f;
+
+// sum: of the row's squares, the same in all lanes that share it; sum_far(): of
+// those of the row times kFar
+template <class F>
+__device__ __forceinline__ float rstd_of(float sum, const NormParams& p, F sum_far) {
+  const float k = static_cast<float>(p.K);
+  if (__builtin_expect(__builtin_amdgcn_readfirstlane(__float_as_int(sum)) == 0x7f800000, 0))   // infinity
+    return recip_root(sum_far() / k + p.eps * kFar * kFar) * kFar;
+  return recip_root(sum / k + p.eps);
+}
+
+// Sum of the squares of 8 elements times k.
+__device__ __forceinline__ float squares8(const float (&h)[8], float k) {
+  float t[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float a = h[2 * i] * k, b = h[2 * i + 1] * k;
+    t[i] = a * a + b * b;
+  }
+  return (t[0] + t[1]) + (t[2] + t[3]);
 }
 
 // W waves per row (kR = max(1, 4 / W) rows per workgroup), C chunks per lane.
@@ -199,7 +226,6 @@ __global__ __launch_bounds__(64 * (W < 4 ? 4 : W)) void add_rmsnorm_kernel(NormP
   const int64_t first = (int64_t)blockIdx.x * kRows + (W == 1 ? threadIdx.x >> 6 : 0);
   for (int64_t r = first; r < p.rows; r += (int64_t)gridDim.x * kRows) {
     float h[C][8];
-    float sum = 0.0f;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
       const int64_t e = 8 * (int64_t)(64 * W * c + lane);
@@ -224,13 +250,13 @@ __global__ __launch_bounds__(64 * (W < 4 ? 4 : W)) void add_rmsnorm_kernel(NormP
         }
       }
     }
+    auto row_squares = [&](float k) __attribute__((always_inline)) {
+      float sum = 0.0f;
 #pragma unroll
-    for (int c = 0; c < C; ++c) {
-      float t[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) t[i] = h[c][2 * i] * h[c][2 * i] + h[c][2 * i + 1] * h[c][2 * i + 1];
-      sum += (t[0] + t[1]) + (t[2] + t[3]);
-    }
+      for (int c = 0; c < C; ++c) sum += squares8(h[c], k);
+      return sum;
+    };
+    const float sum = row_squares(1.0f);
     // the weight: with few chunks per lane (few or short rows, where latency
     // counts) requested before the sum's exchange
     constexpr bool kEarly = C <= 2;
@@ -244,7 +270,19 @@ __global__ __launch_bounds__(64 * (W < 4 ? 4 : W)) void add_rmsnorm_kernel(NormP
 #pragma unroll
       for (int c = 0; c < C; ++c) load_w(c, w[c]);
     }
-    const float rstd = rstd_of(row_sum<W>(sum, part), p);
+    const float total = row_sum<W>(sum, part);
+    // ahead of the root and its branch
+    if (p.res_out) {
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        const int64_t e = 8 * (int64_t)(64 * W * c + lane);
+        const int n = static_cast<int>(std::min<int64_t>(p.K - e, 8));
+        if (n > 0) store_bf16x8<kVec>(p.res_out + r * p.K + e, n, h[c]);
+      }
+    }
+    const float rstd = rstd_of(total, p, [&]() __attribute__((always_inline)) {
+      return row_sum<W>(row_squares(kFar), part);
+    });
 #pragma unroll
     for (int c = 0; c < C; ++c) {
       const int64_t e = 8 * (int64_t)(64 * W * c + lane);
@@ -278,24 +316,27 @@ __global__ __launch_bounds__(64 * kLongWaves) void add_rmsnorm_long(NormParams p
         for (int i = 0; i < 8; ++i) h[i] += a[i];
       }
     };
-    float sum = 0.0f;
-    for (int64_t k = 0; k < steps; ++k) {
-      const int64_t e = k * kStep + 8 * (int64_t)threadIdx.x;
-      const int n = static_cast<int>(std::min<int64_t>(p.K - e, 8));
-      float h[8];
-      load_h(e, n, h);
-      float t[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) t[i] = h[2 * i] * h[2 * i] + h[2 * i + 1] * h[2 * i + 1];
-      sum += (t[0] + t[1]) + (t[2] + t[3]);
-    }
-    const float rstd = rstd_of(row_sum<kLongWaves>(sum, part), p);
+    auto row_squares = [&](float scale) __attribute__((always_inline)) {
+      float sum = 0.0f;
+      for (int64_t k = 0; k < steps; ++k) {
+        const int64_t e = k * kStep + 8 * (int64_t)threadIdx.x;
+        const int n = static_cast<int>(std::min<int64_t>(p.K - e, 8));
+        float h[8];
+        load_h(e, n, h);
+        sum += squares8(h, scale);
+      }
+      return sum;
+    };
+    const float rstd = rstd_of(row_sum<kLongWaves>(row_squares(1.0f), part), p, [&]() __attribute__((always_inline)) {
+      return row_sum<kLongWaves>(row_squares(kFar), part);
+    });
     for (int64_t k = 0; k < steps; ++k) {
       const int64_t e = k * kStep + 8 * (int64_t)threadIdx.x;
       const int n = static_cast<int>(std::min<int64_t>(p.K - e, 8));
       float h[8], w[8] = {};
       load_h(e, n, h);
       if (n > 0) load_weight8<kVec, false>(p, e, n, w);
+      if (p.res_out && n > 0) store_bf16x8<kVec>(p.res_out + r * p.K + e, n, h);
       emit8<kVec>(p, r, e, n, h, w, rstd);
     }
   }
