@@ -403,7 +403,8 @@ typedef enum mx_type { MX_TYPE_BF16 = 0, MX_TYPE_F32 = 1 } mx_type;
  *   residual_out = bf16_rne(h),  y = bf16_rne(n),
  *   (q, s) = MX quantisation of n along kd, as mx_quantize's of a row
  * in fp32 throughout, each output rounded once: the norm reads h before it is
- * rounded to bf16, and q rounds n itself and not y.
+ * rounded to bf16, and q rounds n itself and not y.  Before that rounding n is
+ * within 48 * 2^-24 of the n of its h, for any kd.
  *   x         bf16 [rows, kd], row stride ldx >= kd elements
  *   residual  bf16 [rows, kd], row stride ldr >= kd, or NULL (ldr unused)
  *   weight    [kd], bf16 or fp32 (weight_type); a norm that multiplies by

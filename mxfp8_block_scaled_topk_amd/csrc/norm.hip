@@ -317,15 +317,24 @@ __global__ __launch_bounds__(64 * kLongWaves) void add_rmsnorm_long(NormParams p
       }
     };
     auto row_squares = [&](float scale) __attribute__((always_inline)) {
-      float sum = 0.0f;
+      // 16 chunks at a time, 16 of these at a time: of up to 2048 chunks none
+      // goes through more than 42 additions (one running sum would be off by
+      // 2^-15 where all roundings fall to one side)
+      float sum = 0.0f, sum256 = 0.0f, sum16 = 0.0f;
       for (int64_t k = 0; k < steps; ++k) {
         const int64_t e = k * kStep + 8 * (int64_t)threadIdx.x;
         const int n = static_cast<int>(std::min<int64_t>(p.K - e, 8));
         float h[8];
         load_h(e, n, h);
-        sum += squares8(h, scale);
+        sum16 += squares8(h, scale);
+        if ((k & 15) != 15) continue;
+        sum256 += sum16;
+        sum16 = 0.0f;
+        if ((k & 255) != 255) continue;
+        sum += sum256;
+        sum256 = 0.0f;
       }
-      return sum;
+      return sum + (sum256 + sum16);
     };
     const float rstd = rstd_of(row_sum<kLongWaves>(row_squares(1.0f), part), p, [&]() __attribute__((always_inline)) {
       return row_sum<kLongWaves>(row_squares(kFar), part);
