@@ -639,6 +639,12 @@ def mx_add_rmsnorm(x, weight, residual=None, eps=1e-6, quantize=True, norm_out=F
     if type(x) is not _Tensor or x.dtype is not _BF16:
         _need(x, _BF16, "x")
     shape, dev = x.shape, x.device
+    on_gpu = x.is_cuda
+    if on_gpu:   # before _rows, whose copy of strided leading dims belongs to the stream of the call
+        there = _elsewhere(dev, stream)
+        if there is not None:
+            with there:
+                return mx_add_rmsnorm(x, weight, residual, eps, quantize, norm_out, out)
     if not shape or shape[-1] == 0:
         raise ValueError("x must have at least one element per row")
     K = shape[-1]
@@ -665,11 +671,8 @@ def mx_add_rmsnorm(x, weight, residual=None, eps=1e-6, quantize=True, norm_out=F
             _need_like(r_out, shape, "residual_out", _BF16, dev)
         if y is not None:
             _need_like(y, shape, "y", _BF16, dev)
-    _need_gpu(x, "x")
-    there = _elsewhere(dev, stream)
-    if there is not None:
-        with there:
-            return mx_add_rmsnorm(x, weight, residual, eps, quantize, norm_out, out)
+    if not on_gpu:
+        _need_gpu(x, "x")
     if out is None:
         q = torch.empty(shape, dtype=_U8, device=dev) if quantize else None
         s = torch.empty(s_shape, dtype=_U8, device=dev) if quantize else None
