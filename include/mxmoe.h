@@ -481,7 +481,7 @@ size_t mx_linear_fused_workspace_size(int64_t T, int64_t K, int64_t N, int x_is_
  *             (an odd count of scales padded with a zero byte)
  * y may be the residual itself (the same address); any other overlap of an
  * output or of the workspace is MX_ERR_INVALID_ARG.  Limits:
- * K % 32 == 0, K <= 2^20; T and N as they are.  Alignment: MXFP8 payloads that
+ * K % 32 == 0, K <= 2^20, fewer than 2^30 tiles of 32 x 32 outputs.  Alignment: MXFP8 payloads that
  * are read on 16-byte boundaries, their scales on 4, the workspace on 256.
  */
 int mx_linear_fused(const void* x, const void* x_s, const void* w_u8,

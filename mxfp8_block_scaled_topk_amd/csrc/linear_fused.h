@@ -25,6 +25,7 @@ struct LinParams {
   int bias_f32;
   int act;             // mx_activation
   uint32_t n_tiles, t_tiles;   // lin_stream_kernel's tiles along N and T
+  uint32_t first8;             // its launch's first workgroup, over 8
   int stream_res;      // the residual is too large to be left in the memory-side cache
 };
 

@@ -69,6 +69,9 @@ __device__ __forceinline__ int swz(int r, int c) { return r * kStageK + ((c ^ ((
 // only the weights go through the rings.
 constexpr int kMaxResident = 65536;
 
+// Workgroups per launch (a grid holds fewer than 2^32 threads).
+constexpr uint32_t kGridMax = 1u << 22;
+
 template <int NF, int MF, int WV, int S, bool kTail, int XR>
 __global__ __launch_bounds__(64 * WV) void lin_stream_kernel(LinParams p) {
   constexpr bool kX16 = XR == 0;
@@ -93,7 +96,7 @@ __global__ __launch_bounds__(64 * WV) void lin_stream_kernel(LinParams p) {
   // the tiles, cut along the longer side, so that one L2 sees an operand row.
   const uint32_t share = (p.n_tiles * p.t_tiles) >> 3, spare = (p.n_tiles * p.t_tiles) & 7;
   const uint32_t xcd = blockIdx.x & 7;
-  const uint32_t id = xcd * share + std::min(xcd, spare) + (blockIdx.x >> 3);
+  const uint32_t id = xcd * share + std::min(xcd, spare) + (blockIdx.x >> 3) + p.first8;
   const bool by_rows = p.N >= p.T;
   const uint32_t inner = by_rows ? p.t_tiles : p.n_tiles;
   const uint32_t outer_i = id / inner, inner_i = id - outer_i * inner;
@@ -313,12 +316,13 @@ template <int NF, int MF, int WV, int S, int XR = 32 * MF>
 int launch_stream(LinParams p, hipStream_t stream) {
   p.n_tiles = (uint32_t)((p.N + 32 * NF - 1) / (32 * NF));
   p.t_tiles = (uint32_t)((p.T + 32 * MF - 1) / (32 * MF));
-  const int64_t grid = (int64_t)p.n_tiles * p.t_tiles;
-  if (grid * 64 * WV >= (int64_t)1 << 32) return fail(MX_ERR_UNSUPPORTED, "mx_linear_fused: too many tiles");
-  if (p.K % kStageK)
-    lin_stream_kernel<NF, MF, WV, S, true, XR><<<dim3((unsigned)grid), dim3(64 * WV), 0, stream>>>(p);
-  else
-    lin_stream_kernel<NF, MF, WV, S, false, XR><<<dim3((unsigned)grid), dim3(64 * WV), 0, stream>>>(p);
+  const uint32_t total = p.n_tiles * p.t_tiles;   // under 2^30 (check_sizes)
+  for (uint32_t first = 0; first < total; first += kGridMax) {
+    p.first8 = first / 8;
+    const dim3 grid(std::min(total - first, kGridMax));
+    if (p.K % kStageK) lin_stream_kernel<NF, MF, WV, S, true, XR><<<grid, dim3(64 * WV), 0, stream>>>(p);
+    else lin_stream_kernel<NF, MF, WV, S, false, XR><<<grid, dim3(64 * WV), 0, stream>>>(p);
+  }
   return check_launch("mx_linear_fused");
 }
 
@@ -385,6 +389,9 @@ int check_sizes(int64_t T, int64_t K, int64_t N) {
   if (!dims_in_range({T, N})) return fail(MX_ERR_UNSUPPORTED, "mx_linear_fused: T or N above 2^31 - 1");
   if (K % 32 != 0) return fail(MX_ERR_UNSUPPORTED, "mx_linear_fused: K=%lld is not a multiple of 32", (long long)K);
   if (K > kMaxK) return fail(MX_ERR_UNSUPPORTED, "mx_linear_fused: K=%lld > 2^20", (long long)K);
+  // 32-bit tile indices in every kernel, also a round past the last (an output of a TB)
+  if (((T + 31) / 32) * ((N + 31) / 32) >= (int64_t)1 << 30)
+    return fail(MX_ERR_UNSUPPORTED, "mx_linear_fused: 2^30 or more tiles of 32 x 32 outputs");
   return MX_OK;
 }
 
