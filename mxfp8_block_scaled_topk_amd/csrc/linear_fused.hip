@@ -316,7 +316,7 @@ template <int NF, int MF, int WV, int S, int XR = 32 * MF>
 int launch_stream(LinParams p, hipStream_t stream) {
   p.n_tiles = (uint32_t)((p.N + 32 * NF - 1) / (32 * NF));
   p.t_tiles = (uint32_t)((p.T + 32 * MF - 1) / (32 * MF));
-  const uint32_t total = p.n_tiles * p.t_tiles;   // under 2^30 (check_sizes)
+  const uint32_t total = p.n_tiles * p.t_tiles;   // under 2^30 (the entry point)
   for (uint32_t first = 0; first < total; first += kGridMax) {
     p.first8 = first / 8;
     const dim3 grid(std::min(total - first, kGridMax));
@@ -382,6 +382,9 @@ FusedLayout fused_layout(int64_t T, int64_t K, int x_is_mx) {
   return L;
 }
 
+// Tile indices are 32-bit in every kernel, also a round past the last: an output of a TB.
+bool too_many_tiles(int64_t T, int64_t N) { return ((T + 31) / 32) * ((N + 31) / 32) >= (int64_t)1 << 30; }
+
 int check_sizes(int64_t T, int64_t K, int64_t N) {
   if (T < 0 || K <= 0 || N <= 0)
     return fail(MX_ERR_INVALID_ARG, "mx_linear_fused: bad sizes T=%lld K=%lld N=%lld", (long long)T, (long long)K,
@@ -389,9 +392,6 @@ int check_sizes(int64_t T, int64_t K, int64_t N) {
   if (!dims_in_range({T, N})) return fail(MX_ERR_UNSUPPORTED, "mx_linear_fused: T or N above 2^31 - 1");
   if (K % 32 != 0) return fail(MX_ERR_UNSUPPORTED, "mx_linear_fused: K=%lld is not a multiple of 32", (long long)K);
   if (K > kMaxK) return fail(MX_ERR_UNSUPPORTED, "mx_linear_fused: K=%lld > 2^20", (long long)K);
-  // 32-bit tile indices in every kernel, also a round past the last (an output of a TB)
-  if (((T + 31) / 32) * ((N + 31) / 32) >= (int64_t)1 << 30)
-    return fail(MX_ERR_UNSUPPORTED, "mx_linear_fused: 2^30 or more tiles of 32 x 32 outputs");
   return MX_OK;
 }
 
@@ -401,7 +401,7 @@ int check_sizes(int64_t T, int64_t K, int64_t N) {
 
 extern "C" size_t mx_linear_fused_workspace_size(int64_t T, int64_t K, int64_t N, int x_is_mx) {
   // 0 for sizes mx_linear_fused rejects
-  if (mxmoe::check_sizes(T, K, N) != MX_OK) return 0;
+  if (mxmoe::check_sizes(T, K, N) != MX_OK || mxmoe::too_many_tiles(T, N)) return 0;
   return mxmoe::fused_layout(T, K, x_is_mx).total;
 }
 
@@ -470,6 +470,8 @@ extern "C" int mx_linear_fused(const void* x, const void* x_s, const void* w_u8,
   for (int i = 0; i < 7; ++i)
     if (i != 5 && overlaps(in[5], in[i]))
       return fail(MX_ERR_INVALID_ARG, "mx_linear_fused: the workspace overlaps an input");
+  if (too_many_tiles(T, N))
+    return fail(MX_ERR_UNSUPPORTED, "mx_linear_fused: 2^30 or more tiles of 32 x 32 outputs");
   hipStream_t s = as_stream(stream);
   if (mx_in) {
     p.x = static_cast<const uint8_t*>(x);

@@ -456,7 +456,7 @@ template <int NA, int NB, int WN, int WM, int S>
 int launch_tiles(const LinParams& p, int per_cu, hipStream_t stream) {
   constexpr int BN = 32 * NA * WN, BM = 32 * NB * WM;
   const int64_t m_tiles = (p.T + BM - 1) / BM, n_tiles = (p.N + BN - 1) / BN;
-  const int64_t total = m_tiles * n_tiles;   // under 2^30 (check_sizes)
+  const int64_t total = m_tiles * n_tiles;   // under 2^30 (the entry point)
   const int64_t full = std::max<int64_t>(8, (int64_t)num_cus() * per_cu / 8 * 8);
   const dim3 grid((unsigned)std::min(full, (total + 7) / 8 * 8)), block(64 * WN * WM);
   const bool groups = p.K % (4 * kStageK) == 0 && reinterpret_cast<uintptr_t>(p.xs) % 16 == 0 &&
