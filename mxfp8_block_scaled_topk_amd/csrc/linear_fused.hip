@@ -63,7 +63,7 @@ __device__ __forceinline__ int swz(int r, int c) { return r * kStageK + ((c ^ ((
 // host): the lanes of the tokens beyond repeat them, and the ring is deeper (T =
 // 1, K = N = 4096: 6.1 -> 5.7 us; K = 8192, N = 512: 7.6 -> 7.1).
 //
-// XR = 0 (kX16): p.x is bf16 [T, K], T <= 32 and T K <= kMaxResident (host).  The tokens
+// XR = 0 (kX16): p.x is bf16 [T, K], T <= 32, T K <= kMaxResident, one launch (host).  The tokens
 // stay in LDS as MXFP8 rows of nk stages, swizzled like a slot's, each row an
 // odd number of 128-byte stages long so that 16 rows' chunks hit distinct banks;
 // only the weights go through the rings.
@@ -96,7 +96,7 @@ __global__ __launch_bounds__(64 * WV) void lin_stream_kernel(LinParams p) {
   // the tiles, cut along the longer side, so that one L2 sees an operand row.
   const uint32_t share = (p.n_tiles * p.t_tiles) >> 3, spare = (p.n_tiles * p.t_tiles) & 7;
   const uint32_t xcd = blockIdx.x & 7;
-  const uint32_t id = xcd * share + std::min(xcd, spare) + (blockIdx.x >> 3) + p.first8;
+  const uint32_t id = xcd * share + std::min(xcd, spare) + (blockIdx.x >> 3) + (kX16 ? 0 : p.first8);
   const bool by_rows = p.N >= p.T;
   const uint32_t inner = by_rows ? p.t_tiles : p.n_tiles;
   const uint32_t outer_i = id / inner, inner_i = id - outer_i * inner;
@@ -364,19 +364,24 @@ int launch_linear(const LinParams& p, hipStream_t stream) {
   }
 }
 
-// bf16 tokens that every workgroup quantises for itself (no workspace).  One
-// launch in the place of two: 4 us of host work less.  On the GPU alone (K = N =
-// 2048; quantiser 2.3 us + product) 4.6 against 6.3 us at T = 1, 6.2 against 6.4
-// at T = 16, 8.3 against 6.8 at T = 32, where the workgroup's arithmetic shows.
-bool resident(int64_t T, int64_t K) { return T <= 32 && T * K <= kMaxResident; }
+// bf16 tokens that every workgroup quantises for itself (no workspace): few of
+// them, and no more workgroups than CUs.  It is one launch in the place of two, 4 us
+// of host work less, and one copy of the tokens per workgroup.  On the GPU alone
+// (in place against quantiser + product, K = 2048): N = 2048 4.9 / 6.1 us at T = 1,
+// 6.4 / 6.7 at T = 16, 8.5 / 7.1 at T = 32, where the workgroup's arithmetic
+// shows; N = 8192 6.4 / 7.4, 7.6 / 7.8, 9.7 / 7.9.  Its LDS leaves one workgroup to a
+// CU, and every round of them quantises again: N = 8224 9.0 / 8.0, 11.8 / 8.9, 15.7 /
+// 9.2; N = 131072 75 / 51, 99 / 56, 129 / 63.
+constexpr int64_t kMaxResidentN = 32 * 256;   // (a constant: the workspace query has no device)
+bool resident(int64_t T, int64_t K, int64_t N) { return T <= 32 && T * K <= kMaxResident && N <= kMaxResidentN; }
 
 // Workspace: the MXFP8 form of bf16 tokens.
 struct FusedLayout {
   size_t xq, xs, total;
 };
-FusedLayout fused_layout(int64_t T, int64_t K, int x_is_mx) {
+FusedLayout fused_layout(int64_t T, int64_t K, int64_t N, int x_is_mx) {
   FusedLayout L{0, 0, 0};
-  if (x_is_mx || resident(T, K)) return L;
+  if (x_is_mx || resident(T, K, N)) return L;
   L.xs = align_up((size_t)(T * K), 256);
   L.total = L.xs + align_up((size_t)(T * 2 * ((K + 63) / 64)), 256);
   return L;
@@ -402,7 +407,7 @@ int check_sizes(int64_t T, int64_t K, int64_t N) {
 extern "C" size_t mx_linear_fused_workspace_size(int64_t T, int64_t K, int64_t N, int x_is_mx) {
   // 0 for sizes mx_linear_fused rejects
   if (mxmoe::check_sizes(T, K, N) != MX_OK || mxmoe::too_many_tiles(T, N)) return 0;
-  return mxmoe::fused_layout(T, K, x_is_mx).total;
+  return mxmoe::fused_layout(T, K, N, x_is_mx).total;
 }
 
 extern "C" int mx_linear_fused(const void* x, const void* x_s, const void* w_u8, const void* w_s, const void* bias,
@@ -419,7 +424,7 @@ extern "C" int mx_linear_fused(const void* x, const void* x_s, const void* w_u8,
     return fail(MX_ERR_INVALID_ARG, "mx_linear_fused: unknown activation %d", activation);
   if (!yq_u8 != !ys_u8) return fail(MX_ERR_INVALID_ARG, "mx_linear_fused: yq and ys go together");
   if (y_bf16 && yq_u8) return fail(MX_ERR_INVALID_ARG, "mx_linear_fused: y or (yq, ys), not both");
-  const FusedLayout L = fused_layout(T, K, x_s != nullptr);
+  const FusedLayout L = fused_layout(T, K, N, x_s != nullptr);
   if (T > 0 && (!x || !w_u8 || !w_s || (!y_bf16 && !yq_u8) || (L.total > 0 && !workspace)))
     return fail(MX_ERR_INVALID_ARG, "mx_linear_fused: null pointer");
   if (ws_bytes < L.total)
@@ -476,7 +481,7 @@ extern "C" int mx_linear_fused(const void* x, const void* x_s, const void* w_u8,
   if (mx_in) {
     p.x = static_cast<const uint8_t*>(x);
     p.xs = static_cast<const uint8_t*>(x_s);
-  } else if (resident(T, K)) {
+  } else if (resident(T, K, N)) {
     p.x = static_cast<const uint8_t*>(x);
     return launch_stream<1, 1, 8, 2, 0>(p, s);
   } else {

@@ -34,3 +34,28 @@ def test_linear_fused_2_28_features(mx_in):
     torch.cuda.synchronize()
     assert torch.equal(y[:, :n], first) and torch.equal(y[:, N - n:], last)
     assert torch.equal(y[:, (1 << 27):(1 << 27) + n], mid)
+
+
+@pytest.mark.parametrize("T,K", [(1, 2048), (3, 544), (32, 2048), (32, 96)])
+@pytest.mark.parametrize("N", [8192, 8193, 16424])
+def test_few_bf16_tokens_around_a_round_of_workgroups(T, K, N):
+    """Quantised by every workgroup itself up to 8192 features, ahead of the
+    product past them: the product of mx_quantize's bytes either way.  Small
+    integers, exact in float32 whatever the order of the sums."""
+    gen = torch.Generator(device="cuda").manual_seed(T + N)
+    x = torch.randint(-4, 5, (T, K), device="cuda", generator=gen).bfloat16()
+    w, ws = mx.mx_quantize(torch.randint(-4, 5, (N, K), device="cuda", generator=gen).bfloat16())
+    q, s = mx.mx_quantize(x)
+    say(f"mx_linear_fused T={T} K={K} N={N} few bf16 tokens")
+    a = mx.mx_linear_fused(x, w, ws)
+    b = mx.mx_linear_fused(q, w, ws, x_s=s)
+    aq, a_s = mx.mx_linear_fused(x, w, ws, act="relu", quantize_out=True)
+    bq, b_s = mx.mx_linear_fused(q, w, ws, x_s=s, act="relu", quantize_out=True)
+    torch.cuda.synchronize()
+    want = (x.double() @ w_values(w, ws).T).bfloat16()
+    assert torch.equal(a, want) and torch.equal(a, b) and torch.equal(aq, bq) and torch.equal(a_s, b_s)
+
+
+def w_values(q, s):
+    e = s.reshape(s.shape[0], -1)[:, : -(-q.shape[1] // 32)].double() - 127
+    return q.view(torch.float8_e4m3fn).double() * torch.exp2(e).repeat_interleave(32, dim=1)[:, :q.shape[1]]

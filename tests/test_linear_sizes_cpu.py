@@ -18,3 +18,14 @@ def test_too_many_tiles(T, N):
     args = (at(0), None, at(1), at(2), None, 0, 0, None, T, 32, N, at(3), None, None, at(4), 1 << 43, None)
     assert lib.mx_linear_fused(*args) == -2 and "2^30" in mx.last_error()
     assert mx.linear_fused_workspace_size(T, 32, N, False) == 0
+
+
+@pytest.mark.parametrize("T,K", [(1, 2048), (32, 2048), (1, 65536), (32, 32)])
+def test_tokens_are_quantised_in_place_in_one_round_of_workgroups(T, K):
+    """Few bf16 tokens need no workspace while the workgroups that each quantise
+    them are no more than the 256 CUs, one per 32 features."""
+    for N in (1, 96, 8191, 8192):
+        assert mx.linear_fused_workspace_size(T, K, N, False) == 0
+    for N in (8193, 16384, 131072):
+        assert mx.linear_fused_workspace_size(T, K, N, False) >= T * K + T * 2 * -(-K // 64)
+        assert mx.linear_fused_workspace_size(T, K, N, True) == 0
