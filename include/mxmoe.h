@@ -491,6 +491,25 @@ int mx_linear_fused(const void* x, const void* x_s, const void* w_u8,
                     void* ys_u8, void* workspace, size_t ws_bytes,
                     void* stream);
 
+/* The kernels of mx_linear_fused, by their tiles (weight rows x tokens). */
+typedef enum mx_linear_kernel {
+  MX_LINEAR_32X32 = 0,
+  MX_LINEAR_64X64 = 1,
+  MX_LINEAR_64X96 = 2,
+  MX_LINEAR_64X64_TWICE = 3, /* 64 x 64, two workgroups per CU */
+  MX_LINEAR_128X128 = 4,
+  MX_LINEAR_256X128 = 5,
+  MX_LINEAR_256X256 = 6,
+  MX_LINEAR_32X32_BF16 = 7   /* 32 x 32, bf16 tokens quantised by each workgroup */
+} mx_linear_kernel;
+
+/*
+ * Which of them mx_linear_fused takes for a size on the current device (256
+ * CUs are assumed where there is none), or a negative mx_status for sizes that
+ * it refuses and for T = 0.  For profiles and tests; enqueues nothing.
+ */
+int mx_linear_fused_kernel(int64_t T, int64_t K, int64_t N, int x_is_mx);
+
 /* Description of the last non-OK status returned on this thread. */
 const char* mx_last_error(void);
 

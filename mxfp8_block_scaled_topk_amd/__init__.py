@@ -25,7 +25,7 @@ __all__ = [
     "route_workspace_size", "forward_workspace_size", "last_error", "moe_router", "mx_linear",
     "linear_workspace_size", "mx_quantize_fp4", "moe_route_quant_noalloc", "mx_pack_weights", "route_set_wait_limit",
     "gmm_swiglu_mxquant_packed", "gmm_mx_packed", "moe_mxfp8_forward_packed", "gmm_mx_w4a8", "gmm_swiglu_mxquant_w4a8", "moe_w4a8_forward",
-    "mx_linear_fused", "linear_fused_workspace_size", "mx_add_rmsnorm", "moe_route_mx", "moe_mxfp8_forward_mx",
+    "mx_linear_fused", "linear_fused_workspace_size", "linear_fused_kernel", "mx_add_rmsnorm", "moe_route_mx", "moe_mxfp8_forward_mx",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -83,6 +83,7 @@ def load():
         "moe_route_mx": (I32, [P, P, P, I64, I64, I64, I64, P, P, P, P, P, P, SZ, P]),
         "moe_mxfp8_forward_mx": (I32, [P, P, P, P, I32, P, P, P, P, I64, I64, I64, I64, I64, P, P, SZ, P]),
         "mx_linear_fused_workspace_size": (SZ, [I64, I64, I64, I32]),
+        "mx_linear_fused_kernel": (I32, [I64, I64, I64, I32]),
         "mx_linear_fused": (I32, [P, P, P, P, P, I32, I32, P, I64, I64, I64, P, P, P, P, SZ, P]),
         "mx_last_error": (ctypes.c_char_p, []),
     }
@@ -792,6 +793,18 @@ ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
 
 def linear_fused_workspace_size(T, K, N, x_is_mx):
     return int(load().mx_linear_fused_workspace_size(T, K, N, int(x_is_mx)))
+
+
+LINEAR_KERNELS = ("32x32", "64x64", "64x96", "64x64 twice per CU", "128x128", "256x128", "256x256", "32x32 bf16")
+
+
+def linear_fused_kernel(T, K, N, x_is_mx):
+    """Which of LINEAR_KERNELS (named by their tiles, weight rows x tokens)
+    mx_linear_fused takes for a size on the current device."""
+    index = load().mx_linear_fused_kernel(T, K, N, int(x_is_mx))
+    if index < 0:
+        _check(index, "mx_linear_fused_kernel")
+    return LINEAR_KERNELS[index]
 
 
 def mx_linear_fused(x, w, w_s, x_s=None, bias=None, act="none", residual=None, quantize_out=False, out=None,

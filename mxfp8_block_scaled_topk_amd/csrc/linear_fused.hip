@@ -335,13 +335,13 @@ int launch_stream(LinParams p, hipStream_t stream) {
 // 2080, N = 4099 takes 19.3 us in 260 tiles of 64 x 64, 13.7 us in 903 of 32 x
 // 32.  (Also measured: 32 x 32 over 8 waves, one per CU, and 64 x 32 over 6 or
 // 3; they win by 0.5 % on average.)
-int launch_linear(const LinParams& p, hipStream_t stream) {
-  const int64_t cus = num_cus(), nk = p.nk;
-  auto tiles = [&](int64_t bn, int64_t bm) { return ((p.N + bn - 1) / bn) * ((p.T + bm - 1) / bm); };
+mx_linear_kernel choose(int64_t T, int64_t K, int64_t N) {
+  const int64_t cus = num_cus(), nk = (K + kStageK - 1) / kStageK;
+  auto tiles = [&](int64_t bn, int64_t bm) { return ((N + bn - 1) / bn) * ((T + bm - 1) / bm); };
   auto up = [](int64_t n, int64_t d) { return (n + d - 1) / d; };
   const int64_t t32 = tiles(32, 32), t128 = tiles(128, 128);
-  const bool big = p.N >= (int64_t)1 << 27;   // the tile kernels' 32-bit offsets within 8 rows
-  const int64_t us[7] = {
+  const bool big = N >= (int64_t)1 << 27;   // the tile kernels' 32-bit offsets within 8 rows
+  const int64_t us[7] = {   // in mx_linear_kernel's order
       // K over 4 waves, two workgroups per CU
       t32 <= cus ? 35 + 5 * up(nk, 4) : up(t32, 2 * cus) * (33 + 7 * up(nk, 4)),
       up(tiles(64, 64), cus) * (44 + 11 * up(nk, 4)),           // over 4
@@ -350,16 +350,20 @@ int launch_linear(const LinParams& p, hipStream_t stream) {
       big ? INT64_MAX : t128 <= cus ? 82 + 17 * nk / 2 : up(t128, 2 * cus) * (82 + 11 * nk),   // two per CU
       big || nk < 3 ? INT64_MAX : up(tiles(256, 128), cus) * (100 + 9 * nk),
       big ? INT64_MAX : up(tiles(256, 256), cus) * (174 + 14 * nk)};
-  switch (std::min_element(us, us + 7) - us) {
-    case 0:
+  return static_cast<mx_linear_kernel>(std::min_element(us, us + 7) - us);
+}
+
+int launch_linear(const LinParams& p, hipStream_t stream) {
+  switch (choose(p.T, p.K, p.N)) {
+    case MX_LINEAR_32X32:
       if (p.T <= 8) return launch_stream<1, 1, 4, 3, 8>(p, stream);
       if (p.T <= 16) return launch_stream<1, 1, 4, 3, 16>(p, stream);
       return launch_stream<1, 1, 4, 2>(p, stream);
-    case 1: return launch_stream<2, 2, 4, 2>(p, stream);
-    case 2: return launch_stream<2, 3, 3, 2>(p, stream);
-    case 3: return launch_stream<2, 2, 2, 2>(p, stream);
-    case 4: return launch_lin_tile128(p, stream);
-    case 5: return launch_lin_tile256x128(p, stream);
+    case MX_LINEAR_64X64: return launch_stream<2, 2, 4, 2>(p, stream);
+    case MX_LINEAR_64X96: return launch_stream<2, 3, 3, 2>(p, stream);
+    case MX_LINEAR_64X64_TWICE: return launch_stream<2, 2, 2, 2>(p, stream);
+    case MX_LINEAR_128X128: return launch_lin_tile128(p, stream);
+    case MX_LINEAR_256X128: return launch_lin_tile256x128(p, stream);
     default: return launch_lin_tile256(p, stream);
   }
 }
@@ -389,6 +393,7 @@ FusedLayout fused_layout(int64_t T, int64_t K, int64_t N, int x_is_mx) {
 
 // Tile indices are 32-bit in every kernel, also a round past the last: an output of a TB.
 bool too_many_tiles(int64_t T, int64_t N) { return ((T + 31) / 32) * ((N + 31) / 32) >= (int64_t)1 << 30; }
+int fail_tiles() { return fail(MX_ERR_UNSUPPORTED, "mx_linear_fused: 2^30 or more tiles of 32 x 32 outputs"); }
 
 int check_sizes(int64_t T, int64_t K, int64_t N) {
   if (T < 0 || K <= 0 || N <= 0)
@@ -408,6 +413,15 @@ extern "C" size_t mx_linear_fused_workspace_size(int64_t T, int64_t K, int64_t N
   // 0 for sizes mx_linear_fused rejects
   if (mxmoe::check_sizes(T, K, N) != MX_OK || mxmoe::too_many_tiles(T, N)) return 0;
   return mxmoe::fused_layout(T, K, N, x_is_mx).total;
+}
+
+extern "C" int mx_linear_fused_kernel(int64_t T, int64_t K, int64_t N, int x_is_mx) {
+  using namespace mxmoe;
+  const int rc = check_sizes(T, K, N);
+  if (rc) return rc;
+  if (T == 0) return fail(MX_ERR_INVALID_ARG, "mx_linear_fused_kernel: no tokens");
+  if (too_many_tiles(T, N)) return fail_tiles();
+  return !x_is_mx && resident(T, K, N) ? MX_LINEAR_32X32_BF16 : choose(T, K, N);
 }
 
 extern "C" int mx_linear_fused(const void* x, const void* x_s, const void* w_u8, const void* w_s, const void* bias,
@@ -475,8 +489,7 @@ extern "C" int mx_linear_fused(const void* x, const void* x_s, const void* w_u8,
   for (int i = 0; i < 7; ++i)
     if (i != 5 && overlaps(in[5], in[i]))
       return fail(MX_ERR_INVALID_ARG, "mx_linear_fused: the workspace overlaps an input");
-  if (too_many_tiles(T, N))
-    return fail(MX_ERR_UNSUPPORTED, "mx_linear_fused: 2^30 or more tiles of 32 x 32 outputs");
+  if (too_many_tiles(T, N)) return fail_tiles();
   hipStream_t s = as_stream(stream);
   if (mx_in) {
     p.x = static_cast<const uint8_t*>(x);

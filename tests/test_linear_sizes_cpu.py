@@ -29,3 +29,18 @@ def test_tokens_are_quantised_in_place_in_one_round_of_workgroups(T, K):
     for N in (8193, 16384, 131072):
         assert mx.linear_fused_workspace_size(T, K, N, False) >= T * K + T * 2 * -(-K // 64)
         assert mx.linear_fused_workspace_size(T, K, N, True) == 0
+
+
+def test_which_kernel():
+    """The query: the names' order, the bf16 tokens' kernel, refusals."""
+    lib = mx.load()
+    assert [mx.linear_fused_kernel(T, K, N, True) for T, K, N in
+            ((1, 2048, 2048), (66, 256, 5650), (288, 640, 5400), (132, 256, 5493), (450, 256, 4104), (1030, 1664, 4096),
+             (1440, 512, 5640))] == list(mx.LINEAR_KERNELS[:7])
+    assert mx.linear_fused_kernel(32, 2048, 8192, False) == mx.LINEAR_KERNELS[7]
+    assert mx.linear_fused_kernel(32, 2048, 8193, False) == mx.linear_fused_kernel(32, 2048, 8193, True)
+    assert lib.mx_linear_fused_kernel(0, 64, 64, 1) == -1 and lib.mx_linear_fused_kernel(4, 0, 64, 1) == -1
+    assert lib.mx_linear_fused_kernel(4, 65, 64, 1) == -2 and lib.mx_linear_fused_kernel(1 << 20, 32, 1 << 20, 1) == -2
+    for sizes in ((0, 64, 64), (4, 65, 64)):
+        with pytest.raises(mx.MxError):
+            mx.linear_fused_kernel(*sizes, True)
