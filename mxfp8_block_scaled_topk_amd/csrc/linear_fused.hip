@@ -29,10 +29,11 @@
 // into LDS itself while its first weights are on their way.
 //
 // Bounded by what a CU can take in, about 60 GB/s (26 bytes a cycle) of weights
-// and tokens together, behind 3 us of launch and first loads: T = 32, K = N =
-// 4096 takes 7.0 us (17 MB of weights at 2.4 TB/s), T = 1 5.7 us; K = N = 8192 at T =
-// 1 12.3 us (67 MB, 5.5 TB/s); T = 1, K = N = 2048 from bf16 4.6 us.  The tile is a
-// choice between re-reading the tokens (few rows) and few workgroups (many rows).
+// and tokens together, on as many CUs as there are tiles (N / 32 for few tokens),
+// behind 3 us of launch and first loads: T = 32, K = N = 4096 takes 7.0 us on 128 CUs
+// (17 MB of weights at 2.4 TB/s), T = 1 5.7 us; K = N = 8192 at T = 1 12.2 us (67
+// MB, 5.5 TB/s); T = 1, K = N = 2048 from bf16 4.6 us on 64.  The tile is a choice
+// between re-reading the tokens (few rows) and few workgroups (many rows).
 #include <algorithm>
 
 #include "linear_fused.h"
@@ -334,7 +335,9 @@ int launch_stream(LinParams p, hipStream_t stream) {
 // The smaller kernels differ only in how the tiles fill the rounds: T = 203, K =
 // 2080, N = 4099 takes 19.3 us in 260 tiles of 64 x 64, 13.7 us in 903 of 32 x
 // 32.  (Also measured: 32 x 32 over 8 waves, one per CU, and 64 x 32 over 6 or
-// 3; they win by 0.5 % on average.)
+// 3; they win by 0.5 % on average.  32 x 32 over 8 where one round holds the tiles:
+// T = 1, K = 8192, N = 512 7.0 us instead of 7.2, rows of 2080 up to 7 % less, nearly
+// all others 2 - 9 % more.)
 mx_linear_kernel choose(int64_t T, int64_t K, int64_t N) {
   const int64_t cus = num_cus(), nk = (K + kStageK - 1) / kStageK;
   auto tiles = [&](int64_t bn, int64_t bm) { return ((N + bn - 1) / bn) * ((T + bm - 1) / bm); };

@@ -18,13 +18,13 @@
 //   256 x 128, three slots  0.9 us a stage (2.4 PFLOP/s), half the epilogue
 //   128 x 128, two slots    two workgroups per CU, so that one's epilogue and
 //                           first loads run beside the other's products
-// Measured: T = 16384, K = N = 4096 with bias and residual 254 - 263 us, 2.1 -
+// Measured: T = 16384, K = N = 4096 with bias and residual 251 - 263 us, 2.1 -
 // 2.2 PFLOP/s (the same product in 256 x 256 tiles without a residual 235 us,
 // 2.34; the library's fp8 product without any epilogue 224 us).  What bounds it:
 // operands arriving in LDS, 64 KB a stage at about 47 GB/s per CU (the matrix
 // units are busy half of the time, at 2.1 GHz), then the residual and the output
 // of all CUs in one burst per tile.  T = 2048, K = 2048,
-// N = 4096 to MXFP8 with gelu_tanh 27 us: 15 us of stages, the rest one tile's
+// N = 4096 to MXFP8 with gelu_tanh 27 - 30 us: 15 us of stages, the rest one tile's
 // launch, first loads and epilogue with nothing beside them.
 #include <algorithm>
 #include <type_traits>

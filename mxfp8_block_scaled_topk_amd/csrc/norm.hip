@@ -18,7 +18,7 @@
 // (add_rmsnorm_long).
 // HBM-bound: 2 bytes per element in (4 with a residual), 1 + 1/32 out (2 more
 // for each of residual_out and y).  16384 x 2048 with all of them takes 58 us,
-// 303 MB at 5.2 TB/s (a copy of 256 MB: 5.5); 1031 x 4304 6.8 us; one row of 2048
+// 303 MB at 5.2 TB/s (a copy of 256 MB: 5.5); 1031 x 4304 6.9 us; one row of 2048
 // 2.7 us, of which the launch is 1.7.
 #include <algorithm>
 #include <cfloat>
@@ -362,6 +362,10 @@ void launch_norm(const NormParams& p, hipStream_t stream) {
     add_rmsnorm_kernel<W, C, kVec, kTiny><<<dim3((unsigned)grid), dim3(64 * (W < 4 ? 4 : W)), 0, stream>>>(p); \
   } while (0)
 #define MX_NORM_LAUNCH(W, C) MX_NORM_LAUNCH_T(W, C, false)
+#define MX_NORM_LAUNCH_VEC(W, C)              \
+  do {                                        \
+    if constexpr (kVec) MX_NORM_LAUNCH(W, C); \
+  } while (0)
 #define MX_NORM_LONG()                                                                         \
   add_rmsnorm_long<kVec><<<dim3((unsigned)std::min<int64_t>((int64_t)num_cus() * 2, p.rows)), \
                            dim3(64 * kLongWaves), 0, stream>>>(p)
@@ -375,7 +379,7 @@ void launch_norm(const NormParams& p, hipStream_t stream) {
     else if (chunks <= 512) MX_NORM_LAUNCH(8, 1);
     else if (chunks <= 1024) MX_NORM_LAUNCH(16, 1);
     else if (chunks <= 2048) MX_NORM_LAUNCH(16, 2);
-    else if (kVec && chunks <= 4096) MX_NORM_LAUNCH(16, 4);
+    else if (kVec && chunks <= 4096) MX_NORM_LAUNCH_VEC(16, 4);
     else MX_NORM_LONG();
   } else if (chunks <= 64) MX_NORM_LAUNCH(1, 1);
   else if (chunks <= 128) MX_NORM_LAUNCH(1, 2);
@@ -383,9 +387,10 @@ void launch_norm(const NormParams& p, hipStream_t stream) {
   else if (chunks <= 512) MX_NORM_LAUNCH(4, 2);
   else if (chunks <= 1024) MX_NORM_LAUNCH(4, 4);
   else if (chunks <= 2048) MX_NORM_LAUNCH(8, 4);
-  else if (kVec && chunks <= 4096) MX_NORM_LAUNCH(16, 4);
+  else if (kVec && chunks <= 4096) MX_NORM_LAUNCH_VEC(16, 4);
   else MX_NORM_LONG();
 #undef MX_NORM_LONG
+#undef MX_NORM_LAUNCH_VEC
 #undef MX_NORM_LAUNCH
 #undef MX_NORM_LAUNCH_T
 }

@@ -59,3 +59,22 @@ def test_few_bf16_tokens_around_a_round_of_workgroups(T, K, N):
 def w_values(q, s):
     e = s.reshape(s.shape[0], -1)[:, : -(-q.shape[1] // 32)].double() - 127
     return q.view(torch.float8_e4m3fn).double() * torch.exp2(e).repeat_interleave(32, dim=1)[:, :q.shape[1]]
+
+
+@pytest.mark.parametrize("T,K,N", [(7, 544, 640), (32, 2048, 8192), (33, 2080, 515), (600, 512, 4104), (1500, 672, 5633)])
+def test_bf16_tokens_on_odd_addresses_and_in_place(T, K, N):
+    """bf16 tokens that start at an odd element, with the residual in place:
+    the bytes of the plain call."""
+    gen = torch.Generator(device="cuda").manual_seed(T)
+    x = torch.randn(T, K, device="cuda", generator=gen).bfloat16()
+    w, ws = mx.mx_quantize((0.05 * torch.randn(N, K, device="cuda", generator=gen)).bfloat16())
+    res = torch.randn(T, N, device="cuda", generator=gen).bfloat16()
+    say(f"mx_linear_fused T={T} K={K} N={N} odd bf16 tokens")
+    want = mx.mx_linear_fused(x, w, ws, act="silu", residual=res)
+    odd = torch.zeros(T * K + 1, dtype=torch.bfloat16, device="cuda")[1:].view(T, K)
+    odd.copy_(x)
+    r = torch.zeros(T * N + 1, dtype=torch.bfloat16, device="cuda")[1:].view(T, N)
+    r.copy_(res)
+    got = mx.mx_linear_fused(odd, w, ws, act="silu", residual=r, out=r)
+    torch.cuda.synchronize()
+    assert got is r and torch.equal(got, want)
