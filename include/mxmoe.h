@@ -482,16 +482,18 @@ size_t mx_linear_fused_workspace_size(int64_t T, int64_t K, int64_t N, int x_is_
  * gmm_swiglu_mxquant and gmm_mx add up with the same instruction.
  *   x         uint8 [T, K] e4m3 with x_s uint8 [T, ceil(K/64), 2], or with a
  *             NULL x_s bf16 [T, K], quantised first (the bytes are those of
- *             mx_quantize; few tokens need no workspace for it)
+ *             mx_quantize; up to 32 tokens of up to 65536 elements together
+ *             need no workspace for it while N <= 8192)
  *   w, w_s    uint8 [N, K], [N, ceil(K/64), 2]
  *   bias      [N] bf16 or fp32 (bias_type), or NULL
  *   residual  bf16 [T, N] or NULL
  *   y         bf16 [T, N], or yq uint8 [T, N] and ys uint8 [T, ceil(N/64), 2]
  *             (an odd count of scales padded with a zero byte)
  * y may be the residual itself (the same address); any other overlap of an
- * output or of the workspace is MX_ERR_INVALID_ARG.  Limits:
- * K % 32 == 0, K <= 2^20, fewer than 2^30 tiles of 32 x 32 outputs.  Alignment: MXFP8 payloads that
- * are read on 16-byte boundaries, their scales on 4, the workspace on 256.
+ * output or of the workspace is MX_ERR_INVALID_ARG.  Limits: K % 32 == 0,
+ * K <= 2^20, fewer than 2^30 tiles of 32 x 32 outputs.  Alignment: MXFP8
+ * payloads that are read on 16-byte boundaries, their scales on 4, the workspace
+ * on 256.
  */
 int mx_linear_fused(const void* x, const void* x_s, const void* w_u8,
                     const void* w_s, const void* bias, int bias_type,
