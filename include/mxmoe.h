@@ -23,6 +23,12 @@
  *   moe_route_mx, moe_mxfp8_forward_mx
  *                       routing and the layer for token rows that are already
  *                       MXFP8 (as mx_add_rmsnorm writes them)
+ *   int8_quantize, int8_linear, gmm_int8
+ *                       the products in int8 with a scale per token and output
+ *                       channel: quantiser, dense linear, by expert
+ *   moe_permute, moe_unpermute, moe_unpermute_backward
+ *                       token rows of any type sorted by expert and back with
+ *                       the routing weights, and the gradients
  *   mx_pack_weights, gmm_swiglu_mxquant_packed, gmm_mx_packed,
  *   moe_mxfp8_forward_packed
  *                       load-time weight cast into the GEMMs' tile layout,
@@ -391,8 +397,9 @@ int mx_linear(const void* x_bf16, const void* w_u8, const void* w_s,
               int64_t T, int64_t K, int64_t N, void* y_bf16,
               void* workspace, size_t ws_bytes, void* stream);
 
-/* Element types of a norm's weight and of a linear's bias. */
-typedef enum mx_type { MX_TYPE_BF16 = 0, MX_TYPE_F32 = 1 } mx_type;
+/* Element types: of a norm's weight and of a linear's bias (bf16, fp32), and of
+ * moe_unpermute's rows (all three). */
+typedef enum mx_type { MX_TYPE_BF16 = 0, MX_TYPE_F32 = 1, MX_TYPE_F16 = 2 } mx_type;
 
 /*
  * Residual addition, root-mean-square norm and MX quantisation in one pass,
@@ -520,6 +527,120 @@ typedef enum mx_linear_kernel {
  * it refuses and for T = 0.  For profiles and tests; enqueues nothing.
  */
 int mx_linear_fused_kernel(int64_t T, int64_t K, int64_t N, int x_is_mx);
+
+/*
+ * The INT8 path: W8A8 with one fp32 scale per token and per output channel, the
+ * other 8-bit format beside MXFP8 ("PR #30768 report", implementation breakdown:
+ * the activation quantiser goes by type, e4m3 or int8).
+ *
+ * int8_quantize: `rows` rows of `kd` bf16 elements (row stride `ld` >= kd) to
+ * int8 codes q [rows, kd] and scales s fp32 [rows]; the tokens of a product, or a
+ * weight's output channels (rows of [N, K] or [E, N, K]) at load time:
+ *   s[r] = max(amax[r] * fl(1/127), 2^-126),   amax[r] = max |x[r, :]|
+ *   q[r, c] = nearest integer to fl(x[r, c] * fl(1 / s[r])), ties to even
+ * with fl and the products rounded to fp32, so that every code is determined;
+ * |q| <= 127.  Any kd from 1 to 2^24, any alignment of whole elements (rows of a
+ * multiple of 8 elements on 16-byte boundaries, q on 8, are the fastest).
+ */
+int int8_quantize(const void* x_bf16, int64_t rows, int64_t kd, int64_t ld,
+                  void* q_i8, float* s, void* stream);
+
+/* Workspace bytes int8_linear needs (x_is_int8: x comes as int8). */
+size_t int8_linear_workspace_size(int64_t T, int64_t K, int64_t N, int x_is_int8);
+
+/*
+ * Dense INT8 linear layer with its epilogue fused:
+ *   z[t, n]   = (sum_k xq[t, k] * wq[n, k]) * x_s[t] * w_s[n]
+ *   y[t, n]   = bf16_rne( activation(z[t, n] + bias[n]) + residual[t, n] )
+ * the sum exact (int32), everything after it in fp32.  Codes may be any int8,
+ * -128 among them; scales any finite fp32.
+ *   x         int8 [T, K] with x_s fp32 [T], or with a NULL x_s bf16 [T, K],
+ *             quantised first (as int8_quantize)
+ *   w, w_s    int8 [N, K], fp32 [N]
+ *   bias      [N] bf16 or fp32 (bias_type), or NULL
+ *   residual  bf16 [T, N] or NULL;  y bf16 [T, N]
+ * y may be the residual itself (the same address); any other overlap of y or of
+ * the workspace is MX_ERR_INVALID_ARG.  Limits: K % 16 == 0, K < 2^17 (the sum
+ * stays within int32), N < 2^30, fewer than 2^30 tiles of 32 x 32 outputs.
+ * Alignment: int8 operands on 16-byte boundaries, the workspace on 256, the rest
+ * on their elements.
+ */
+int int8_linear(const void* x, const float* x_s, const void* w_i8,
+                const float* w_s, const void* bias, int bias_type,
+                int activation, const void* residual_bf16, int64_t T,
+                int64_t K, int64_t N, void* y_bf16, void* workspace,
+                size_t ws_bytes, void* stream);
+
+/*
+ * Grouped INT8 product over rows sorted by expert (gmm_mx's counterpart), for
+ * expert e and its rows m:
+ *   z[m, n] = (sum_k a[m, k] * w[e, n, k]) * a_s[m] * w_s[e, n]
+ *   y[m, n] = bf16_rne( z[m, n] )                            swiglu == 0
+ *   y[m, n] = bf16_rne( silu(z[m, n]) * z[m, N + n] )        swiglu != 0
+ *   a  int8 [M, K], a_s fp32 [M]
+ *   w  int8 [E, N, K], w_s fp32 [E, N]; with swiglu [E, 2N, K] and [E, 2N], the
+ *      gate rows first (as w13)
+ *   y  bf16 [M, N]
+ * group_list int64 [E], group_list_type 0 = cumulative, 1 = count.  Rows not
+ * owned by any expert are not written.  Limits and alignment as int8_linear,
+ * E <= 1024; fewer than 2^30 tiles of 32 x 32 outputs for M + 32 E rows.
+ */
+int gmm_int8(const void* a_i8, const float* a_s, const void* w_i8,
+             const float* w_s, const int64_t* group_list, int group_list_type,
+             int swiglu, int64_t M, int64_t N, int64_t K, int64_t E,
+             void* y_bf16, void* stream);
+
+/*
+ * Token rows of any type sorted by expert: moe_route_quant without the
+ * quantiser.  Row p of xp is token sorted_row[p] / k's row, byte for byte; with
+ * x_s (the scales of int8 rows; xp_s then too) its scale goes along.
+ *   x    [T, K] elements of elem_bytes = 1, 2 or 4, row stride ldx >= K elements
+ *   x_s  fp32 [T] or NULL, xp_s fp32 [T*k] or NULL
+ *   xp   [T*k, K], dense
+ * The maps, the group list, the workspace (moe_route_quant_workspace_size, on an
+ * 8-byte boundary), the bounded waits and the limits are those of
+ * moe_route_quant, but K may be anything from 1 to 2^24 and rows may lie on any
+ * boundary of elements.  Rows past sum(group_list) are left unwritten.  An output
+ * that overlaps an input, another output or the workspace is MX_ERR_INVALID_ARG.
+ * Its gradient is moe_unpermute without weights.
+ */
+int moe_permute(const void* x, int64_t ldx, int64_t elem_bytes, const float* x_s,
+                const int32_t* topk_ids, int64_t T, int64_t K, int64_t k,
+                int64_t E, void* xp, float* xp_s, int32_t* sorted_row,
+                int32_t* expanded_row_idx, int64_t* group_list, void* workspace,
+                size_t ws_bytes, void* stream);
+
+/*
+ * Expert rows back to their tokens, weights applied: moe_finalize for rows of
+ * any width and type, also without weights.
+ *   out[t, :] = round( sum_{j=0}^{k-1} w[t, j] * y[expanded_row_idx[t*k+j], :] )
+ * accumulated in fp32 in ascending j, each product and sum rounded to fp32, the
+ * result once to the rows' type; w = 1 with a NULL topk_w.  Entries outside
+ * [0, M) are skipped; a token with none left gets zeros.
+ *   y [M, K], out [T, K] of `type` (mx_type); topk_w fp32 [T, k] or NULL;
+ *   expanded_row_idx int32 [T*k]
+ * K from 1 to 2^24, T*k < 2^31, any alignment of whole elements.  out overlaps no
+ * input (MX_ERR_INVALID_ARG).
+ */
+int moe_unpermute(const void* y, int type, const float* topk_w,
+                  const int32_t* expanded_row_idx, int64_t T, int64_t K,
+                  int64_t k, int64_t M, void* out, void* stream);
+
+/*
+ * The gradients of moe_unpermute (and of moe_finalize), for p =
+ * expanded_row_idx[t*k+j]:
+ *   dy[p, :] = round( w[t, j] * dout[t, :] )            w = 1 with a NULL topk_w
+ *   dw[t, j] = sum_c dout[t, c] * y[p, c]  in fp32      (0 where p is no row)
+ *   dout [T, K], y and dy [M, K] of `type`; y may be NULL when dw is; dw fp32
+ *   [T, k] or NULL.
+ * Rows of dy that no entry names are left as they are, so the entries within
+ * [0, M) have to be distinct, as moe_permute makes them (of a row named twice the
+ * contents are unspecified).  Limits, alignment and overlaps as moe_unpermute.
+ */
+int moe_unpermute_backward(const void* dout, int type, const void* y,
+                           const float* topk_w, const int32_t* expanded_row_idx,
+                           int64_t T, int64_t K, int64_t k, int64_t M, void* dy,
+                           float* dw, void* stream);
 
 /* Description of the last non-OK status returned on this thread. */
 const char* mx_last_error(void);

@@ -7,8 +7,8 @@ current stream); outputs are allocated here when not passed in.  Any non-OK
 status from the library raises ``MxError`` with the library's message.
 
 Formats (see include/mxmoe.h): e4m3 payloads and e8m0 scales are uint8
-tensors; scales use the pair-split layout [rows, ceil(cols/64), 2]; bf16
-tensors are torch.bfloat16; group lists are int64 (type 1 = counts,
+tensors; scales use the pair-split layout [rows, ceil(cols/64), 2]; int8 codes
+are torch.int8 with fp32 scales per row; bf16 tensors are torch.bfloat16; group lists are int64 (type 1 = counts,
 type 0 = inclusive cumulative counts).
 """
 
@@ -26,6 +26,8 @@ __all__ = [
     "linear_workspace_size", "mx_quantize_fp4", "moe_route_quant_noalloc", "mx_pack_weights", "route_set_wait_limit",
     "gmm_swiglu_mxquant_packed", "gmm_mx_packed", "moe_mxfp8_forward_packed", "gmm_mx_w4a8", "gmm_swiglu_mxquant_w4a8", "moe_w4a8_forward",
     "mx_linear_fused", "linear_fused_workspace_size", "linear_fused_kernel", "mx_add_rmsnorm", "moe_route_mx", "moe_mxfp8_forward_mx",
+    "int8_quantize", "int8_linear", "int8_linear_workspace_size", "gmm_int8", "moe_permute", "moe_unpermute",
+    "moe_unpermute_backward",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -85,6 +87,13 @@ def load():
         "mx_linear_fused_workspace_size": (SZ, [I64, I64, I64, I32]),
         "mx_linear_fused_kernel": (I32, [I64, I64, I64, I32]),
         "mx_linear_fused": (I32, [P, P, P, P, P, I32, I32, P, I64, I64, I64, P, P, P, P, SZ, P]),
+        "int8_quantize": (I32, [P, I64, I64, I64, P, P, P]),
+        "int8_linear_workspace_size": (SZ, [I64, I64, I64, I32]),
+        "int8_linear": (I32, [P, P, P, P, P, I32, I32, P, I64, I64, I64, P, P, SZ, P]),
+        "gmm_int8": (I32, [P, P, P, P, P, I32, I32, I64, I64, I64, I64, P, P]),
+        "moe_permute": (I32, [P, I64, I64, P, P, I64, I64, I64, I64, P, P, P, P, P, P, SZ, P]),
+        "moe_unpermute": (I32, [P, I32, P, P, I64, I64, I64, I64, P, P]),
+        "moe_unpermute_backward": (I32, [P, I32, P, P, P, I64, I64, I64, I64, P, P, P]),
         "mx_last_error": (ctypes.c_char_p, []),
     }
     for name, (res, args) in sig.items():
@@ -878,3 +887,297 @@ def mx_linear_fused(x, w, w_s, x_s=None, bias=None, act="none", residual=None, q
     if rc:
         _check(rc, "mx_linear_fused")
     return (yq, ys) if quantize_out else y
+
+
+_I8, _I32 = torch.int8, torch.int32
+
+
+def int8_quantize(x, out=None, stream=None):
+    """bf16 rows [..., K] (rows may be strided) to int8 with one fp32 scale per
+    row: s = max(amax / 127, 2^-126), q = round(x / s), in the fp32 steps that
+    include/mxmoe.h gives.  The tokens of int8_linear and gmm_int8, or their
+    weights at load time ([N, K], [E, N, K]: a scale per output channel).
+    Returns (q int8 [..., K], s fp32 [...]); ``out`` gives the two instead."""
+    if type(x) is not _Tensor or x.dtype is not _BF16:
+        _need(x, _BF16, "x")
+    shape, dev = x.shape, x.device
+    if x.is_cuda:   # before _rows, whose copy of strided leading dims belongs to the stream of the call
+        there = _elsewhere(dev, stream)
+        if there is not None:
+            with there:
+                return int8_quantize(x, out)
+    if not shape or shape[-1] == 0:
+        raise ValueError("x must have at least one element per row")
+    x2, ldx = _rows(x, "x")
+    if out is not None:
+        q, s = out
+        _need_like(q, shape, "q", _I8, dev)
+        _need_like(s, shape[:-1], "s", _F32, dev)
+    _need_gpu(x, "x")
+    if out is None:
+        q = torch.empty(shape, dtype=_I8, device=dev)
+        s = torch.empty(shape[:-1], dtype=_F32, device=dev)
+    rc = load().int8_quantize(x2.data_ptr(), x2.shape[0], shape[-1], ldx, q.data_ptr(), s.data_ptr(),
+                              _raw_stream(dev.index))
+    if rc:
+        _check(rc, "int8_quantize")
+    return q, s
+
+
+def int8_linear_workspace_size(T, K, N, x_is_int8):
+    return int(load().int8_linear_workspace_size(T, K, N, int(x_is_int8)))
+
+
+def int8_linear(x, w, w_s, x_s=None, bias=None, act="none", residual=None, out=None, workspace=None, stream=None):
+    """Dense INT8 linear with its epilogue: act((x . w^T) x_s w_s + bias) +
+    residual, the product exact, the rest in fp32 and rounded once.
+
+    x: bf16 [T, K], or int8 [T, K] with x_s fp32 [T]; w, w_s: int8 [N, K], fp32
+    [N] (as int8_quantize makes them); bias: bf16 or fp32 [N]; act: a key of
+    ACTIVATIONS; residual: bf16 [T, N].  Returns y bf16 [T, N]; ``out`` gives it
+    instead (and may be the residual)."""
+    int8_in = x_s is not None
+    _need(x, _I8 if int8_in else _BF16, "x", 2)
+    if type(w) is not _Tensor or w.dim() != 2:
+        _need(w, _I8, "w", 2)
+    T, K = x.shape
+    N = w.shape[0]
+    dev = x.device
+    if not x.is_contiguous():
+        raise ValueError("x must be contiguous")
+    if int8_in:
+        _need_like(x_s, (T,), "x_s", _F32, dev)
+    _need_like(w, (N, K), "w", _I8, dev)
+    _need_like(w_s, (N,), "w_s", _F32, dev)
+    btype = TYPE_BF16
+    if bias is not None:
+        if isinstance(bias, _Tensor) and bias.dtype is _F32:
+            btype = TYPE_F32
+        _need_like(bias, (N,), "bias", _F32 if btype else _BF16, dev)
+    if act not in ACTIVATIONS:
+        raise ValueError(f"act must be one of {', '.join(ACTIVATIONS)}, got {act!r}")
+    if residual is not None:
+        _need_like(residual, (T, N), "residual", _BF16, dev)
+    if out is not None:
+        _need_like(out, (T, N), "out", _BF16, dev)
+    lib = load()
+    need = 0 if int8_in else lib.int8_linear_workspace_size(T, K, N, 0)
+    if workspace is not None:
+        _need_workspace(workspace, need, dev)
+    _need_gpu(x, "x")
+    there = _elsewhere(dev, stream)
+    if there is not None:
+        with there:
+            return int8_linear(x, w, w_s, x_s, bias, act, residual, out, workspace)
+    if workspace is None and need:
+        workspace = torch.empty(need, dtype=_U8, device=dev)
+    if out is None:
+        out = torch.empty((T, N), dtype=_BF16, device=dev)
+    rc = lib.int8_linear(x.data_ptr(), _addr(x_s), w.data_ptr(), w_s.data_ptr(), _addr(bias), btype, ACTIVATIONS[act],
+                         _addr(residual), T, K, N, out.data_ptr(), _addr(workspace),
+                         0 if workspace is None else workspace.numel(), _raw_stream(dev.index))
+    if rc:
+        _check(rc, "int8_linear")
+    return out
+
+
+def gmm_int8(a, a_s, w, w_s, group_list, group_list_type=GROUP_COUNT, swiglu=False, out=None, stream=None):
+    """Grouped INT8 product of rows sorted by expert: a int8 [M, K], a_s fp32 [M],
+    w int8 [E, N, K], w_s fp32 [E, N], group_list int64 [E].  With ``swiglu`` w
+    holds 2 N rows per expert, gate then up, and y = silu(gate) * up.  Returns y
+    bf16 [M, N]; rows that no expert owns are not written."""
+    _need(a, _I8, "a", 2)
+    _need(w, _I8, "w", 3)
+    M, K = a.shape
+    E, rows = w.shape[:2]
+    if swiglu and rows % 2:
+        raise ValueError(f"w must be [E, 2N, {K}] with swiglu, got {tuple(w.shape)}")
+    N = rows // 2 if swiglu else rows
+    dev = a.device
+    if not a.is_contiguous():
+        raise ValueError("a must be contiguous")
+    _need_like(a_s, (M,), "a_s", _F32, dev)
+    _need_like(w, (E, rows, K), "w", _I8, dev)
+    _need_like(w_s, (E, rows), "w_s", _F32, dev)
+    _need_like(group_list, (E,), "group_list", torch.int64, dev)
+    if out is not None:
+        _need_like(out, (M, N), "out", _BF16, dev)
+    _need_gpu(a, "a")
+    there = _elsewhere(dev, stream)
+    if there is not None:
+        with there:
+            return gmm_int8(a, a_s, w, w_s, group_list, group_list_type, swiglu, out)
+    if out is None:
+        out = torch.empty((M, N), dtype=_BF16, device=dev)
+    rc = load().gmm_int8(a.data_ptr(), a_s.data_ptr(), w.data_ptr(), w_s.data_ptr(), group_list.data_ptr(),
+                         group_list_type, 1 if swiglu else 0, M, N, K, E, out.data_ptr(), _raw_stream(dev.index))
+    if rc:
+        _check(rc, "gmm_int8")
+    return out
+
+
+def moe_permute(x, topk_ids, E, x_s=None, out=None, workspace=None, stream=None):
+    """Token rows sorted by expert, as they are: x [T, K] of any type of 1, 2 or 4
+    bytes (rows may be strided), topk_ids int32 [T, k]; x_s fp32 [T] (the scales
+    of int8 rows) goes along.  Returns (xp [T*k, K], xp_s [T*k] or None,
+    sorted_row, expanded_row_idx, group_list), the maps as moe_route_quant's;
+    ``out`` gives the five instead.  Rows behind the last expert's (ids outside
+    [0, E) are dropped) stay as they are.  Its gradient with respect to x is
+    moe_unpermute of xp's gradient, without weights."""
+    if not isinstance(x, _Tensor):
+        _need(x, None, "x")
+    if x.dim() != 2:
+        raise ValueError(f"x must have 2 dims, got {x.dim()}")
+    size = x.element_size()
+    if size not in (1, 2, 4) or x.is_complex():
+        raise TypeError(f"x must be of a type of 1, 2 or 4 bytes, got {x.dtype}")
+    if type(topk_ids) is not _Tensor or topk_ids.dim() != 2:
+        _need(topk_ids, _I32, "topk_ids", 2)
+    T, K = x.shape
+    if K == 0:
+        raise ValueError("x must have at least one element per row")
+    k = topk_ids.shape[1]
+    M = T * k
+    dev = x.device
+    x2, ldx = _rows(x, "x")
+    _need_like(topk_ids, (T, k), "topk_ids", _I32, dev)
+    if x_s is not None:
+        _need_like(x_s, (T,), "x_s", _F32, dev)
+    if out is not None:
+        xp, xps, sr, eri, gl = out
+        _need_like(xp, (M, K), "xp", x.dtype, dev)
+        if (xps is None) != (x_s is None):
+            raise ValueError("xp_s goes with x_s")
+        if xps is not None:
+            _need_like(xps, (M,), "xp_s", _F32, dev)
+        _need_like(sr, (M,), "sorted_row", _I32, dev)
+        _need_like(eri, (M,), "expanded_row_idx", _I32, dev)
+        _need_like(gl, (E,), "group_list", torch.int64, dev)
+    lib = load()
+    need = lib.moe_route_quant_workspace_size(T, k, E)
+    if workspace is not None:
+        _need_workspace(workspace, need, dev)
+    _need_gpu(x, "x")
+    there = _elsewhere(dev, stream)
+    if there is not None:
+        with there:
+            return moe_permute(x, topk_ids, E, x_s, out, workspace)
+    if out is None:
+        xp = torch.empty((M, K), dtype=x.dtype, device=dev)
+        xps = torch.empty(M, dtype=_F32, device=dev) if x_s is not None else None
+        sr = torch.empty(M, dtype=_I32, device=dev)
+        eri = torch.empty(M, dtype=_I32, device=dev)
+        gl = torch.empty(E, dtype=torch.int64, device=dev)
+    if workspace is None and need:
+        workspace = torch.empty(need, dtype=_U8, device=dev)
+    rc = lib.moe_permute(x2.data_ptr(), ldx, size, _addr(x_s), topk_ids.data_ptr(), T, K, k, E, xp.data_ptr(),
+                         _addr(xps), sr.data_ptr(), eri.data_ptr(), gl.data_ptr(), _addr(workspace),
+                         0 if workspace is None else workspace.numel(), _raw_stream(dev.index))
+    if rc:
+        _check(rc, "moe_permute")
+    return xp, xps, sr, eri, gl
+
+
+TYPE_F16 = 2
+_ROW_TYPES = {torch.bfloat16: TYPE_BF16, torch.float32: TYPE_F32, torch.float16: TYPE_F16}
+
+
+def _row_type(t, name):
+    """The rows' type by number."""
+    kind = _ROW_TYPES.get(t.dtype) if isinstance(t, _Tensor) else None
+    if kind is None:
+        if not isinstance(t, _Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+        raise TypeError(f"{name} must be bfloat16, float16 or float32, got {t.dtype}")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must have 2 dims, got {t.dim()}")
+    if t.shape[1] == 0:
+        raise ValueError(f"{name} must have at least one element per row")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return kind
+
+
+def _tokens(expanded_row_idx, k, dev):
+    """T of expanded_row_idx [T*k] (of any shape)."""
+    if not isinstance(k, int) or k <= 0:
+        raise ValueError(f"k must be a positive int, got {k!r}")
+    _need(expanded_row_idx, _I32, "expanded_row_idx")
+    n = expanded_row_idx.numel()
+    if n % k:
+        raise ValueError(f"expanded_row_idx must hold T*k entries, got {n} with k = {k}")
+    _need_like(expanded_row_idx, expanded_row_idx.shape, "expanded_row_idx", _I32, dev)
+    return n // k
+
+
+def moe_unpermute(y, expanded_row_idx, k, topk_w=None, out=None, stream=None):
+    """Expert rows back to their tokens: out[t] = sum_j topk_w[t, j] *
+    y[expanded_row_idx[t*k+j]], in fp32 and rounded once; without weights their
+    plain sum (the gradient of moe_permute).  y: bf16, fp16 or fp32 [M, K] of any
+    K; topk_w: fp32 [T, k].  Entries outside [0, M) are skipped.  Returns out
+    [T, K] of y's type."""
+    kind = _row_type(y, "y")
+    M, K = y.shape
+    dev = y.device
+    T = _tokens(expanded_row_idx, k, dev)
+    if topk_w is not None:
+        _need_like(topk_w, (T, k), "topk_w", _F32, dev)
+    if out is not None:
+        _need_like(out, (T, K), "out", y.dtype, dev)
+    _need_gpu(y, "y")
+    there = _elsewhere(dev, stream)
+    if there is not None:
+        with there:
+            return moe_unpermute(y, expanded_row_idx, k, topk_w, out)
+    if out is None:
+        out = torch.empty((T, K), dtype=y.dtype, device=dev)
+    rc = load().moe_unpermute(y.data_ptr(), kind, _addr(topk_w), expanded_row_idx.data_ptr(), T, K, k, M,
+                              out.data_ptr(), _raw_stream(dev.index))
+    if rc:
+        _check(rc, "moe_unpermute")
+    return out
+
+
+def moe_unpermute_backward(dout, expanded_row_idx, k, topk_w=None, y=None, out=None, stream=None):
+    """The gradients of moe_unpermute (and moe_finalize): dy[p] = topk_w[t, j] *
+    dout[t] for p = expanded_row_idx[t*k+j], and with ``y`` also dw[t, j] =
+    <dout[t], y[p]> in fp32 (0 for a dropped entry).  dout [T, K] and y [M, K]:
+    bf16, fp16 or fp32; M = T*k without y.  Returns (dy [M, K], dw [T, k] or
+    None); ``out`` gives the two instead.  Rows that no entry names are zeros in a
+    dy made here and stay as they are in one given."""
+    kind = _row_type(dout, "dout")
+    K = dout.shape[1]
+    dev = dout.device
+    T = _tokens(expanded_row_idx, k, dev)
+    if dout.shape[0] != T:
+        raise ValueError(f"dout must have {T} rows, got {dout.shape[0]}")
+    if topk_w is not None:
+        _need_like(topk_w, (T, k), "topk_w", _F32, dev)
+    M = T * k
+    if y is not None:
+        _row_type(y, "y")
+        M = y.shape[0]
+        _need_like(y, (M, K), "y", dout.dtype, dev)
+    if out is not None:
+        dy, dw = out
+        if y is None:
+            _need(dy, dout.dtype, "dy", 2)
+            M = dy.shape[0]
+        _need_like(dy, (M, K), "dy", dout.dtype, dev)
+        if (dw is None) != (y is None):
+            raise ValueError("dw goes with y")
+        if dw is not None:
+            _need_like(dw, (T, k), "dw", _F32, dev)
+    _need_gpu(dout, "dout")
+    there = _elsewhere(dev, stream)
+    if there is not None:
+        with there:
+            return moe_unpermute_backward(dout, expanded_row_idx, k, topk_w, y, out)
+    if out is None:
+        dy = torch.zeros((M, K), dtype=dout.dtype, device=dev)
+        dw = torch.empty((T, k), dtype=_F32, device=dev) if y is not None else None
+    rc = load().moe_unpermute_backward(dout.data_ptr(), kind, _addr(y), _addr(topk_w), expanded_row_idx.data_ptr(), T,
+                                       K, k, M, dy.data_ptr(), _addr(dw), _raw_stream(dev.index))
+    if rc:
+        _check(rc, "moe_unpermute_backward")
+    return dy, dw

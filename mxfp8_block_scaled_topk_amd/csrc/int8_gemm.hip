@@ -1,0 +1,289 @@
+// int8_linear and gmm_int8: products of int8 rows with fp32 scales per token and
+// per output channel,
+//
+//   z[t, n] = (sum_k xq[t, k] wq[n, k]) xs[t] ws[n]
+//
+// the sum exact in int32 (K < 2^17).
+#include <algorithm>
+
+#include "linear_fused.h"
+
+namespace mxmoe {
+
+int launch_int8_quantize(const uint16_t* x, int64_t rows, int64_t kd, int64_t ld, int8_t* q, float* s,
+                         hipStream_t stream);
+
+namespace {
+
+typedef int v4i __attribute__((ext_vector_type(4)));
+typedef int v16i __attribute__((ext_vector_type(16)));
+
+constexpr int kMaxE = 1024;
+constexpr int64_t kMaxK = ((int64_t)1 << 17) - 16;
+
+struct Int8Params {
+  LinParams e;           // sizes and the epilogue's operands
+  const int8_t* x;       // [M, K]
+  const float* xs;       // [M]
+  const int8_t* w;       // [E, rows, K]
+  const float* ws;       // [E, rows]
+  const int64_t* gl;     // [E], or null: one group of all rows
+  int gl_type, E;
+  int64_t rows;          // weight rows per expert (2 N with swiglu)
+  int swiglu;
+};
+
+constexpr int kBN = 64, kBM = 64, kBK = 64, kPitch = 80;
+
+__global__ __launch_bounds__(256) void int8_simple_kernel(Int8Params p) {
+  __shared__ __attribute__((aligned(16))) int8_t sa[kBN * kPitch];
+  __shared__ __attribute__((aligned(16))) int8_t sb[kBM * kPitch];
+  __shared__ int64_t s_row0[kMaxE + 1];
+  __shared__ int s_tile0[kMaxE + 1];
+  __shared__ float part[4 * 32 * 36];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int li = lane & 31, lg = lane >> 5;
+  const int E = p.gl ? p.E : 1;
+  if (tid == 0) {
+    int64_t run = 0;
+    int tiles = 0;
+    for (int e = 0; e < E; ++e) {
+      int64_t n = !p.gl ? p.e.T : p.gl_type == 1 ? p.gl[e] : p.gl[e] - (e ? p.gl[e - 1] : 0);
+      n = std::min<int64_t>(std::max<int64_t>(n, 0), p.e.T - run);
+      s_row0[e] = run;
+      s_tile0[e] = tiles;
+      tiles += (int)((n + kBM - 1) / kBM);
+      run += n;
+    }
+    s_row0[E] = run;
+    s_tile0[E] = tiles;
+  }
+  __syncthreads();
+  const int64_t N = p.e.N, K = p.e.K;
+  const int tile_n = p.swiglu ? kBN / 2 : kBN;
+  const int64_t n_tiles = (N + tile_n - 1) / tile_n;
+  const int64_t total = s_tile0[E] * n_tiles;
+  for (int64_t tile = blockIdx.x; tile < total; tile += gridDim.x) {
+    const int mt = (int)(tile / n_tiles);
+    const int64_t n0 = (tile % n_tiles) * tile_n;
+    int e = 0;
+    while (s_tile0[e + 1] <= mt) ++e;
+    const int64_t m0 = s_row0[e] + (int64_t)(mt - s_tile0[e]) * kBM, m1 = s_row0[e + 1];
+    v16i acc[2] = {};   // swiglu: gate and up
+    const int wn = wave & 1, wm = wave >> 1;
+    for (int64_t k0 = 0; k0 < K; k0 += kBK) {
+      __syncthreads();
+      const int r = tid >> 2, c = tid & 3;
+      uint4 ua = make_uint4(0, 0, 0, 0), ub = ua;
+      if (k0 + 16 * c < K) {
+        const int64_t n = p.swiglu ? n0 + (r & 31) : n0 + r;
+        const int64_t wr = n + (p.swiglu && r >= 32 ? N : 0);
+        if (n < N) ua = *reinterpret_cast<const uint4*>(p.w + (e * p.rows + wr) * K + k0 + 16 * c);
+        if (m0 + r < m1) ub = *reinterpret_cast<const uint4*>(p.x + (m0 + r) * K + k0 + 16 * c);
+      }
+      *reinterpret_cast<uint4*>(sa + r * kPitch + 16 * c) = ua;
+      *reinterpret_cast<uint4*>(sb + r * kPitch + 16 * c) = ub;
+      __syncthreads();
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        const v4i b = *reinterpret_cast<const v4i*>(sb + (32 * wm + li) * kPitch + 32 * s + 16 * lg);
+        if (p.swiglu) {
+          if (wn == 0)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const v4i a = *reinterpret_cast<const v4i*>(sa + (32 * h + li) * kPitch + 32 * s + 16 * lg);
+              acc[h] = __builtin_amdgcn_mfma_i32_32x32x32_i8(a, b, acc[h], 0, 0, 0);
+            }
+        } else {
+          const v4i a = *reinterpret_cast<const v4i*>(sa + (32 * wn + li) * kPitch + 32 * s + 16 * lg);
+          acc[0] = __builtin_amdgcn_mfma_i32_32x32x32_i8(a, b, acc[0], 0, 0, 0);
+        }
+      }
+    }
+    // lane: token li, features 8 q + 4 lg + i of the wave's 32
+    const int64_t m = m0 + 32 * wm + li;
+    const float xs = m < m1 ? p.xs[m] : 0.0f;
+    float* mine = part + wave * 32 * 36;
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int f = 8 * q + 4 * lg + i;
+        const int64_t n = n0 + (p.swiglu ? 0 : 32 * wn) + f;
+        float z = 0.0f;
+        if (n < N) {
+          z = (float)acc[0][4 * q + i] * xs * p.ws[e * p.rows + n];
+          if (p.swiglu) {
+            const float u = (float)acc[1][4 * q + i] * xs * p.ws[e * p.rows + N + n];
+            z = z * __builtin_amdgcn_rcpf(1.0f + __expf(-z)) * u;
+          }
+        }
+        mine[li * 36 + f] = z;
+      }
+    __syncthreads();
+    for (int u0 = 0; u0 < 32; u0 += 16) {
+      if (p.swiglu && wn == 1) break;
+      const int tl = u0 + (lane >> 2);
+      const int64_t t = m0 + 32 * wm + tl, n = n0 + (p.swiglu ? 0 : 32 * wn) + 8 * (lane & 3);
+      const int cnt = t < m1 ? (int)std::min<int64_t>(N - n, 8) : 0;
+      float z[8], b[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) z[i] = mine[tl * 36 + 8 * (lane & 3) + i];
+      uint4 res = make_uint4(0, 0, 0, 0);
+      epilogue_bias(p.e, n, cnt, b);
+      if (p.e.res && cnt > 0) res = load_res8<false>(p.e.res + t * N + n, cnt);
+      epilogue8(p.e, Place{t * N + n, 0, 0, 0}, n, cnt, b, res, z);
+    }
+  }
+}
+
+int launch_int8(const Int8Params& p, hipStream_t stream, const char* name) {
+  const int64_t n_tiles = (p.e.N + (p.swiglu ? kBN / 2 : kBN) - 1) / (p.swiglu ? kBN / 2 : kBN);
+  const int64_t upper = ((p.e.T + kBM - 1) / kBM + (p.gl ? p.E : 0)) * n_tiles;
+  int8_simple_kernel<<<dim3((unsigned)std::min<int64_t>(upper, 256 * 8)), dim3(256), 0, stream>>>(p);
+  return check_launch(name);
+}
+
+bool too_many_tiles(int64_t T, int64_t N) { return ((T + 31) / 32) * ((N + 31) / 32) >= (int64_t)1 << 30; }
+
+int check_sizes(const char* name, int64_t T, int64_t K, int64_t N) {
+  if (T < 0 || K <= 0 || N <= 0)
+    return fail(MX_ERR_INVALID_ARG, "%s: bad sizes rows=%lld K=%lld N=%lld", name, (long long)T, (long long)K,
+                (long long)N);
+  if (!dims_in_range({T, 2 * std::min<int64_t>(N, kMaxDim)}))
+    return fail(MX_ERR_UNSUPPORTED, "%s: rows above 2^31 - 1 or N above 2^30 - 1", name);
+  if (K % 16 != 0) return fail(MX_ERR_UNSUPPORTED, "%s: K=%lld is not a multiple of 16", name, (long long)K);
+  if (K > kMaxK) return fail(MX_ERR_UNSUPPORTED, "%s: K=%lld >= 2^17", name, (long long)K);
+  if (too_many_tiles(T, N)) return fail(MX_ERR_UNSUPPORTED, "%s: 2^30 or more tiles of 32 x 32 outputs", name);
+  return MX_OK;
+}
+
+// Workspace: the int8 form of bf16 tokens.
+struct Int8Layout {
+  size_t xs, total;
+};
+Int8Layout int8_layout(int64_t T, int64_t K, int x_is_int8) {
+  if (x_is_int8) return {0, 0};
+  const size_t xs = align_up((size_t)(T * K), 256);
+  return {xs, xs + align_up((size_t)T * 4, 256)};
+}
+
+}  // namespace
+
+}  // namespace mxmoe
+
+extern "C" size_t int8_linear_workspace_size(int64_t T, int64_t K, int64_t N, int x_is_int8) {
+  // 0 for sizes int8_linear rejects
+  if (mxmoe::check_sizes("int8_linear", T, K, N) != MX_OK) return 0;
+  return mxmoe::int8_layout(T, K, x_is_int8).total;
+}
+
+extern "C" int int8_linear(const void* x, const float* x_s, const void* w_i8, const float* w_s, const void* bias,
+                           int bias_type, int activation, const void* residual_bf16, int64_t T, int64_t K, int64_t N,
+                           void* y_bf16, void* workspace, size_t ws_bytes, void* stream) {
+  using namespace mxmoe;
+  int rc = check_sizes("int8_linear", T, K, N);
+  if (rc) return rc;
+  if (bias && bias_type != MX_TYPE_BF16 && bias_type != MX_TYPE_F32)
+    return fail(MX_ERR_INVALID_ARG, "int8_linear: bias_type must be MX_TYPE_BF16 or MX_TYPE_F32, got %d", bias_type);
+  if (activation < MX_ACT_NONE || activation > MX_ACT_GELU_TANH)
+    return fail(MX_ERR_INVALID_ARG, "int8_linear: unknown activation %d", activation);
+  const bool int8_in = x_s != nullptr;
+  const Int8Layout L = int8_layout(T, K, int8_in);
+  if (T > 0 && (!x || !w_i8 || !w_s || !y_bf16 || (L.total > 0 && !workspace)))
+    return fail(MX_ERR_INVALID_ARG, "int8_linear: null pointer");
+  if (ws_bytes < L.total)
+    return fail(MX_ERR_WORKSPACE, "int8_linear: workspace %zu bytes < %zu", ws_bytes, L.total);
+  if (reinterpret_cast<uintptr_t>(x) % (int8_in ? 16 : 2) || reinterpret_cast<uintptr_t>(w_i8) % 16 ||
+      reinterpret_cast<uintptr_t>(x_s) % 4 || reinterpret_cast<uintptr_t>(w_s) % 4 ||
+      reinterpret_cast<uintptr_t>(bias) % (bias_type == MX_TYPE_F32 ? 4 : 2) ||
+      reinterpret_cast<uintptr_t>(residual_bf16) % 2 || reinterpret_cast<uintptr_t>(y_bf16) % 2 ||
+      (L.total > 0 && reinterpret_cast<uintptr_t>(workspace) % 256))
+    return fail(MX_ERR_UNSUPPORTED, "int8_linear: misaligned pointer");
+  if (T == 0) return MX_OK;
+  // Outputs overlap nothing, except that y may take the residual's place.
+  const uint64_t dense = (uint64_t)T * (uint64_t)N * 2;
+  const Span in[7] = {{x, (uint64_t)T * (uint64_t)K * (int8_in ? 1 : 2)},
+                      {x_s, (uint64_t)T * 4},
+                      {w_i8, (uint64_t)N * (uint64_t)K},
+                      {w_s, (uint64_t)N * 4},
+                      {bias, (uint64_t)N * (bias_type == MX_TYPE_F32 ? 4 : 2)},
+                      {workspace, L.total},
+                      {residual_bf16, dense}};
+  for (int i = 0; i < 7; ++i) {
+    if (overlaps({y_bf16, dense}, in[i]) && !(i == 6 && y_bf16 == residual_bf16))
+      return fail(MX_ERR_INVALID_ARG, "int8_linear: the output overlaps an input or the workspace");
+    if (i != 5 && overlaps(in[5], in[i]))
+      return fail(MX_ERR_INVALID_ARG, "int8_linear: the workspace overlaps an input");
+  }
+  Int8Params p{};
+  p.e.T = T;
+  p.e.K = K;
+  p.e.N = N;
+  p.e.bias = bias;
+  p.e.bias_f32 = bias_type == MX_TYPE_F32;
+  p.e.act = activation;
+  p.e.res = static_cast<const uint16_t*>(residual_bf16);
+  p.e.y = static_cast<uint16_t*>(y_bf16);
+  p.w = static_cast<const int8_t*>(w_i8);
+  p.ws = w_s;
+  p.rows = N;
+  hipStream_t s = as_stream(stream);
+  if (int8_in) {
+    p.x = static_cast<const int8_t*>(x);
+    p.xs = x_s;
+  } else {
+    int8_t* xq = static_cast<int8_t*>(workspace);
+    float* xs = reinterpret_cast<float*>(static_cast<char*>(workspace) + L.xs);
+    rc = launch_int8_quantize(static_cast<const uint16_t*>(x), T, K, K, xq, xs, s);
+    if (rc) return rc;
+    p.x = xq;
+    p.xs = xs;
+  }
+  return launch_int8(p, s, "int8_linear");
+}
+
+extern "C" int gmm_int8(const void* a_i8, const float* a_s, const void* w_i8, const float* w_s,
+                        const int64_t* group_list, int group_list_type, int swiglu, int64_t M, int64_t N, int64_t K,
+                        int64_t E, void* y_bf16, void* stream) {
+  using namespace mxmoe;
+  int rc = check_sizes("gmm_int8", M, K, N);
+  if (rc) return rc;
+  if (E <= 0) return fail(MX_ERR_INVALID_ARG, "gmm_int8: bad E=%lld", (long long)E);
+  if (E > kMaxE) return fail(MX_ERR_UNSUPPORTED, "gmm_int8: E=%lld > %d", (long long)E, kMaxE);
+  // (an expert's last tile may be partly empty: E more rows of tiles)
+  if (too_many_tiles(M + 32 * E, N))
+    return fail(MX_ERR_UNSUPPORTED, "gmm_int8: 2^30 or more tiles of 32 x 32 outputs");
+  if (group_list_type != 0 && group_list_type != 1)
+    return fail(MX_ERR_INVALID_ARG, "gmm_int8: group_list_type must be 0 (cumulative) or 1 (count), got %d",
+                group_list_type);
+  if (!group_list || (M > 0 && (!a_i8 || !a_s || !w_i8 || !w_s || !y_bf16)))
+    return fail(MX_ERR_INVALID_ARG, "gmm_int8: null pointer");
+  if (reinterpret_cast<uintptr_t>(a_i8) % 16 || reinterpret_cast<uintptr_t>(w_i8) % 16 ||
+      reinterpret_cast<uintptr_t>(a_s) % 4 || reinterpret_cast<uintptr_t>(w_s) % 4 ||
+      reinterpret_cast<uintptr_t>(group_list) % 8 || reinterpret_cast<uintptr_t>(y_bf16) % 2)
+    return fail(MX_ERR_UNSUPPORTED, "gmm_int8: misaligned pointer");
+  if (M == 0) return MX_OK;
+  const int64_t rows = swiglu ? 2 * N : N;
+  const Span in[5] = {{a_i8, (uint64_t)M * (uint64_t)K}, {a_s, (uint64_t)M * 4},
+                      {w_i8, (uint64_t)E * (uint64_t)rows * (uint64_t)K}, {w_s, (uint64_t)E * (uint64_t)rows * 4},
+                      {group_list, (uint64_t)E * 8}};
+  for (const Span& i : in)
+    if (overlaps({y_bf16, (uint64_t)M * (uint64_t)N * 2}, i))
+      return fail(MX_ERR_INVALID_ARG, "gmm_int8: the output overlaps an input");
+  Int8Params p{};
+  p.e.T = M;
+  p.e.K = K;
+  p.e.N = N;
+  p.e.y = static_cast<uint16_t*>(y_bf16);
+  p.x = static_cast<const int8_t*>(a_i8);
+  p.xs = a_s;
+  p.w = static_cast<const int8_t*>(w_i8);
+  p.ws = w_s;
+  p.gl = group_list;
+  p.gl_type = group_list_type;
+  p.E = (int)E;
+  p.rows = rows;
+  p.swiglu = swiglu != 0;
+  return launch_int8(p, as_stream(stream), "gmm_int8");
+}

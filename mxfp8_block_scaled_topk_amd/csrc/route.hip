@@ -84,6 +84,10 @@ struct RouteParams {
   const uint16_t* x;     // bf16 rows (moe_route_quant)
   const uint8_t* mxq;    // MXFP8 rows and their scales (moe_route_mx)
   const uint8_t* mxs;
+  const uint8_t* rows;   // rows of any type (moe_permute), their stride in bytes
+  int64_t ld_bytes;
+  const float* row_s;    // a scale per token, or null
+  float* out_s;
   const int32_t* ids;
   uint8_t* xq;
   uint8_t* xs;
@@ -100,9 +104,10 @@ struct RouteParams {
   int k, E, nbits, tpc, nch, G, S;
   int split;            // scatter workgroups (shares) per chunk
   int nbuf;             // tokens of a share quantised into LDS before the wait
-  int row_bytes;        // LDS bytes per such token: K payload, then the scales, padded to 16
+  int row_bytes;        // LDS bytes per such token: K payload, then the scales, padded to 16 (moe_permute, where K
+                        // counts bytes: the row's 16-byte pieces)
   int lds_ints;         // dynamic LDS of the launch, in ints
-  int stream;           // moe_route_mx: the rows are over 128 MB, half the memory-side cache, and go past it
+  int stream;           // moe_route_mx, moe_permute: the rows are over 128 MB, half the memory-side cache, and go past it
                         // (measured: 16K tokens of 2048 to 8 experts, 268 MB, 77 -> 70 us; 2049 of 4096, 67 MB,
                         // would take 21.6 instead of 20.2)
   int scales16;         // xs rows can be written (and mxs rows read) 16 bytes at a time
@@ -269,11 +274,42 @@ __device__ __forceinline__ void quant_half_block(const RouteParams& p, int64_t t
   quant_half_regs(src[0], src[1], q, sb);
 }
 
+// What a launch does with the token rows: quantises bf16 (moe_route_quant), takes
+// MXFP8 and its scales (moe_route_mx), or moves rows of any type (moe_permute).
+constexpr int kRowsQuant = 0, kRowsMx = 1, kRowsAny = 2;
+
+// moe_permute's rows are K bytes on any boundary, in pieces of 16 (fewer in a row
+// of fewer): piece i starts at byte 16 i, a row's last one 16 bytes before its
+// end, so that some bytes may come twice.  In LDS piece i lies at 16 i.
+__device__ __forceinline__ int64_t piece_at(const RouteParams& p, int i) {
+  return p.K >= 16 ? std::min<int64_t>(16 * (int64_t)i, p.K - 16) : 0;
+}
+__device__ __forceinline__ u32x4_any load_piece(const RouteParams& p, const uint8_t* src) {
+  if (p.K >= 16) return *reinterpret_cast<const u32x4_any*>(src);
+  u32x4_any u = {0, 0, 0, 0};
+#pragma unroll
+  for (int b = 0; b < 15; ++b)
+    if (b < (int)p.K) u[b >> 2] |= (uint32_t)src[b] << (8 * (b & 3));
+  return u;
+}
+__device__ __forceinline__ void store_piece(const RouteParams& p, uint8_t* dst, const u32x4_any& u) {
+  if (p.K < 16) {
+#pragma unroll
+    for (int b = 0; b < 15; ++b)
+      if (b < (int)p.K) dst[b] = static_cast<uint8_t>(u[b >> 2] >> (8 * (b & 3)));
+  } else if (p.stream) {
+    __builtin_nontemporal_store(u, reinterpret_cast<u32x4_any*>(dst));
+  } else {
+    asm volatile("" ::: "memory");   // keeps the two stores apart: merged, the hint is lost
+    *reinterpret_cast<u32x4_any*>(dst) = u;
+  }
+}
+
 // 16 bytes from LDS to an output row; past the caches when they could not hold
 // the output anyway (see RouteParams::stream).
-template <bool kMx>
+template <int kRows>
 __device__ __forceinline__ void put16(uint8_t* dst, const uint8_t* src, int stream) {
-  if constexpr (kMx) {
+  if constexpr (kRows == kRowsMx) {
     typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
     if (stream) {
       __builtin_nontemporal_store(*reinterpret_cast<const u32x4*>(src), reinterpret_cast<u32x4*>(dst));
@@ -284,9 +320,8 @@ __device__ __forceinline__ void put16(uint8_t* dst, const uint8_t* src, int stre
   *reinterpret_cast<uint4*>(dst) = *reinterpret_cast<const uint4*>(src);
 }
 
-// kSingle: all assignments in one chunk (no leaders, no waits).  kMx: the
-// token rows are MXFP8 already.
-template <bool kSingle, bool kMx>
+// kSingle: all assignments in one chunk (no leaders, no waits).
+template <bool kSingle, int kRows>
 __global__ __launch_bounds__(kThreads) void route_quant_kernel(RouteParams p) {
   // dynamic LDS: [4E ints: per-wave expert counts, or a leader's chunk counts
   // (its whole LDS)] [kThreads ints: s_pos] [the share's quantised rows,
@@ -314,13 +349,14 @@ __global__ __launch_bounds__(kThreads) void route_quant_kernel(RouteParams p) {
     return;
   }
   constexpr bool single = kSingle;
+  constexpr bool kMx = kRows == kRowsMx, kAny = kRows == kRowsAny;
   int* s_wcnt = dyn;                 // [4][E]
   int* s_pos = dyn + 4 * E;          // [kThreads]
   uint8_t* xbuf = reinterpret_cast<uint8_t*>(dyn + 4 * E + kThreads);
   const int64_t M = p.T * p.k;
-  const int nb = (int)(p.K / 32);      // K <= 2^24: every in-row index below fits 32 bits
+  const int nb = (int)(p.K / 32);      // K <= 2^24 (kAny 2^26): every in-row index below fits 32 bits
   const int s_stride = ((nb + 1) / 2) * 2;
-  const int hpr = 2 * nb;              // half-blocks per token row
+  const int hpr = kAny ? (int)((p.K + 15) / 16) : 2 * nb;   // half-blocks per token row (kAny: pieces)
   int ready = single ? 1 : -1;   // block-uniform: -1 not yet waited, 1 counts published, 0 count here
 
   const int64_t w = (int64_t)blockIdx.x - p.S;   // (chunk c, share `part` of its tokens)
@@ -369,6 +405,27 @@ __global__ __launch_bounds__(kThreads) void route_quant_kernel(RouteParams p) {
   const int rowb = p.row_bytes;   // payload K bytes, then s_stride scale bytes, padded to 16
   const int n_it = nbt * hpr;     // half-blocks; even, so lane pairs stay together
   constexpr int kLd = 4;          // half-blocks whose loads a lane has in flight at once
+  if constexpr (kAny) {
+    for (int it0 = tid; it0 < n_it; it0 += kLd * kThreads) {
+      u32x4_any u[kLd];
+#pragma unroll
+      for (int i = 0; i < kLd; ++i) {
+        const int it = it0 + i * kThreads;
+        if (it < n_it) {
+          const int tl = it / hpr, hb = it - tl * hpr;
+          u[i] = load_piece(p, p.rows + (t0 + tb + tl) * p.ld_bytes + piece_at(p, hb));
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kLd; ++i) {
+        const int it = it0 + i * kThreads;
+        if (it < n_it) {
+          const int tl = it / hpr, hb = it - tl * hpr;
+          *reinterpret_cast<uint4*>(xbuf + tl * rowb + hb * 16) = make_uint4(u[i].x, u[i].y, u[i].z, u[i].w);
+        }
+      }
+    }
+  }
   if constexpr (kMx) {
     // a payload row is hpr 16-byte pieces
     typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));   // (an array of uint4 would go to scratch)
@@ -405,7 +462,7 @@ __global__ __launch_bounds__(kThreads) void route_quant_kernel(RouteParams p) {
       }
     }
   }
-  for (int it0 = tid; !kMx && it0 < n_it; it0 += kLd * kThreads) {
+  for (int it0 = tid; !kMx && !kAny && it0 < n_it; it0 += kLd * kThreads) {
     uint4 u[kLd][2];
 #pragma unroll
     for (int i = 0; i < kLd; ++i) {
@@ -527,13 +584,38 @@ __global__ __launch_bounds__(kThreads) void route_quant_kernel(RouteParams p) {
 
   // ---- stores: each buffered row to the token's k rows ---------------------
   const int k = p.k;
+  if constexpr (kAny) {
+    for (int idx = tid; idx < nbt * k * hpr; idx += kThreads) {
+      const int rowi = idx / hpr, ch = idx - rowi * hpr;
+      const int tl = rowi / k, j = rowi - tl * k;
+      const int r = s_pos[(tb + tl) * k + j];
+      if (r < 0) continue;
+      const uint4 u = *reinterpret_cast<const uint4*>(xbuf + tl * rowb + ch * 16);
+      store_piece(p, p.xq + (int64_t)r * p.K + piece_at(p, ch), u32x4_any{u.x, u.y, u.z, u.w});
+    }
+    if (p.row_s)
+      for (int idx = tid; idx < (te - tb) * k; idx += kThreads) {
+        const int r = s_pos[tb * k + idx];
+        if (r >= 0) p.out_s[r] = p.row_s[t0 + tb + idx / k];
+      }
+    // the share's tokens past the LDS budget
+    for (int64_t it = (int64_t)nbt * hpr + tid; it < (int64_t)(te - tb) * hpr; it += kThreads) {
+      const int tl = tb + (int)(it / hpr), hb = (int)(it % hpr);
+      const u32x4_any u = load_piece(p, p.rows + (t0 + tl) * p.ld_bytes + piece_at(p, hb));
+      for (int j = 0; j < k; ++j) {
+        const int r = s_pos[tl * k + j];
+        if (r >= 0) store_piece(p, p.xq + (int64_t)r * p.K + piece_at(p, hb), u);
+      }
+    }
+    return;
+  }
   const int n16 = (int)(p.K / 16);   // 16-byte pieces of a payload row
   for (int idx = tid; idx < nbt * k * n16; idx += kThreads) {
     const int rowi = idx / n16, ch = idx - rowi * n16;
     const int tl = rowi / k, j = rowi - tl * k;
     const int r = s_pos[(tb + tl) * k + j];
     if (r < 0) continue;
-    put16<kMx>(p.xq + (int64_t)r * p.K + ch * 16, xbuf + tl * rowb + ch * 16, p.stream);
+    put16<kRows>(p.xq + (int64_t)r * p.K + ch * 16, xbuf + tl * rowb + ch * 16, p.stream);
   }
   if (p.scales16) {
     const int s16 = s_stride / 16;
@@ -543,7 +625,7 @@ __global__ __launch_bounds__(kThreads) void route_quant_kernel(RouteParams p) {
       const int r = s_pos[(tb + tl) * k + j];
       if (r < 0) continue;
       // (only scale rows of whole lines go past the caches)
-      put16<kMx>(p.xs + (int64_t)r * s_stride + ch * 16, xbuf + tl * rowb + p.K + ch * 16, p.stream && s_stride % 128 == 0);
+      put16<kRows>(p.xs + (int64_t)r * s_stride + ch * 16, xbuf + tl * rowb + p.K + ch * 16, p.stream && s_stride % 128 == 0);
     }
   } else {
     for (int idx = tid; idx < nbt * k * s_stride; idx += kThreads) {
@@ -643,13 +725,14 @@ size_t route_workspace_bytes(int64_t T, int64_t k, int64_t E) {
          align_up((size_t)(s.S + 1) * 8, 256);
 }
 
-int check_route_args(int64_t T, int64_t K, int64_t k, int64_t E, const char* name) {
+// any_k: K need not be a multiple of 32 (moe_permute).
+int check_route_sizes(int64_t T, int64_t K, int64_t k, int64_t E, const char* name, bool any_k) {
   if (T < 0 || K <= 0 || k <= 0 || E <= 0)
     return fail(MX_ERR_INVALID_ARG, "%s: bad sizes T=%lld K=%lld k=%lld E=%lld", name,
                 (long long)T, (long long)K, (long long)k, (long long)E);
   if (k > E) return fail(MX_ERR_INVALID_ARG, "%s: k=%lld > E=%lld", name, (long long)k, (long long)E);
   if (!dims_in_range({T, K})) return fail(MX_ERR_UNSUPPORTED, "%s: T or K above 2^31 - 1", name);
-  if (K % 32 != 0) return fail(MX_ERR_UNSUPPORTED, "%s: K=%lld is not a multiple of 32", name, (long long)K);
+  if (!any_k && K % 32 != 0) return fail(MX_ERR_UNSUPPORTED, "%s: K=%lld is not a multiple of 32", name, (long long)K);
   if (K > (int64_t)1 << 24) return fail(MX_ERR_UNSUPPORTED, "%s: K=%lld > 2^24", name, (long long)K);
   if (k > kThreads) return fail(MX_ERR_UNSUPPORTED, "%s: k=%lld > %d", name, (long long)k, kThreads);
   if (E > kMaxE) return fail(MX_ERR_UNSUPPORTED, "%s: E=%lld > %d", name, (long long)E, kMaxE);
@@ -659,21 +742,38 @@ int check_route_args(int64_t T, int64_t K, int64_t k, int64_t E, const char* nam
   return MX_OK;
 }
 
+int check_route_args(int64_t T, int64_t K, int64_t k, int64_t E, const char* name) {
+  return check_route_sizes(T, K, k, E, name, false);
+}
+
 namespace {
 
-// x: bf16 rows, or null when the rows are MXFP8 (mxq, mxs).
-int launch_route(const uint16_t* x, const uint8_t* mxq, const uint8_t* mxs, const int32_t* ids, int64_t T, int64_t K,
-                 int64_t k, int64_t E, uint8_t* xq, uint8_t* xs, int32_t* sorted_row, int32_t* eri,
-                 int64_t* group_list, void* ws, hipStream_t stream) {
+// The token rows of a launch: bf16, MXFP8, or rows of any type (then K counts their bytes).
+struct RouteRows {
+  const uint16_t* x;
+  const uint8_t* mxq;
+  const uint8_t* mxs;
+  const uint8_t* rows;
+  int64_t ld_bytes;
+  const float* row_s;
+  float* out_s;
+};
+
+int launch_route(const RouteRows& in, const int32_t* ids, int64_t T, int64_t K, int64_t k, int64_t E, uint8_t* xq,
+                 uint8_t* xs, int32_t* sorted_row, int32_t* eri, int64_t* group_list, void* ws, hipStream_t stream) {
   if (T == 0) {
     zero_i64<<<dim3((unsigned)((E + 255) / 256)), dim3(256), 0, stream>>>(group_list, (int)E);
     return check_launch("moe_route_quant(zero)");
   }
   const Split sp = split_of(T, k);
   RouteParams p{};
-  p.x = x;
-  p.mxq = mxq;
-  p.mxs = mxs;
+  p.x = in.x;
+  p.mxq = in.mxq;
+  p.mxs = in.mxs;
+  p.rows = in.rows;
+  p.ld_bytes = in.ld_bytes;
+  p.row_s = in.row_s;
+  p.out_s = in.out_s;
   p.ids = ids;
   p.xq = xq;
   p.xs = xs;
@@ -707,7 +807,7 @@ int launch_route(const uint16_t* x, const uint8_t* mxq, const uint8_t* mxs, cons
   // most one token per share); a batch of one chunk (nothing to wait for)
   // takes at most kSingleShares
   const int64_t nb = K / 32, s_stride = ((nb + 1) / 2) * 2;
-  const int64_t row_bytes = (int64_t)align_up((size_t)(K + s_stride), 16);
+  const int64_t row_bytes = (int64_t)align_up((size_t)(K + (in.rows ? 0 : s_stride)), 16);
   const int64_t want = sp.S == 0 ? kSingleShares : (int64_t)num_cus() * kScatterPerCU;
   int64_t split = 1;
   while (split < sp.tpc &&
@@ -722,11 +822,12 @@ int launch_route(const uint16_t* x, const uint8_t* mxq, const uint8_t* mxs, cons
   p.lds_ints = (int)(lds / 4);
   p.stream = T * k * K > (int64_t)128 << 20;
   p.scales16 =
-      ((reinterpret_cast<uintptr_t>(xs) | reinterpret_cast<uintptr_t>(mxs)) % 16 == 0 && s_stride % 16 == 0) ? 1 : 0;
+      ((reinterpret_cast<uintptr_t>(xs) | reinterpret_cast<uintptr_t>(in.mxs)) % 16 == 0 && s_stride % 16 == 0) ? 1 : 0;
   const int64_t grid = sp.S + sp.nch * split;
   if (sp.S == 0) {
-    if (x) route_quant_kernel<true, false><<<dim3((unsigned)grid), dim3(kThreads), lds, stream>>>(p);
-    else route_quant_kernel<true, true><<<dim3((unsigned)grid), dim3(kThreads), lds, stream>>>(p);
+    if (in.x) route_quant_kernel<true, kRowsQuant><<<dim3((unsigned)grid), dim3(kThreads), lds, stream>>>(p);
+    else if (in.mxq) route_quant_kernel<true, kRowsMx><<<dim3((unsigned)grid), dim3(kThreads), lds, stream>>>(p);
+    else route_quant_kernel<true, kRowsAny><<<dim3((unsigned)grid), dim3(kThreads), lds, stream>>>(p);
   } else {
     hipStreamCaptureStatus cs = hipStreamCaptureStatusNone;
     if (hipStreamIsCapturing(stream, &cs) != hipSuccess)
@@ -736,8 +837,9 @@ int launch_route(const uint16_t* x, const uint8_t* mxq, const uint8_t* mxs, cons
       const int rc = check_launch("moe_route_quant(generation)");
       if (rc) return rc;
     }
-    if (x) route_quant_kernel<false, false><<<dim3((unsigned)grid), dim3(kThreads), lds, stream>>>(p);
-    else route_quant_kernel<false, true><<<dim3((unsigned)grid), dim3(kThreads), lds, stream>>>(p);
+    if (in.x) route_quant_kernel<false, kRowsQuant><<<dim3((unsigned)grid), dim3(kThreads), lds, stream>>>(p);
+    else if (in.mxq) route_quant_kernel<false, kRowsMx><<<dim3((unsigned)grid), dim3(kThreads), lds, stream>>>(p);
+    else route_quant_kernel<false, kRowsAny><<<dim3((unsigned)grid), dim3(kThreads), lds, stream>>>(p);
   }
   return check_launch("route_quant_kernel");
 }
@@ -747,13 +849,15 @@ int launch_route(const uint16_t* x, const uint8_t* mxq, const uint8_t* mxs, cons
 int launch_route_quant(const uint16_t* x, const int32_t* ids, int64_t T, int64_t K, int64_t k,
                        int64_t E, uint8_t* xq, uint8_t* xs, int32_t* sorted_row, int32_t* eri,
                        int64_t* group_list, void* ws, hipStream_t stream) {
-  return launch_route(x, nullptr, nullptr, ids, T, K, k, E, xq, xs, sorted_row, eri, group_list, ws, stream);
+  return launch_route({x, nullptr, nullptr, nullptr, 0, nullptr, nullptr}, ids, T, K, k, E, xq, xs, sorted_row, eri,
+                      group_list, ws, stream);
 }
 
 int launch_route_mx(const uint8_t* q, const uint8_t* s, const int32_t* ids, int64_t T, int64_t K, int64_t k,
                     int64_t E, uint8_t* xq, uint8_t* xs, int32_t* sorted_row, int32_t* eri, int64_t* group_list,
                     void* ws, hipStream_t stream) {
-  return launch_route(nullptr, q, s, ids, T, K, k, E, xq, xs, sorted_row, eri, group_list, ws, stream);
+  return launch_route({nullptr, q, s, nullptr, 0, nullptr, nullptr}, ids, T, K, k, E, xq, xs, sorted_row, eri,
+                      group_list, ws, stream);
 }
 
 }  // namespace mxmoe
@@ -818,6 +922,48 @@ extern "C" int moe_route_mx(const void* q_u8, const void* s_u8, const int32_t* t
   return launch_route_mx(static_cast<const uint8_t*>(q_u8), static_cast<const uint8_t*>(s_u8), topk_ids, T, K, k, E,
                          static_cast<uint8_t*>(xq_u8), static_cast<uint8_t*>(xs_u8), sorted_row, expanded_row_idx,
                          group_list, workspace, as_stream(stream));
+}
+
+extern "C" int moe_permute(const void* x, int64_t ldx, int64_t elem_bytes, const float* x_s, const int32_t* topk_ids,
+                           int64_t T, int64_t K, int64_t k, int64_t E, void* xp, float* xp_s, int32_t* sorted_row,
+                           int32_t* expanded_row_idx, int64_t* group_list, void* workspace, size_t ws_bytes,
+                           void* stream) {
+  using namespace mxmoe;
+  int rc = check_route_sizes(T, K, k, E, "moe_permute", true);
+  if (rc) return rc;
+  if (elem_bytes != 1 && elem_bytes != 2 && elem_bytes != 4)
+    return fail(MX_ERR_INVALID_ARG, "moe_permute: elem_bytes must be 1, 2 or 4, got %lld", (long long)elem_bytes);
+  if (ldx < K) return fail(MX_ERR_INVALID_ARG, "moe_permute: ldx=%lld < K=%lld", (long long)ldx, (long long)K);
+  if (!dims_in_range({ldx})) return fail(MX_ERR_UNSUPPORTED, "moe_permute: ldx above 2^31 - 1");
+  const size_t need = route_workspace_bytes(T, k, E);
+  if (!x_s != !xp_s) return fail(MX_ERR_INVALID_ARG, "moe_permute: x_s and xp_s go together");
+  if (!group_list || (need > 0 && !workspace)) return fail(MX_ERR_INVALID_ARG, "moe_permute: null pointer");
+  if (T > 0 && (!x || !topk_ids || !xp || !sorted_row || !expanded_row_idx))
+    return fail(MX_ERR_INVALID_ARG, "moe_permute: null pointer");
+  if (ws_bytes < need)
+    return fail(MX_ERR_WORKSPACE, "moe_permute: workspace %zu bytes < %zu needed", ws_bytes, need);
+  const uintptr_t es = (uintptr_t)elem_bytes;
+  if (reinterpret_cast<uintptr_t>(x) % es || reinterpret_cast<uintptr_t>(xp) % es ||
+      reinterpret_cast<uintptr_t>(x_s) % 4 || reinterpret_cast<uintptr_t>(xp_s) % 4 ||
+      reinterpret_cast<uintptr_t>(topk_ids) % 4 || reinterpret_cast<uintptr_t>(sorted_row) % 4 ||
+      reinterpret_cast<uintptr_t>(expanded_row_idx) % 4 || reinterpret_cast<uintptr_t>(group_list) % 8 ||
+      reinterpret_cast<uintptr_t>(workspace) % 8)
+    return fail(MX_ERR_UNSUPPORTED, "moe_permute: misaligned pointer");
+  // every row is read while others are being written: no output may lie over an input
+  const uint64_t M = (uint64_t)(T * k), row = (uint64_t)K * es;
+  const uint64_t x_bytes = T > 0 ? (uint64_t)(T - 1) * (uint64_t)ldx * es + row : 0;
+  const Span in[3] = {{x, x_bytes}, {x_s, (uint64_t)T * 4}, {topk_ids, M * 4}};
+  const Span out[6] = {{xp, M * row}, {xp_s, M * 4}, {sorted_row, M * 4}, {expanded_row_idx, M * 4},
+                       {group_list, (uint64_t)E * 8}, {workspace, need}};
+  for (int o = 0; o < 6; ++o) {
+    for (int i = 0; i < 3; ++i)
+      if (overlaps(out[o], in[i])) return fail(MX_ERR_INVALID_ARG, "moe_permute: an output overlaps an input");
+    for (int i = o + 1; i < 6; ++i)
+      if (overlaps(out[o], out[i])) return fail(MX_ERR_INVALID_ARG, "moe_permute: two outputs overlap");
+  }
+  return launch_route({nullptr, nullptr, nullptr, static_cast<const uint8_t*>(x), ldx * elem_bytes, x_s, xp_s},
+                      topk_ids, T, (int64_t)row, k, E, static_cast<uint8_t*>(xp), nullptr, sorted_row,
+                      expanded_row_idx, group_list, workspace, as_stream(stream));
 }
 
 // ---------------------------------------------------------------------------
