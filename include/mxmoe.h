@@ -561,7 +561,7 @@ size_t int8_linear_workspace_size(int64_t T, int64_t K, int64_t N, int x_is_int8
  *   residual  bf16 [T, N] or NULL;  y bf16 [T, N]
  * y may be the residual itself (the same address); any other overlap of y or of
  * the workspace is MX_ERR_INVALID_ARG.  Limits: K % 16 == 0, K < 2^17 (the sum
- * stays within int32), N < 2^30, fewer than 2^30 tiles of 32 x 32 outputs.
+ * stays within int32), N < 2^30, fewer than 2^28 tiles of 32 x 32 outputs.
  * Alignment: int8 operands on 16-byte boundaries, the workspace on 256, the rest
  * on their elements.
  */
@@ -583,7 +583,7 @@ int int8_linear(const void* x, const float* x_s, const void* w_i8,
  *   y  bf16 [M, N]
  * group_list int64 [E], group_list_type 0 = cumulative, 1 = count.  Rows not
  * owned by any expert are not written.  Limits and alignment as int8_linear,
- * E <= 1024; fewer than 2^30 tiles of 32 x 32 outputs for M + 32 E rows.
+ * E <= 1024; fewer than 2^28 tiles of 32 x 32 outputs for M + 32 E rows.
  */
 int gmm_int8(const void* a_i8, const float* a_s, const void* w_i8,
              const float* w_s, const int64_t* group_list, int group_list_type,

@@ -6,145 +6,33 @@
 // the sum exact in int32 (K < 2^17).
 #include <algorithm>
 
-#include "linear_fused.h"
+#include "int8.h"
 
 namespace mxmoe {
 
 int launch_int8_quantize(const uint16_t* x, int64_t rows, int64_t kd, int64_t ld, int8_t* q, float* s,
                          hipStream_t stream);
 
+int launch_int8_stream(const Int8Params& p, hipStream_t stream, const char* name);
+int launch_int8_tile256(const Int8Params& p, hipStream_t stream, const char* name);
+int launch_int8_tile128(const Int8Params& p, hipStream_t stream, const char* name);
+
 namespace {
 
-typedef int v4i __attribute__((ext_vector_type(4)));
-typedef int v16i __attribute__((ext_vector_type(16)));
-
-constexpr int kMaxE = 1024;
 constexpr int64_t kMaxK = ((int64_t)1 << 17) - 16;
 
-struct Int8Params {
-  LinParams e;           // sizes and the epilogue's operands
-  const int8_t* x;       // [M, K]
-  const float* xs;       // [M]
-  const int8_t* w;       // [E, rows, K]
-  const float* ws;       // [E, rows]
-  const int64_t* gl;     // [E], or null: one group of all rows
-  int gl_type, E;
-  int64_t rows;          // weight rows per expert (2 N with swiglu)
-  int swiglu;
-};
-
-constexpr int kBN = 64, kBM = 64, kBK = 64, kPitch = 80;
-
-__global__ __launch_bounds__(256) void int8_simple_kernel(Int8Params p) {
-  __shared__ __attribute__((aligned(16))) int8_t sa[kBN * kPitch];
-  __shared__ __attribute__((aligned(16))) int8_t sb[kBM * kPitch];
-  __shared__ int64_t s_row0[kMaxE + 1];
-  __shared__ int s_tile0[kMaxE + 1];
-  __shared__ float part[4 * 32 * 36];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int li = lane & 31, lg = lane >> 5;
-  const int E = p.gl ? p.E : 1;
-  if (tid == 0) {
-    int64_t run = 0;
-    int tiles = 0;
-    for (int e = 0; e < E; ++e) {
-      int64_t n = !p.gl ? p.e.T : p.gl_type == 1 ? p.gl[e] : p.gl[e] - (e ? p.gl[e - 1] : 0);
-      n = std::min<int64_t>(std::max<int64_t>(n, 0), p.e.T - run);
-      s_row0[e] = run;
-      s_tile0[e] = tiles;
-      tiles += (int)((n + kBM - 1) / kBM);
-      run += n;
-    }
-    s_row0[E] = run;
-    s_tile0[E] = tiles;
-  }
-  __syncthreads();
-  const int64_t N = p.e.N, K = p.e.K;
-  const int tile_n = p.swiglu ? kBN / 2 : kBN;
-  const int64_t n_tiles = (N + tile_n - 1) / tile_n;
-  const int64_t total = s_tile0[E] * n_tiles;
-  for (int64_t tile = blockIdx.x; tile < total; tile += gridDim.x) {
-    const int mt = (int)(tile / n_tiles);
-    const int64_t n0 = (tile % n_tiles) * tile_n;
-    int e = 0;
-    while (s_tile0[e + 1] <= mt) ++e;
-    const int64_t m0 = s_row0[e] + (int64_t)(mt - s_tile0[e]) * kBM, m1 = s_row0[e + 1];
-    v16i acc[2] = {};   // swiglu: gate and up
-    const int wn = wave & 1, wm = wave >> 1;
-    for (int64_t k0 = 0; k0 < K; k0 += kBK) {
-      __syncthreads();
-      const int r = tid >> 2, c = tid & 3;
-      uint4 ua = make_uint4(0, 0, 0, 0), ub = ua;
-      if (k0 + 16 * c < K) {
-        const int64_t n = p.swiglu ? n0 + (r & 31) : n0 + r;
-        const int64_t wr = n + (p.swiglu && r >= 32 ? N : 0);
-        if (n < N) ua = *reinterpret_cast<const uint4*>(p.w + (e * p.rows + wr) * K + k0 + 16 * c);
-        if (m0 + r < m1) ub = *reinterpret_cast<const uint4*>(p.x + (m0 + r) * K + k0 + 16 * c);
-      }
-      *reinterpret_cast<uint4*>(sa + r * kPitch + 16 * c) = ua;
-      *reinterpret_cast<uint4*>(sb + r * kPitch + 16 * c) = ub;
-      __syncthreads();
-#pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        const v4i b = *reinterpret_cast<const v4i*>(sb + (32 * wm + li) * kPitch + 32 * s + 16 * lg);
-        if (p.swiglu) {
-          if (wn == 0)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const v4i a = *reinterpret_cast<const v4i*>(sa + (32 * h + li) * kPitch + 32 * s + 16 * lg);
-              acc[h] = __builtin_amdgcn_mfma_i32_32x32x32_i8(a, b, acc[h], 0, 0, 0);
-            }
-        } else {
-          const v4i a = *reinterpret_cast<const v4i*>(sa + (32 * wn + li) * kPitch + 32 * s + 16 * lg);
-          acc[0] = __builtin_amdgcn_mfma_i32_32x32x32_i8(a, b, acc[0], 0, 0, 0);
-        }
-      }
-    }
-    // lane: token li, features 8 q + 4 lg + i of the wave's 32
-    const int64_t m = m0 + 32 * wm + li;
-    const float xs = m < m1 ? p.xs[m] : 0.0f;
-    float* mine = part + wave * 32 * 36;
-#pragma unroll
-    for (int q = 0; q < 4; ++q)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int f = 8 * q + 4 * lg + i;
-        const int64_t n = n0 + (p.swiglu ? 0 : 32 * wn) + f;
-        float z = 0.0f;
-        if (n < N) {
-          z = (float)acc[0][4 * q + i] * xs * p.ws[e * p.rows + n];
-          if (p.swiglu) {
-            const float u = (float)acc[1][4 * q + i] * xs * p.ws[e * p.rows + N + n];
-            z = z * __builtin_amdgcn_rcpf(1.0f + __expf(-z)) * u;
-          }
-        }
-        mine[li * 36 + f] = z;
-      }
-    __syncthreads();
-    for (int u0 = 0; u0 < 32; u0 += 16) {
-      if (p.swiglu && wn == 1) break;
-      const int tl = u0 + (lane >> 2);
-      const int64_t t = m0 + 32 * wm + tl, n = n0 + (p.swiglu ? 0 : 32 * wn) + 8 * (lane & 3);
-      const int cnt = t < m1 ? (int)std::min<int64_t>(N - n, 8) : 0;
-      float z[8], b[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) z[i] = mine[tl * 36 + 8 * (lane & 3) + i];
-      uint4 res = make_uint4(0, 0, 0, 0);
-      epilogue_bias(p.e, n, cnt, b);
-      if (p.e.res && cnt > 0) res = load_res8<false>(p.e.res + t * N + n, cnt);
-      epilogue8(p.e, Place{t * N + n, 0, 0, 0}, n, cnt, b, res, z);
-    }
-  }
+int launch_int8(Int8Params& p, hipStream_t stream, const char* name) {
+  p.e.nk = (int)((p.e.K + kStageK - 1) / kStageK);
+  p.present = (int)((p.e.K - (int64_t)(p.e.nk - 1) * kStageK) / 16);
+  const int64_t per = p.gl ? p.e.T / p.E : p.e.T;
+  if (per <= 32) return launch_int8_stream(p, stream, name);
+  if (per <= 256) return launch_int8_tile128(p, stream, name);
+  return launch_int8_tile256(p, stream, name);
 }
 
-int launch_int8(const Int8Params& p, hipStream_t stream, const char* name) {
-  const int64_t n_tiles = (p.e.N + (p.swiglu ? kBN / 2 : kBN) - 1) / (p.swiglu ? kBN / 2 : kBN);
-  const int64_t upper = ((p.e.T + kBM - 1) / kBM + (p.gl ? p.E : 0)) * n_tiles;
-  int8_simple_kernel<<<dim3((unsigned)std::min<int64_t>(upper, 256 * 8)), dim3(256), 0, stream>>>(p);
-  return check_launch(name);
-}
-
-bool too_many_tiles(int64_t T, int64_t N) { return ((T + 31) / 32) * ((N + 31) / 32) >= (int64_t)1 << 30; }
+// Tile indices are 32-bit in every kernel, also a round past the last: of tiles of
+// 16 x 16 there are four times as many (an output of half a TB).
+bool too_many_tiles(int64_t T, int64_t N) { return ((T + 31) / 32) * ((N + 31) / 32) >= (int64_t)1 << 28; }
 
 int check_sizes(const char* name, int64_t T, int64_t K, int64_t N) {
   if (T < 0 || K <= 0 || N <= 0)
@@ -154,7 +42,7 @@ int check_sizes(const char* name, int64_t T, int64_t K, int64_t N) {
     return fail(MX_ERR_UNSUPPORTED, "%s: rows above 2^31 - 1 or N above 2^30 - 1", name);
   if (K % 16 != 0) return fail(MX_ERR_UNSUPPORTED, "%s: K=%lld is not a multiple of 16", name, (long long)K);
   if (K > kMaxK) return fail(MX_ERR_UNSUPPORTED, "%s: K=%lld >= 2^17", name, (long long)K);
-  if (too_many_tiles(T, N)) return fail(MX_ERR_UNSUPPORTED, "%s: 2^30 or more tiles of 32 x 32 outputs", name);
+  if (too_many_tiles(T, N)) return fail(MX_ERR_UNSUPPORTED, "%s: 2^28 or more tiles of 32 x 32 outputs", name);
   return MX_OK;
 }
 
@@ -250,10 +138,10 @@ extern "C" int gmm_int8(const void* a_i8, const float* a_s, const void* w_i8, co
   int rc = check_sizes("gmm_int8", M, K, N);
   if (rc) return rc;
   if (E <= 0) return fail(MX_ERR_INVALID_ARG, "gmm_int8: bad E=%lld", (long long)E);
-  if (E > kMaxE) return fail(MX_ERR_UNSUPPORTED, "gmm_int8: E=%lld > %d", (long long)E, kMaxE);
+  if (E > kInt8MaxE) return fail(MX_ERR_UNSUPPORTED, "gmm_int8: E=%lld > %d", (long long)E, kInt8MaxE);
   // (an expert's last tile may be partly empty: E more rows of tiles)
   if (too_many_tiles(M + 32 * E, N))
-    return fail(MX_ERR_UNSUPPORTED, "gmm_int8: 2^30 or more tiles of 32 x 32 outputs");
+    return fail(MX_ERR_UNSUPPORTED, "gmm_int8: 2^28 or more tiles of 32 x 32 outputs");
   if (group_list_type != 0 && group_list_type != 1)
     return fail(MX_ERR_INVALID_ARG, "gmm_int8: group_list_type must be 0 (cumulative) or 1 (count), got %d",
                 group_list_type);
