@@ -2,6 +2,7 @@
 // tables and the matrix instructions' types.
 #pragma once
 
+#include "int8_codes.h"
 #include "linear_fused.h"
 
 namespace mxmoe {
@@ -98,8 +99,22 @@ __device__ __forceinline__ int expert_of(const int* tile0, int E, int t) {
   return uniform(block * per + __popcll(__ballot(lane < per && e < E && tile0[std::min(e, E)] <= t)) - 1);
 }
 
-// The epilogue of 8 consecutive features of a token, the first cnt of which exist,
-// at element el + lane_el of y: bias, activation, residual (load_res8's), bf16.
+// 8 consecutive features of a token, the first cnt of which exist, to bf16 at
+// element el + lane_el of y.
+__device__ __forceinline__ void store8(uint16_t* y, int64_t el, uint32_t lane_el, int cnt, const float (&z)[8]) {
+  if (cnt <= 0) return;
+  const u32x4_any o = {bf16x2(z[0], z[1]), bf16x2(z[2], z[3]), bf16x2(z[4], z[5]), bf16x2(z[6], z[7])};
+  y = at(y, el, lane_el);
+  if (cnt >= 8) {
+    // written once: past the caches, which hold the operands of the tiles to come
+    __builtin_nontemporal_store(o, reinterpret_cast<u32x4_any*>(y));
+  } else {
+#pragma unroll
+    for (int i = 0; i < 7; ++i)
+      if (i < cnt) y[i] = static_cast<uint16_t>(o[i >> 1] >> (16 * (i & 1)));
+  }
+}
+// The linear's epilogue: bias, activation, residual (load_res8's), then store8.
 __device__ __forceinline__ void finish8(const LinParams& p, int64_t el, uint32_t lane_el, int cnt, const float (&b)[8],
                                         const uint4& res, float (&z)[8]) {
 #pragma unroll
@@ -109,17 +124,7 @@ __device__ __forceinline__ void finish8(const LinParams& p, int64_t el, uint32_t
   unpack_bf16x8(res, r);
 #pragma unroll
   for (int i = 0; i < 8; ++i) z[i] += r[i];
-  if (cnt <= 0) return;
-  const u32x4_any o = {bf16x2(z[0], z[1]), bf16x2(z[2], z[3]), bf16x2(z[4], z[5]), bf16x2(z[6], z[7])};
-  uint16_t* y = at(p.y, el, lane_el);
-  if (cnt >= 8) {
-    // written once: past the caches, which hold the operands of the tiles to come
-    __builtin_nontemporal_store(o, reinterpret_cast<u32x4_any*>(y));
-  } else {
-#pragma unroll
-    for (int i = 0; i < 7; ++i)
-      if (i < cnt) y[i] = static_cast<uint16_t>(o[i >> 1] >> (16 * (i & 1)));
-  }
+  store8(p.y, el, lane_el, cnt, z);
 }
 
 // silu(g) u with the hardware exp and reciprocal (about 1 ulp each)

@@ -13,21 +13,58 @@ namespace mxmoe {
 int launch_int8_quantize(const uint16_t* x, int64_t rows, int64_t kd, int64_t ld, int8_t* q, float* s,
                          hipStream_t stream);
 
-int launch_int8_stream(const Int8Params& p, hipStream_t stream, const char* name);
-int launch_int8_tile256(const Int8Params& p, hipStream_t stream, const char* name);
+int launch_int8_32x16(const Int8Params& p, hipStream_t stream, const char* name);
+int launch_int8_32x16_wide(const Int8Params& p, hipStream_t stream, const char* name);
+int launch_int8_32x32(const Int8Params& p, hipStream_t stream, const char* name);
+int launch_int8_64x64(const Int8Params& p, hipStream_t stream, const char* name);
 int launch_int8_tile128(const Int8Params& p, hipStream_t stream, const char* name);
+int launch_int8_tile256(const Int8Params& p, hipStream_t stream, const char* name);
+bool int8_resident(int64_t T, int64_t K, int64_t N);
+int launch_int8_resident(const Int8Params& p, hipStream_t stream, const char* name);
 
 namespace {
 
 constexpr int64_t kMaxK = ((int64_t)1 << 17) - 16;
 
+// The kernels by their tiles (weight rows x rows of x), the waves that share a
+// tile's K, and the workgroups of a CU.
+struct Kernel {
+  int64_t bn, bm, waves, per_cu;
+  int64_t first, round, stage;         // time in 0.01 us: first + rounds (round + stages of a wave * stage)
+  int64_t g_first, g_round, g_stage;   // of gmm_int8
+  int (*launch)(const Int8Params&, hipStream_t, const char*);
+};
+const Kernel kKernels[] = {
+    {32, 16, 4, 2, 226, 99, 50, 507, 47, 73, launch_int8_32x16},
+    {32, 16, 8, 1, 257, 84, 56, 568, 15, 84, launch_int8_32x16_wide},
+    {32, 32, 4, 2, 210, 129, 61, 522, 40, 89, launch_int8_32x32},
+    {64, 64, 2, 2, 155, 335, 88, 521, 115, 95, launch_int8_64x64},
+    {128, 128, 1, 2, 0, 597, 81, 467, 224, 90, launch_int8_tile128},
+    {256, 256, 1, 1, 0, 924, 157, 647, 119, 134, launch_int8_tile256},
+};
+
+// Which kernel: the one whose time a line through its measured times says is
+// shortest.  Its tiles go over the CUs in rounds; a round costs a part per tile and
+// a part per k stage of a wave.  gmm_int8's rows lie with the experts as the device's
+// group list says: the host counts a tile for every expert (or row, if these are
+// fewer) and half a tile for what is left over behind whole ones.
 int launch_int8(Int8Params& p, hipStream_t stream, const char* name) {
   p.e.nk = (int)((p.e.K + kStageK - 1) / kStageK);
   p.present = (int)((p.e.K - (int64_t)(p.e.nk - 1) * kStageK) / 16);
-  const int64_t per = p.gl ? p.e.T / p.E : p.e.T;
-  if (per <= 32) return launch_int8_stream(p, stream, name);
-  if (per <= 256) return launch_int8_tile128(p, stream, name);
-  return launch_int8_tile256(p, stream, name);
+  const int64_t cus = num_cus(), M = p.e.T;
+  auto up = [](int64_t n, int64_t d) { return (n + d - 1) / d; };
+  const Kernel* best = nullptr;
+  int64_t best_us = 0;
+  for (const Kernel& k : kKernels) {
+    const int64_t m_tiles = p.gl ? std::min<int64_t>(M, p.E) + std::max<int64_t>(0, M - p.E * k.bm / 2) / k.bm : up(M, k.bm);
+    const int64_t rounds = up(m_tiles * up(p.rows, k.bn), cus * k.per_cu), stages = up(p.e.nk, k.waves);
+    const int64_t us = p.gl ? k.g_first + rounds * (k.g_round + stages * k.g_stage) : k.first + rounds * (k.round + stages * k.stage);
+    if (!best || us < best_us) {
+      best = &k;
+      best_us = us;
+    }
+  }
+  return best->launch(p, stream, name);
 }
 
 // Tile indices are 32-bit in every kernel, also a round past the last: of tiles of
@@ -50,8 +87,8 @@ int check_sizes(const char* name, int64_t T, int64_t K, int64_t N) {
 struct Int8Layout {
   size_t xs, total;
 };
-Int8Layout int8_layout(int64_t T, int64_t K, int x_is_int8) {
-  if (x_is_int8) return {0, 0};
+Int8Layout int8_layout(int64_t T, int64_t K, int64_t N, int x_is_int8) {
+  if (x_is_int8 || int8_resident(T, K, N)) return {0, 0};
   const size_t xs = align_up((size_t)(T * K), 256);
   return {xs, xs + align_up((size_t)T * 4, 256)};
 }
@@ -63,7 +100,7 @@ Int8Layout int8_layout(int64_t T, int64_t K, int x_is_int8) {
 extern "C" size_t int8_linear_workspace_size(int64_t T, int64_t K, int64_t N, int x_is_int8) {
   // 0 for sizes int8_linear rejects
   if (mxmoe::check_sizes("int8_linear", T, K, N) != MX_OK) return 0;
-  return mxmoe::int8_layout(T, K, x_is_int8).total;
+  return mxmoe::int8_layout(T, K, N, x_is_int8).total;
 }
 
 extern "C" int int8_linear(const void* x, const float* x_s, const void* w_i8, const float* w_s, const void* bias,
@@ -77,7 +114,7 @@ extern "C" int int8_linear(const void* x, const float* x_s, const void* w_i8, co
   if (activation < MX_ACT_NONE || activation > MX_ACT_GELU_TANH)
     return fail(MX_ERR_INVALID_ARG, "int8_linear: unknown activation %d", activation);
   const bool int8_in = x_s != nullptr;
-  const Int8Layout L = int8_layout(T, K, int8_in);
+  const Int8Layout L = int8_layout(T, K, N, int8_in);
   if (T > 0 && (!x || !w_i8 || !w_s || !y_bf16 || (L.total > 0 && !workspace)))
     return fail(MX_ERR_INVALID_ARG, "int8_linear: null pointer");
   if (ws_bytes < L.total)
@@ -113,6 +150,7 @@ extern "C" int int8_linear(const void* x, const float* x_s, const void* w_i8, co
   p.e.act = activation;
   p.e.res = static_cast<const uint16_t*>(residual_bf16);
   p.e.y = static_cast<uint16_t*>(y_bf16);
+  p.e.stream_res = T * N > (int64_t)48 << 20;
   p.w = static_cast<const int8_t*>(w_i8);
   p.ws = w_s;
   p.rows = N;
@@ -120,6 +158,11 @@ extern "C" int int8_linear(const void* x, const float* x_s, const void* w_i8, co
   if (int8_in) {
     p.x = static_cast<const int8_t*>(x);
     p.xs = x_s;
+  } else if (int8_resident(T, K, N)) {
+    p.x = static_cast<const int8_t*>(x);
+    p.e.nk = (int)((K + kStageK - 1) / kStageK);
+    p.present = (int)((K - (int64_t)(p.e.nk - 1) * kStageK) / 16);
+    return launch_int8_resident(p, s, "int8_linear");
   } else {
     int8_t* xq = static_cast<int8_t*>(workspace);
     float* xs = reinterpret_cast<float*>(static_cast<char*>(workspace) + L.xs);

@@ -15,7 +15,7 @@
 // that are read twice (int8_quantize_long).
 #include <algorithm>
 
-#include "fused.h"
+#include "int8_codes.h"
 
 namespace mxmoe {
 
@@ -32,54 +32,8 @@ struct QuantParams {
 // elements then come twice, with the same codes.
 __device__ __forceinline__ int64_t chunk_at(int64_t e, int64_t K) { return std::min<int64_t>(e, K - 8); }
 
-// The largest magnitude of 8 bf16, as bits (their order is the magnitudes').
-__device__ __forceinline__ uint32_t amax8(const u32x4_any& u) {
-  uint32_t m = 0;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    m = std::max(m, u[i] & 0x7fffu);
-    m = std::max(m, (u[i] >> 16) & 0x7fffu);
-  }
-  return m;
-}
-
-// Four codes as bytes: adding 3 * 2^22 leaves the nearest integer, ties to even,
-// in the sum's last bits (|v| < 2^22).
-__device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d) {
-  constexpr float kMagic = 12582912.0f;
-  const uint32_t ua = __float_as_uint(a + kMagic), ub = __float_as_uint(b + kMagic);
-  const uint32_t uc = __float_as_uint(c + kMagic), ud = __float_as_uint(d + kMagic);
-  const uint32_t lo = __builtin_amdgcn_perm(ub, ua, 0x0c0c0400);   // bytes 0 of ua and ub
-  const uint32_t hi = __builtin_amdgcn_perm(ud, uc, 0x04000c0c);
-  return lo | hi;
-}
-
 __device__ __forceinline__ void store_codes8(int8_t* d, const u32x4_any& u, float r) {
-  float v[8];
-  unpack_bf16x8(make_uint4(u.x, u.y, u.z, u.w), v);
-#pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = v[i] * r;
-  const u32x2_any o = {codes4(v[0], v[1], v[2], v[3]), codes4(v[4], v[5], v[6], v[7])};
-  __builtin_nontemporal_store(o, reinterpret_cast<u32x2_any*>(d));
-}
-
-__device__ __forceinline__ float scale_of(uint32_t amax_bits) {
-  return fmaxf(bf16_to_f32(amax_bits) * (1.0f / 127.0f), 0x1p-126f);
-}
-
-template <int kCtrl, int kRowMask = 0xf>
-__device__ __forceinline__ uint32_t dpp_max(uint32_t x) {
-  return std::max(x, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, kCtrl, kRowMask, 0xf, false));
-}
-// Maximum over the 64 lanes of a wave (all active), by wave_sum's moves.
-__device__ __forceinline__ uint32_t wave_max(uint32_t x) {
-  x = dpp_max<0x111>(x);        // row_shr:1
-  x = dpp_max<0x112>(x);        // row_shr:2
-  x = dpp_max<0x114>(x);        // row_shr:4
-  x = dpp_max<0x118>(x);        // row_shr:8
-  x = dpp_max<0x142, 0xa>(x);   // row_bcast:15
-  x = dpp_max<0x143, 0xc>(x);   // row_bcast:31
-  return (uint32_t)__builtin_amdgcn_readlane((int)x, 63);
+  __builtin_nontemporal_store(int8_codes8(u, r), reinterpret_cast<u32x2_any*>(d));
 }
 
 template <int W>
@@ -115,7 +69,7 @@ __global__ __launch_bounds__(64 * (W < 4 ? 4 : W)) void int8_quantize_kernel(Qua
     }
 #pragma unroll
     for (int c = 0; c < C; ++c) m = std::max(m, amax8(u[c]));
-    const float s = scale_of(row_max<W>(m, part));
+    const float s = int8_scale(row_max<W>(m, part));
     if (lane == 0) p.s[r] = s;
     const float inv = 1.0f / s;
 #pragma unroll
@@ -135,7 +89,7 @@ __global__ __launch_bounds__(64 * kLongWaves) void int8_quantize_long(QuantParam
     uint32_t m = 0;
     for (int64_t e = 8 * (int64_t)threadIdx.x; e < p.K; e += 8 * 64 * kLongWaves)
       m = std::max(m, amax8(*reinterpret_cast<const u32x4_any*>(x + chunk_at(e, p.K))));
-    const float s = scale_of(row_max<kLongWaves>(m, part));
+    const float s = int8_scale(row_max<kLongWaves>(m, part));
     if (threadIdx.x == 0) p.s[r] = s;
     const float inv = 1.0f / s;
     for (int64_t e = 8 * (int64_t)threadIdx.x; e < p.K; e += 8 * 64 * kLongWaves)
@@ -149,7 +103,7 @@ __global__ __launch_bounds__(256) void int8_quantize_tiny(QuantParams p) {
     const uint16_t* x = p.x + r * p.ldx;
     uint32_t m = 0;
     for (int i = 0; i < (int)p.K; ++i) m = std::max<uint32_t>(m, x[i] & 0x7fffu);
-    const float s = scale_of(m);
+    const float s = int8_scale(m);
     p.s[r] = s;
     const float inv = 1.0f / s;
     for (int i = 0; i < (int)p.K; ++i)

@@ -14,6 +14,10 @@
 // The workgroups are persistent.  A wave's stream of stages runs on into its next
 // tile while the sums of the last one are stored, or, with kOnce, the sums take the
 // ring's place and a tile's loads begin when the last one is stored.
+//
+// kBf16: p.x is bf16 [T, K], T <= 16 and T K <= kMaxResident (host): every
+// workgroup quantises the tokens itself, as int8_quantize does, into rows that stay
+// in LDS, swizzled like a slot's; only the weights go through the rings.
 #include <algorithm>
 
 #include "int8.h"
@@ -22,9 +26,11 @@ namespace mxmoe {
 
 namespace {
 
-template <int NR, int MT, int WV, int S, bool kGrouped, bool kSwiglu, bool kOnce>
+constexpr int kMaxResident = 65536;
+
+template <int NR, int MT, int WV, int S, bool kGrouped, bool kSwiglu, bool kOnce, bool kBf16>
 __global__ __launch_bounds__(64 * WV) void int8_stream_kernel(Int8Params p, uint32_t n_tiles, uint32_t t_tiles) {
-  constexpr int kRowsW = 16 * NR, kRowsX = 16 * MT, kRows = kRowsW + kRowsX;
+  constexpr int kRowsW = 16 * NR, kRowsX = 16 * MT, kRows = kRowsW + (kBf16 ? 0 : kRowsX);   // LDS rows per slot
   constexpr int kOut = kSwiglu ? kRowsW / 2 : kRowsW;   // features a tile computes
   constexpr int kScaleOps = (kRows + 63) / 64;
   constexpr int kSlot = kRows * kStageK + kScaleOps * 256;
@@ -35,8 +41,13 @@ __global__ __launch_bounds__(64 * WV) void int8_stream_kernel(Int8Params p, uint
   static_assert(S >= 2 && S <= 4 && (S - 1) * kOps < 64, "vmcnt range");
   static_assert(!kOnce || kPart <= kRing, "the partial tiles reuse the ring");
   static_assert(!kSwiglu || NR % 2 == 0, "gate and up fragments");
+  static_assert(!kBf16 || (kOnce && !kGrouped && MT == 1), "resident tokens");
   __shared__ __attribute__((aligned(16))) uint8_t ring[kRing];
   __shared__ __attribute__((aligned(16))) uint8_t parts[kOnce ? 16 : 2 * kPart];
+  // kBf16: a row has an odd number of stages, so that 16 rows' chunks hit distinct banks: at most T (K + 256) bytes
+  __shared__ __attribute__((aligned(16))) uint8_t xres[kBf16 ? kMaxResident + 16 * 256 : 16];
+  __shared__ uint32_t s_amax[kBf16 ? 16 : 1];
+  __shared__ float s_xs[kBf16 ? 16 : 1];
   extern __shared__ int s_tab[];   // kGrouped: tile0 and row0, E + 1 each
 
   const int tid = threadIdx.x, lane = tid & 63;
@@ -143,11 +154,58 @@ __global__ __launch_bounds__(64 * WV) void int8_stream_kernel(Int8Params p, uint
     for (int i = 0; i < S; ++i) issue_next(0);
   }
 
+  const int xstages = nk | 1;   // kBf16: stages of 128 bytes per token row
+  if constexpr (kBf16) {
+    constexpr int kThreads = 64 * WV, kIn = kMaxResident / 8 / kThreads;   // 8 elements at a time, all in flight
+    const int per_row = (int)K / 8, total8 = (int)p.e.T * per_row;
+    const uint16_t* x = reinterpret_cast<const uint16_t*>(p.x);
+    u32x4_any in[kIn];
+    if (tid < 16) s_amax[tid] = 0;
+#pragma unroll
+    for (int i = 0; i < kIn; ++i)
+      if (tid + i * kThreads < total8) in[i] = *reinterpret_cast<const u32x4_any*>(x + 8 * (int64_t)(tid + i * kThreads));
+#pragma unroll
+    for (int i = 0; i < S; ++i) issue_next(0);   // the first weights, behind the tokens
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kIn; ++i) {
+      const int u = tid + i * kThreads, r = u / per_row;
+      if (i * kThreads >= total8) break;   // uniform
+      const uint32_t m = u < total8 ? amax8(in[i]) : 0;
+      if (__ballot(r != uniform(r)) == 0) {   // a wave within one row
+        const uint32_t most = wave_max(m);
+        if (lane == 0 && u < total8) atomicMax(&s_amax[r], most);
+      } else if (u < total8) {
+        atomicMax(&s_amax[r], m);
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kIn; ++i) {
+      const int u = tid + i * kThreads;
+      if (u >= total8) break;
+      const int r = u / per_row, c8 = u - r * per_row;
+      const float sx = int8_scale(s_amax[r]);
+      if (c8 == 0) s_xs[r] = sx;
+      const u32x2_any q = int8_codes8(in[i], 1.0f / sx);
+      uint8_t* row = xres + (r * xstages + (c8 >> 4)) * kStageK;
+      *reinterpret_cast<uint2*>(row + ((((c8 >> 1) & 7) ^ ((r >> 1) & 7)) << 4) + 8 * (c8 & 1)) = make_uint2(q.x, q.y);
+    }
+    // zeros behind the rows' ends
+    if (tid < 8 * (int)p.e.T && (tid & 7) >= p.present) {
+      const int r = tid >> 3;
+      *reinterpret_cast<uint4*>(xres + (r * xstages + nk - 1) * kStageK + (((tid & 7) ^ ((r >> 1) & 7)) << 4)) = make_uint4(0, 0, 0, 0);
+    }
+    __syncthreads();
+  }
+
   for (int tj = 0; tj < my_tiles; ++tj) {
     if constexpr (kOnce) {
       if (tj > 0) __syncthreads();   // the last tile's sums are read
+      if (!kBf16 || tj > 0) {
 #pragma unroll
-      for (int i = 0; i < S; ++i) issue_next(tj);
+        for (int i = 0; i < S; ++i) issue_next(tj);
+      }
     }
     v4i acc[NR][MT];
 #pragma unroll
@@ -170,8 +228,15 @@ __global__ __launch_bounds__(64 * WV) void int8_stream_kernel(Int8Params p, uint
         for (int f = 0; f < NR; ++f)
           fa[s][f] = *reinterpret_cast<const v4i*>(sl + chunk_offset(16 * f + li, 4 * s + lc));
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
-          fb[s][m] = *reinterpret_cast<const v4i*>(sl + chunk_offset(kRowsW + 16 * m + li, 4 * s + lc));
+        for (int m = 0; m < MT; ++m) {
+          if constexpr (kBf16) {
+            const int r = std::min(li, (int)p.e.T - 1);
+            fb[s][m] = *reinterpret_cast<const v4i*>(xres + (r * xstages + wave + i * WV) * kStageK +
+                                                     (((4 * s + lc) ^ ((r >> 1) & 7)) << 4));
+          } else {
+            fb[s][m] = *reinterpret_cast<const v4i*>(sl + chunk_offset(kRowsW + 16 * m + li, 4 * s + lc));
+          }
+        }
       }
 #pragma unroll
       for (int j = 0; j < kScaleOps; ++j)
@@ -179,7 +244,7 @@ __global__ __launch_bounds__(64 * WV) void int8_stream_kernel(Int8Params p, uint
       wait_lds();   // the slot is read: refill it
       --in_flight;
       issue_next(tj);
-      if (p.present < 8 && wave + i * WV == nk - 1) {
+      if (!kBf16 && p.present < 8 && wave + i * WV == nk - 1) {
 #pragma unroll
         for (int s = 0; s < 2; ++s)
 #pragma unroll
@@ -234,7 +299,7 @@ __global__ __launch_bounds__(64 * WV) void int8_stream_kernel(Int8Params p, uint
             s[4 + i] += b[i];
           }
         }
-        const float xs = __uint_as_float(scales[kRowsW + tl]);
+        const float xs = kBf16 ? s_xs[tl] : __uint_as_float(scales[kRowsW + tl]);
 #pragma unroll
         for (int i = 0; i < 8; ++i) z[i] = (float)s[i] * xs * __uint_as_float(scales[f + i]);
       };
@@ -252,29 +317,53 @@ __global__ __launch_bounds__(64 * WV) void int8_stream_kernel(Int8Params p, uint
 #pragma unroll
         for (int i = 0; i < 8; ++i) z[i] = silu_mul(z[i], up[i]);
       }
-      finish8(p.e, t * N + n, 0, cnt8, b, res, z);
+      if constexpr (kGrouped) store8(p.e.y, t * N + n, 0, cnt8, z);
+      else finish8(p.e, t * N + n, 0, cnt8, b, res, z);
     }
   }
 }
 
-template <int NR, int MT, int WV, int S, bool kGrouped, bool kSwiglu, bool kOnce>
+template <int NR, int MT, int WV, int S, bool kGrouped, bool kSwiglu, bool kOnce, bool kBf16 = false>
 int launch_stream(const Int8Params& p, int per_cu, hipStream_t stream, const char* name) {
   constexpr int kOut = kSwiglu ? 8 * NR : 16 * NR;
   const int64_t n_tiles = (p.e.N + kOut - 1) / kOut;
   const int64_t t_tiles = (p.e.T + 16 * MT - 1) / (16 * MT) + (kGrouped ? p.E : 0);
   const int64_t grid = std::min<int64_t>(n_tiles * t_tiles, (int64_t)num_cus() * per_cu);
   const size_t tab = kGrouped ? (size_t)(p.E + 1) * 8 : 0;
-  int8_stream_kernel<NR, MT, WV, S, kGrouped, kSwiglu, kOnce>
+  int8_stream_kernel<NR, MT, WV, S, kGrouped, kSwiglu, kOnce, kBf16>
       <<<dim3((unsigned)grid), dim3(64 * WV), tab, stream>>>(p, (uint32_t)n_tiles, (uint32_t)t_tiles);
   return check_launch(name);
 }
 
 }  // namespace
 
-int launch_int8_stream(const Int8Params& p, hipStream_t stream, const char* name) {
-  if (!p.gl) return launch_stream<2, 1, 4, 3, false, false, false>(p, 2, stream, name);
-  if (p.swiglu) return launch_stream<2, 1, 4, 3, true, true, false>(p, 2, stream, name);
-  return launch_stream<2, 1, 4, 3, true, false, false>(p, 2, stream, name);
+namespace {
+
+template <int NR, int MT, int WV, int S, bool kOnce>
+int launch_any(const Int8Params& p, int per_cu, hipStream_t stream, const char* name) {
+  if (!p.gl) return launch_stream<NR, MT, WV, S, false, false, kOnce>(p, per_cu, stream, name);
+  if (p.swiglu) return launch_stream<NR, MT, WV, S, true, true, kOnce>(p, per_cu, stream, name);
+  return launch_stream<NR, MT, WV, S, true, false, kOnce>(p, per_cu, stream, name);
+}
+
+}  // namespace
+
+int launch_int8_32x16(const Int8Params& p, hipStream_t stream, const char* name) {
+  return launch_any<2, 1, 4, 2, false>(p, 2, stream, name);
+}
+int launch_int8_32x16_wide(const Int8Params& p, hipStream_t stream, const char* name) {
+  return launch_any<2, 1, 8, 2, false>(p, 1, stream, name);
+}
+int launch_int8_32x32(const Int8Params& p, hipStream_t stream, const char* name) {
+  return launch_any<2, 2, 4, 2, true>(p, 2, stream, name);
+}
+int launch_int8_64x64(const Int8Params& p, hipStream_t stream, const char* name) {
+  return launch_any<4, 4, 2, 2, true>(p, 2, stream, name);
+}
+
+bool int8_resident(int64_t T, int64_t K, int64_t N) { return T <= 16 && T * K <= kMaxResident && N <= 32 * 256; }
+int launch_int8_resident(const Int8Params& p, hipStream_t stream, const char* name) {
+  return launch_stream<2, 1, 8, 2, false, false, true, true>(p, 1, stream, name);
 }
 
 }  // namespace mxmoe

@@ -129,7 +129,7 @@ __global__ __launch_bounds__(64 * WN * WM) void int8_tile_kernel(Int8Params p, i
   };
   constexpr int kLoadOps = kOpsA + kOpsB;
   // a stage's loads go out behind the first MFMAs of one sub-step
-  constexpr int kPer = 4;
+  constexpr int kPer = 2;
   auto load_part = [&](int i, const Src& s, int ks, int gs) __attribute__((always_inline)) {
     const uint32_t base = ring0 + (uint32_t)(gs & 1) * (uint32_t)kSlot;
     const int present = ks == nk - 1 ? p.present : 8;
@@ -319,8 +319,7 @@ __global__ __launch_bounds__(64 * WN * WM) void int8_tile_kernel(Int8Params p, i
         auto el_of = [&](int i) __attribute__((always_inline)) -> int64_t {
           return (t_w + kStep * i) * N + cur.n0 + (kSwiglu ? row / 2 : row);
         };
-        uint4 res[kGrouped ? 1 : 8];
-        res[0] = make_uint4(0, 0, 0, 0);
+        uint4 res[8];   // (not kGrouped)
 #pragma unroll
         for (int fm = 0; fm < NB; ++fm) {
 #pragma unroll
@@ -351,19 +350,21 @@ __global__ __launch_bounds__(64 * WN * WM) void int8_tile_kernel(Int8Params p, i
               }
             }
           }
-          float b[8] = {}, sg[8], su[8];
           auto get8 = [&](const float* src, float (&v)[8]) __attribute__((always_inline)) {
             const float4 a = reinterpret_cast<const float4*>(src)[0], c = reinterpret_cast<const float4*>(src)[1];
             v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
             v[4] = c.x; v[5] = c.y; v[6] = c.z; v[7] = c.w;
           };
-          get8(s_ws + row + 8 * rc, sg);
-          if constexpr (kSwiglu) get8(s_ws + row + 32 + 8 * rc, su);
-          if constexpr (!kGrouped) get8(s_bias + row + 8 * rc, b);
 #pragma unroll
           for (int it = 0; it < kTok / kStep; ++it) {
             const int r = kStep * it + rr, i = kTok / kStep * fm + it;
             const float xs = s_xs[32 * NB * wm + 32 * fm + r];
+            // (read again for every token: held, they would spill)
+            float b[8] = {}, sg[8], su[8];
+            const int at_row = opaque(row + 8 * rc);
+            get8(s_ws + at_row, sg);
+            if constexpr (kSwiglu) get8(s_ws + at_row + 32, su);
+            if constexpr (!kGrouped) get8(s_bias + at_row, b);
             auto read8 = [&](int chunk, const float (&ws)[8], float (&z)[8]) __attribute__((always_inline)) {
               const i32x4 z0 = *reinterpret_cast<const lds_i32x4*>(stg + r * 256 + ((chunk ^ (r & 15)) << 4));
               const i32x4 z1 = *reinterpret_cast<const lds_i32x4*>(stg + r * 256 + (((chunk + 1) ^ (r & 15)) << 4));
@@ -381,7 +382,9 @@ __global__ __launch_bounds__(64 * WN * WM) void int8_tile_kernel(Int8Params p, i
 #pragma unroll
               for (int v = 0; v < 8; ++v) z[v] = silu_mul(z[v], u[v]);
             }
-            finish8(p.e, el_of(i), lane_el, rr + kStep * i < t_left ? cnt : 0, b, res[kGrouped ? 0 : i], z);
+            const int have = rr + kStep * i < t_left ? cnt : 0;
+            if constexpr (kGrouped) store8(p.e.y, el_of(i), lane_el, have, z);
+            else finish8(p.e, el_of(i), lane_el, have, b, res[i], z);
             __builtin_amdgcn_sched_barrier(0);   // one row at a time
           }
           asm volatile("" ::: "memory");

@@ -102,6 +102,25 @@ def test_linear(i):
                     residual=c % 4 < 2, in_place=c % 8 < 2, what=f"case {c}")
 
 
+@pytest.mark.parametrize("T,K,N", [
+    (1, 16, 5), (1, 2048, 4096), (1, 65536, 33), (2, 4112, 100), (3, 144, 257), (5, 2048, 8192), (7, 9360, 64), (13, 240, 70),
+    (16, 4096, 96), (16, 16, 64), (15, 2064, 31), (9, 528, 8190), (1, 2048, 8224), (16, 4112, 40),
+])
+def test_few_bf16_tokens(T, K, N):
+    """Tokens that every workgroup quantises itself, and the sizes just past them."""
+    linear_case(T, K, N, T + K, int8_in=False, bias="fp32", act="silu", residual=True, what="bf16 tokens")
+    if T <= 16 and T * K <= 65536 and N <= 8192:
+        assert mx.int8_linear_workspace_size(T, K, N, False) == 0
+    # the same codes and scales as int8_quantize's
+    x = torch.randn((T, K), device="cuda").bfloat16()
+    x[:, ::7] *= 30
+    w, ws = i8_dev(codes(np.random.default_rng(1), (N, K))), torch.full((N,), 2.0 ** -10, device="cuda")
+    q, s = mx.int8_quantize(x)
+    a, b = mx.int8_linear(x, w, ws), mx.int8_linear(q, w, ws, x_s=s)
+    torch.cuda.synchronize()
+    assert torch.equal(a, b)
+
+
 def test_extremes_are_exact():
     """Sums of the largest magnitude: +-128 * 128 * K, and cancelling ones."""
     K = 131056
