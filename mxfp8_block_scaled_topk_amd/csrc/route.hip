@@ -405,24 +405,21 @@ __global__ __launch_bounds__(kThreads) void route_quant_kernel(RouteParams p) {
   const int rowb = p.row_bytes;   // payload K bytes, then s_stride scale bytes, padded to 16
   const int n_it = nbt * hpr;     // half-blocks; even, so lane pairs stay together
   constexpr int kLd = 4;          // half-blocks whose loads a lane has in flight at once
+  // kAny: a group of 64 lanes (16 where a row has no more pieces) takes a row at a time
+  const int lanes = kAny && hpr <= 16 ? 16 : 64, group = tid / lanes, groups = kThreads / lanes, sub = tid % lanes;
   if constexpr (kAny) {
-    for (int it0 = tid; it0 < n_it; it0 += kLd * kThreads) {
-      u32x4_any u[kLd];
+    for (int tl = group; tl < nbt; tl += groups) {
+      const uint8_t* src = p.rows + (t0 + tb + tl) * p.ld_bytes;
+      uint8_t* dst = xbuf + tl * rowb;
+      for (int hb0 = sub; hb0 < hpr; hb0 += kLd * lanes) {
+        u32x4_any u[kLd];
 #pragma unroll
-      for (int i = 0; i < kLd; ++i) {
-        const int it = it0 + i * kThreads;
-        if (it < n_it) {
-          const int tl = it / hpr, hb = it - tl * hpr;
-          u[i] = load_piece(p, p.rows + (t0 + tb + tl) * p.ld_bytes + piece_at(p, hb));
-        }
-      }
+        for (int i = 0; i < kLd; ++i)
+          if (hb0 + i * lanes < hpr) u[i] = load_piece(p, src + piece_at(p, hb0 + i * lanes));
 #pragma unroll
-      for (int i = 0; i < kLd; ++i) {
-        const int it = it0 + i * kThreads;
-        if (it < n_it) {
-          const int tl = it / hpr, hb = it - tl * hpr;
-          *reinterpret_cast<uint4*>(xbuf + tl * rowb + hb * 16) = make_uint4(u[i].x, u[i].y, u[i].z, u[i].w);
-        }
+        for (int i = 0; i < kLd; ++i)
+          if (hb0 + i * lanes < hpr)
+            *reinterpret_cast<uint4*>(dst + (hb0 + i * lanes) * 16) = make_uint4(u[i].x, u[i].y, u[i].z, u[i].w);
       }
     }
   }
@@ -585,13 +582,15 @@ __global__ __launch_bounds__(kThreads) void route_quant_kernel(RouteParams p) {
   // ---- stores: each buffered row to the token's k rows ---------------------
   const int k = p.k;
   if constexpr (kAny) {
-    for (int idx = tid; idx < nbt * k * hpr; idx += kThreads) {
-      const int rowi = idx / hpr, ch = idx - rowi * hpr;
-      const int tl = rowi / k, j = rowi - tl * k;
-      const int r = s_pos[(tb + tl) * k + j];
+    for (int rowi = group; rowi < nbt * k; rowi += groups) {
+      const int r = s_pos[tb * k + rowi];
       if (r < 0) continue;
-      const uint4 u = *reinterpret_cast<const uint4*>(xbuf + tl * rowb + ch * 16);
-      store_piece(p, p.xq + (int64_t)r * p.K + piece_at(p, ch), u32x4_any{u.x, u.y, u.z, u.w});
+      const uint8_t* src = xbuf + (rowi / k) * rowb;
+      uint8_t* dst = p.xq + (int64_t)r * p.K;
+      for (int hb = sub; hb < hpr; hb += lanes) {
+        const uint4 u = *reinterpret_cast<const uint4*>(src + hb * 16);
+        store_piece(p, dst + piece_at(p, hb), u32x4_any{u.x, u.y, u.z, u.w});
+      }
     }
     if (p.row_s)
       for (int idx = tid; idx < (te - tb) * k; idx += kThreads) {

@@ -95,23 +95,53 @@ __device__ __forceinline__ void store_piece(uint8_t* p, const u32x4_any& u) {
 
 constexpr int kThreads = 256;
 
-template <int kType>
+__device__ __forceinline__ int64_t uniform(int64_t v) {
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)v);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)((uint64_t)v >> 32));
+  return (int64_t)(((uint64_t)hi << 32) | lo);
+}
+
+// kLanes = 64: a wave takes 64 pieces of a token at a time, whose k indices and
+// weights come through the scalar unit.  16: rows of 16 pieces at most, four tokens
+// a wave.  The rows of kBatch assignments are requested before they are added.
+template <int kType, int kLanes>
 __global__ __launch_bounds__(kThreads) void unpermute_kernel(UnpermuteParams p) {
-  constexpr int kPer = Elem<kType>::kPer;
+  constexpr int kPer = Elem<kType>::kPer, kBatch = 8;
+  const int lane = threadIdx.x & 63;
   const int64_t pieces = (p.row_bytes + 15) / 16;
-  const int64_t total = p.T * pieces;
-  for (int64_t it = blockIdx.x * (int64_t)kThreads + threadIdx.x; it < total; it += (int64_t)gridDim.x * kThreads) {
-    const int64_t t = it / pieces;
-    const int64_t at = std::min<int64_t>(16 * (it - t * pieces), p.row_bytes - 16);
+  const int64_t blocks = (pieces + 63) / 64;   // of a row; 1 when kLanes = 16
+  const int64_t units = kLanes == 64 ? p.T * blocks : (p.T + 3) / 4;
+  const int64_t first = (int64_t)blockIdx.x * (kThreads / 64) + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  for (int64_t u = first; u < units; u += (int64_t)gridDim.x * (kThreads / 64)) {
+    const int64_t t = kLanes == 64 ? uniform(u / blocks) : 4 * u + lane / kLanes;
+    const int64_t piece = kLanes == 64 ? (u - t * blocks) * 64 + lane : lane % kLanes;
+    if (piece >= pieces || t >= p.T) continue;
+    const int64_t at = std::min<int64_t>(16 * piece, p.row_bytes - 16);
     float acc[kPer] = {};
-    for (int j = 0; j < p.k; ++j) {
-      const int32_t r = p.eri[t * p.k + j];
-      if (r < 0 || r >= p.M) continue;
-      float v[kPer];
-      unpack<kType>(load_piece(p.y + r * p.row_bytes + at), v);
-      const float w = p.w ? p.w[t * p.k + j] : 1.0f;
+    for (int j0 = 0; j0 < p.k; j0 += kBatch) {
+      u32x4_any row[kBatch];
+      int32_t r[kBatch];
+      float w[kBatch];
+      bool ok[kBatch];
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) acc[i] += w * v[i];
+      for (int b = 0; b < kBatch; ++b) {   // (assignments past the last repeat it)
+        const int64_t i = t * p.k + std::min(j0 + b, p.k - 1);
+        r[b] = p.eri[i];
+        w[b] = p.w ? p.w[i] : 1.0f;
+      }
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b) {
+        ok[b] = j0 + b < p.k && r[b] >= 0 && r[b] < p.M;
+        if (ok[b]) row[b] = load_piece(p.y + r[b] * p.row_bytes + at);
+      }
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b) {
+        if (!ok[b]) continue;
+        float v[kPer];
+        unpack<kType>(row[b], v);
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) acc[i] += w[b] * v[i];
+      }
     }
     store_piece(p.out + t * p.row_bytes + at, pack<kType>(acc));
   }
@@ -133,48 +163,181 @@ __global__ __launch_bounds__(kThreads) void unpermute_tiny(UnpermuteParams p) {
   }
 }
 
-// One workgroup per assignment.
+// The sum over 16 lanes (a DPP row), in its last lane.
+__device__ __forceinline__ float row_sum16(float x) {
+  x += dpp_f32<0x111>(0.0f, x);   // row_shr:1
+  x += dpp_f32<0x112>(0.0f, x);   // row_shr:2
+  x += dpp_f32<0x114>(0.0f, x);   // row_shr:4
+  x += dpp_f32<0x118>(0.0f, x);   // row_shr:8
+  return x;
+}
+
+// W waves share a token (four tokens of one wave each in a workgroup, or with
+// kLanes = 16 four tokens a wave), whose row of dout stays in registers, C pieces a
+// lane, while its rows of y are read and those of dy written, kBatch assignments at
+// a time.  With few tokens `splits` workgroups (waves) share a token's assignments,
+// `per` each.
+template <int kType, int W, int C, int kLanes>
+__global__ __launch_bounds__(64 * (W < 4 ? 4 : W)) void unpermute_backward_kernel(UnpermuteParams p, int splits, int per) {
+  constexpr int kPer = Elem<kType>::kPer, kBytes = Elem<kType>::kBytes, kBatch = 2;
+  constexpr int kUnits = W < 4 ? 4 : 1;   // per workgroup
+  static_assert(W == 1 || (W >= 4 && kLanes == 64), "a wave per token, or the workgroup's waves share one");
+  __shared__ float part[kBatch][W];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int64_t pieces = (p.row_bytes + 15) / 16;
+  const int64_t units = (kLanes == 64 ? p.T : (p.T + 3) / 4) * splits;
+  const int64_t first = (int64_t)blockIdx.x * kUnits + (W == 1 ? __builtin_amdgcn_readfirstlane(tid >> 6) : 0);
+  for (int64_t u = first; u < units; u += (int64_t)gridDim.x * kUnits) {
+    const int64_t tb = uniform(u / splits);
+    const int j0 = (int)(u - tb * splits) * per, j1 = std::min(j0 + per, p.k);
+    const int64_t t = kLanes == 64 ? tb : 4 * tb + lane / kLanes;
+    const bool real = kLanes == 64 || t < p.T;
+    u32x4_any d[C];
+    int64_t at[C];
+    bool has[C];
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      const int64_t piece = W == 1 ? c * kLanes + lane % kLanes : c * 64 * W + tid;
+      has[c] = real && piece < pieces;
+      at[c] = std::min<int64_t>(16 * piece, p.row_bytes - 16);
+      if (has[c]) d[c] = load_piece(p.dout + t * p.row_bytes + at[c]);
+    }
+    for (int j = j0; j < j1; j += kBatch) {
+      int32_t r[kBatch];
+      float w[kBatch], sum[kBatch];
+      bool ok[kBatch];
+      u32x4_any y[kBatch][C];
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b) {
+        // (assignments past the last repeat it)
+        const int64_t i = (real ? t : 0) * p.k + std::min(j + b, j1 - 1);
+        r[b] = p.eri[i];
+        w[b] = p.w ? p.w[i] : 1.0f;
+        sum[b] = 0.0f;
+      }
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b) {
+        ok[b] = real && j + b < j1 && r[b] >= 0 && r[b] < p.M;
+        if (p.dw && ok[b]) {
+#pragma unroll
+          for (int c = 0; c < C; ++c)
+            if (has[c]) y[b][c] = load_piece(p.y + r[b] * p.row_bytes + at[c]);
+        }
+      }
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b) {
+        if (!ok[b]) continue;
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+          if (!has[c]) continue;
+          float v[kPer];
+          unpack<kType>(d[c], v);
+          if (p.dw) {
+            float z[kPer];
+            unpack<kType>(y[b][c], z);
+            const int64_t piece = W == 1 ? c * kLanes + lane % kLanes : c * 64 * W + tid;
+            const int skip = (int)(16 * piece - at[c]) / kBytes;   // elements that the piece before holds too
+#pragma unroll
+            for (int e = 0; e < kPer; ++e) sum[b] += e >= skip ? v[e] * z[e] : 0.0f;
+          }
+#pragma unroll
+          for (int e = 0; e < kPer; ++e) v[e] *= w[b];
+          store_piece(p.out + r[b] * p.row_bytes + at[c], pack<kType>(v));
+        }
+      }
+      if (!p.dw) continue;
+      if constexpr (kLanes == 16) {
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) {
+          sum[b] = row_sum16(sum[b]);
+          if (lane % 16 == 15 && real && j + b < j1) p.dw[t * p.k + j + b] = sum[b];
+        }
+      } else {
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) sum[b] = wave_sum(sum[b]);
+        if constexpr (W > 1) {
+          __syncthreads();   // the last partials are read
+          if (lane == 0) {
+#pragma unroll
+            for (int b = 0; b < kBatch; ++b) part[b][tid >> 6] = sum[b];
+          }
+          __syncthreads();
+#pragma unroll
+          for (int b = 0; b < kBatch; ++b) {
+            sum[b] = 0.0f;
+#pragma unroll
+            for (int i = 0; i < W; ++i) sum[b] += part[b][i];
+          }
+        }
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b)
+          if (j + b < j1 && (W == 1 ? lane : tid) == b) p.dw[t * p.k + j + b] = sum[b];
+      }
+    }
+  }
+}
+
+// Rows of more than 64 KB: a workgroup per assignment, dout read for each.
+constexpr int kLongWaves = 16;
 template <int kType>
-__global__ __launch_bounds__(kThreads) void unpermute_backward_kernel(UnpermuteParams p) {
+__global__ __launch_bounds__(64 * kLongWaves) void unpermute_backward_long(UnpermuteParams p) {
   constexpr int kPer = Elem<kType>::kPer, kBytes = Elem<kType>::kBytes;
-  __shared__ float part[kThreads / 64];
+  __shared__ float part[kLongWaves];
   const int64_t total = p.T * p.k;
   for (int64_t i = blockIdx.x; i < total; i += gridDim.x) {
     const int64_t t = i / p.k;
     const int32_t r = p.eri[i];
-    const bool real = r >= 0 && r < p.M;
     float sum = 0.0f;
-    if (real) {
+    if (r >= 0 && r < p.M) {
       const float w = p.w ? p.w[i] : 1.0f;
-      if (p.row_bytes >= 16) {
-        for (int64_t b = 16 * (int64_t)threadIdx.x; b < p.row_bytes; b += 16 * kThreads) {
-          const int64_t at = std::min<int64_t>(b, p.row_bytes - 16);
-          const int skip = (int)(b - at) / kBytes;   // elements that the piece before holds too
-          float d[kPer];
-          unpack<kType>(load_piece(p.dout + t * p.row_bytes + at), d);
-          if (p.dw) {
-            float v[kPer];
-            unpack<kType>(load_piece(p.y + r * p.row_bytes + at), v);
+      for (int64_t b = 16 * (int64_t)threadIdx.x; b < p.row_bytes; b += 16 * 64 * kLongWaves) {
+        const int64_t at = std::min<int64_t>(b, p.row_bytes - 16);
+        const int skip = (int)(b - at) / kBytes;   // elements that the piece before holds too
+        float d[kPer];
+        unpack<kType>(load_piece(p.dout + t * p.row_bytes + at), d);
+        if (p.dw) {
+          float v[kPer];
+          unpack<kType>(load_piece(p.y + r * p.row_bytes + at), v);
 #pragma unroll
-            for (int e = 0; e < kPer; ++e) sum += e >= skip ? d[e] * v[e] : 0.0f;
-          }
-#pragma unroll
-          for (int e = 0; e < kPer; ++e) d[e] *= w;
-          store_piece(p.out + r * p.row_bytes + at, pack<kType>(d));
+          for (int e = 0; e < kPer; ++e) sum += e >= skip ? d[e] * v[e] : 0.0f;
         }
-      } else if (threadIdx.x < p.K) {
-        const int64_t at = threadIdx.x * kBytes;
-        const float d = load1<kType>(p.dout + t * p.row_bytes + at);
-        if (p.dw) sum = d * load1<kType>(p.y + r * p.row_bytes + at);
-        store1<kType>(p.out + r * p.row_bytes + at, d * w);
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) d[e] *= w;
+        store_piece(p.out + r * p.row_bytes + at, pack<kType>(d));
       }
     }
     if (!p.dw) continue;
     sum = wave_sum(sum);
-    __syncthreads();   // the previous assignment's partials are read
+    __syncthreads();   // the last assignment's partials are read
     if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = sum;
     __syncthreads();
-    if (threadIdx.x == 0) p.dw[i] = (part[0] + part[1]) + (part[2] + part[3]);
+    if (threadIdx.x == 0) {
+      sum = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kLongWaves; ++w) sum += part[w];
+      p.dw[i] = sum;
+    }
+  }
+}
+
+// Rows of fewer than 16 bytes: an assignment a thread.
+template <int kType>
+__global__ __launch_bounds__(kThreads) void unpermute_backward_tiny(UnpermuteParams p) {
+  constexpr int kBytes = Elem<kType>::kBytes;
+  const int64_t total = p.T * p.k;
+  for (int64_t i = blockIdx.x * (int64_t)kThreads + threadIdx.x; i < total; i += (int64_t)gridDim.x * kThreads) {
+    const int64_t t = i / p.k;
+    const int32_t r = p.eri[i];
+    float sum = 0.0f;
+    if (r >= 0 && r < p.M) {
+      const float w = p.w ? p.w[i] : 1.0f;
+      for (int c = 0; c < (int)p.K; ++c) {
+        const float d = load1<kType>(p.dout + t * p.row_bytes + c * kBytes);
+        if (p.dw) sum += d * load1<kType>(p.y + r * p.row_bytes + c * kBytes);
+        store1<kType>(p.out + r * p.row_bytes + c * kBytes, d * w);
+      }
+    }
+    if (p.dw) p.dw[i] = sum;
   }
 }
 
@@ -200,21 +363,44 @@ int by_type(int type, F f) {
 }
 
 int launch_unpermute(const UnpermuteParams& p, int type, hipStream_t stream) {
-  const int64_t total = p.row_bytes < 16 ? p.T * p.K : p.T * ((p.row_bytes + 15) / 16);
-  const int64_t grid = std::min<int64_t>((total + kThreads - 1) / kThreads, (int64_t)num_cus() * 32);
+  const int64_t pieces = (p.row_bytes + 15) / 16, cap = (int64_t)num_cus() * 32;
   return by_type(type, [&](auto t) {
     constexpr int kType = decltype(t)::value;
-    if (p.row_bytes < 16) unpermute_tiny<kType><<<dim3((unsigned)grid), dim3(kThreads), 0, stream>>>(p);
-    else unpermute_kernel<kType><<<dim3((unsigned)grid), dim3(kThreads), 0, stream>>>(p);
+    auto grid = [&](int64_t n, int64_t per) { return dim3((unsigned)std::min<int64_t>((n + per - 1) / per, cap)); };
+    if (p.row_bytes < 16) unpermute_tiny<kType><<<grid(p.T * p.K, kThreads), dim3(kThreads), 0, stream>>>(p);
+    else if (pieces <= 16) unpermute_kernel<kType, 16><<<grid((p.T + 3) / 4, 4), dim3(kThreads), 0, stream>>>(p);
+    else unpermute_kernel<kType, 64><<<grid(p.T * ((pieces + 63) / 64), 4), dim3(kThreads), 0, stream>>>(p);
     return check_launch("moe_unpermute");
   });
 }
 
 int launch_unpermute_backward(const UnpermuteParams& p, int type, hipStream_t stream) {
-  const int64_t grid = std::min<int64_t>(p.T * p.k, (int64_t)num_cus() * 32);
+  const int64_t pieces = (p.row_bytes + 15) / 16, cap = (int64_t)num_cus() * 32;
   return by_type(type, [&](auto t) {
     constexpr int kType = decltype(t)::value;
-    unpermute_backward_kernel<kType><<<dim3((unsigned)grid), dim3(kThreads), 0, stream>>>(p);
+    auto grid = [&](int64_t n, int64_t per) { return dim3((unsigned)std::min<int64_t>((n + per - 1) / per, cap)); };
+    // a token's assignments over several units until there are four workgroups a CU
+    auto go = [&](auto w, auto c, auto lanes) {
+      constexpr int W = decltype(w)::value, C = decltype(c)::value, L = decltype(lanes)::value;
+      const int64_t tokens = L == 64 ? p.T : (p.T + 3) / 4, in_wg = W < 4 ? 4 : 1;
+      const int64_t want = (int64_t)num_cus() * 4 * in_wg;
+      const int64_t splits = std::max<int64_t>(1, std::min<int64_t>(p.k, want / tokens));
+      const int64_t per = (p.k + splits - 1) / splits, used = (p.k + per - 1) / per;
+      unpermute_backward_kernel<kType, W, C, L><<<grid(tokens * used, in_wg), dim3(64 * (W < 4 ? 4 : W)), 0, stream>>>(
+          p, (int)used, (int)per);
+    };
+    using std::integral_constant;
+    const bool few = p.T * p.k <= num_cus();
+    if (p.row_bytes < 16) unpermute_backward_tiny<kType><<<grid(p.T * p.k, kThreads), dim3(kThreads), 0, stream>>>(p);
+    else if (pieces <= 16) go(integral_constant<int, 1>{}, integral_constant<int, 1>{}, integral_constant<int, 16>{});
+    else if (pieces <= 64) go(integral_constant<int, 1>{}, integral_constant<int, 1>{}, integral_constant<int, 64>{});
+    else if (few && pieces <= 256) go(integral_constant<int, 4>{}, integral_constant<int, 1>{}, integral_constant<int, 64>{});
+    else if (few && pieces <= 1024) go(integral_constant<int, 16>{}, integral_constant<int, 1>{}, integral_constant<int, 64>{});
+    else if (pieces <= 128) go(integral_constant<int, 1>{}, integral_constant<int, 2>{}, integral_constant<int, 64>{});
+    else if (pieces <= 256) go(integral_constant<int, 1>{}, integral_constant<int, 4>{}, integral_constant<int, 64>{});
+    else if (pieces <= 1024) go(integral_constant<int, 4>{}, integral_constant<int, 4>{}, integral_constant<int, 64>{});
+    else if (pieces <= 4096) go(integral_constant<int, 16>{}, integral_constant<int, 4>{}, integral_constant<int, 64>{});
+    else unpermute_backward_long<kType><<<grid(p.T * p.k, 1), dim3(64 * kLongWaves), 0, stream>>>(p);
     return check_launch("moe_unpermute_backward");
   });
 }

@@ -57,8 +57,9 @@ def lin(lib, T=4, K=64, N=96, x=at(0), xs=at(1), w=at(2), ws=at(3), b=at(4), bt=
 def test_linear_validation(lib):
     for kw in (dict(T=-1), dict(K=0), dict(N=0), dict(bt=2), dict(bt=-1), dict(act=5), dict(act=-1), dict(x=None),
                dict(w=None), dict(ws=None), dict(y=None), dict(y=at(0)), dict(y=at(1)), dict(y=at(2)), dict(y=at(3)),
-               dict(y=at(4)), dict(y=odd(5, 2)), dict(xs=None, wsp=None, wsb=1 << 20), dict(xs=None, wsp=at(0), wsb=1 << 20),
-               dict(xs=None, wsp=at(6), wsb=1 << 20), dict(xs=None, wsp=at(5), wsb=1 << 20)):
+               dict(y=at(4)), dict(y=odd(5, 2)), dict(T=40, xs=None, wsp=None, wsb=1 << 20),
+               dict(T=40, xs=None, wsp=at(0), wsb=1 << 20), dict(T=40, xs=None, wsp=at(6), wsb=1 << 20),
+               dict(T=40, xs=None, wsp=at(5), wsb=1 << 20)):
         assert lin(lib, **kw) == INVALID, kw
     for v in NEG:
         for n in ("T", "K", "N"):
@@ -69,13 +70,14 @@ def test_linear_validation(lib):
     for kw in (dict(K=8), dict(K=72), dict(K=1 << 17), dict(K=1 << 20), dict(N=1 << 30), dict(T=1 << 30, N=1 << 10),
                dict(x=odd(0, 8)), dict(w=odd(2, 8)), dict(xs=odd(1, 2)), dict(ws=odd(3, 1)), dict(b=odd(4, 1)),
                dict(b=odd(4, 2), bt=1), dict(r=odd(5, 1)), dict(y=odd(6, 1)), dict(xs=None, x=odd(0, 1), wsp=at(9), wsb=1 << 20),
-               dict(xs=None, wsp=odd(9, 128), wsb=1 << 20)):
+               dict(T=40, xs=None, wsp=odd(9, 128), wsb=1 << 20)):
         assert lin(lib, **kw) == UNSUPPORTED, kw
-    need = lib.int8_linear_workspace_size(4, 64, 96, 0)
-    assert need >= 4 * 64 + 16 and lib.int8_linear_workspace_size(4, 64, 96, 1) == 0
-    assert lin(lib, xs=None, wsp=at(9), wsb=need - 1) == WORKSPACE
+    need = lib.int8_linear_workspace_size(40, 64, 96, 0)
+    assert need >= 40 * 64 + 160 and lib.int8_linear_workspace_size(40, 64, 96, 1) == 0
+    assert lib.int8_linear_workspace_size(4, 64, 96, 0) == 0   # few tokens are quantised in place
+    assert lin(lib, T=40, xs=None, wsp=at(9), wsb=need - 1) == WORKSPACE
     for v in NEG + BIG + [0]:
-        assert lib.int8_linear_workspace_size(4, v, 96, 0) == 0
+        assert lib.int8_linear_workspace_size(40, v, 96, 0) == 0
     assert lin(lib, T=0, x=None, w=None, ws=None, y=None, b=None, r=None) == OK
 
 
