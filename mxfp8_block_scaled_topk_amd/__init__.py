@@ -1016,6 +1016,9 @@ def gmm_int8(a, a_s, w, w_s, group_list, group_list_type=GROUP_COUNT, swiglu=Fal
     return out
 
 
+_ELEMENT_BYTES = {torch.bfloat16: 2, torch.float16: 2, torch.float32: 4, torch.int8: 1, torch.uint8: 1}   # (the usual ones)
+
+
 def moe_permute(x, topk_ids, E, x_s=None, out=None, workspace=None, stream=None):
     """Token rows sorted by expert, as they are: x [T, K] of any type of 1, 2 or 4
     bytes (rows may be strided), topk_ids int32 [T, k]; x_s fp32 [T] (the scales
@@ -1026,20 +1029,23 @@ def moe_permute(x, topk_ids, E, x_s=None, out=None, workspace=None, stream=None)
     moe_unpermute of xp's gradient, without weights."""
     if not isinstance(x, _Tensor):
         _need(x, None, "x")
-    if x.dim() != 2:
-        raise ValueError(f"x must have 2 dims, got {x.dim()}")
-    size = x.element_size()
-    if size not in (1, 2, 4) or x.is_complex():
-        raise TypeError(f"x must be of a type of 1, 2 or 4 bytes, got {x.dtype}")
+    shape = x.shape
+    if len(shape) != 2:
+        raise ValueError(f"x must have 2 dims, got {len(shape)}")
+    size = _ELEMENT_BYTES.get(x.dtype)
+    if size is None:
+        size = x.element_size()
+        if size not in (1, 2, 4) or x.is_complex():
+            raise TypeError(f"x must be of a type of 1, 2 or 4 bytes, got {x.dtype}")
     if type(topk_ids) is not _Tensor or topk_ids.dim() != 2:
         _need(topk_ids, _I32, "topk_ids", 2)
-    T, K = x.shape
+    T, K = shape
     if K == 0:
         raise ValueError("x must have at least one element per row")
     k = topk_ids.shape[1]
     M = T * k
     dev = x.device
-    x2, ldx = _rows(x, "x")
+    x2, ldx = (x, K) if x.is_contiguous() else _rows(x, "x")
     _need_like(topk_ids, (T, k), "topk_ids", _I32, dev)
     if x_s is not None:
         _need_like(x_s, (T,), "x_s", _F32, dev)
@@ -1084,14 +1090,15 @@ _ROW_TYPES = {torch.bfloat16: TYPE_BF16, torch.float32: TYPE_F32, torch.float16:
 
 def _row_type(t, name):
     """The rows' type by number."""
-    kind = _ROW_TYPES.get(t.dtype) if isinstance(t, _Tensor) else None
+    if not isinstance(t, _Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    kind = _ROW_TYPES.get(t.dtype)
     if kind is None:
-        if not isinstance(t, _Tensor):
-            raise TypeError(f"{name} must be a torch.Tensor")
         raise TypeError(f"{name} must be bfloat16, float16 or float32, got {t.dtype}")
-    if t.dim() != 2:
-        raise ValueError(f"{name} must have 2 dims, got {t.dim()}")
-    if t.shape[1] == 0:
+    shape = t.shape
+    if len(shape) != 2:
+        raise ValueError(f"{name} must have 2 dims, got {len(shape)}")
+    if shape[1] == 0:
         raise ValueError(f"{name} must have at least one element per row")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
@@ -1102,11 +1109,13 @@ def _tokens(expanded_row_idx, k, dev):
     """T of expanded_row_idx [T*k] (of any shape)."""
     if not isinstance(k, int) or k <= 0:
         raise ValueError(f"k must be a positive int, got {k!r}")
-    _need(expanded_row_idx, _I32, "expanded_row_idx")
-    n = expanded_row_idx.numel()
+    e = expanded_row_idx
+    if not (type(e) is _Tensor and e.dtype is _I32 and e.is_contiguous() and e.device == dev):
+        _need(e, _I32, "expanded_row_idx")
+        _need_shape(e, e.shape, "expanded_row_idx", _I32, dev)
+    n = e.numel()
     if n % k:
         raise ValueError(f"expanded_row_idx must hold T*k entries, got {n} with k = {k}")
-    _need_like(expanded_row_idx, expanded_row_idx.shape, "expanded_row_idx", _I32, dev)
     return n // k
 
 
@@ -1146,24 +1155,26 @@ def moe_unpermute_backward(dout, expanded_row_idx, k, topk_w=None, y=None, out=N
     None); ``out`` gives the two instead.  Rows that no entry names are zeros in a
     dy made here and stay as they are in one given."""
     kind = _row_type(dout, "dout")
-    K = dout.shape[1]
+    rows, K = dout.shape
     dev = dout.device
     T = _tokens(expanded_row_idx, k, dev)
-    if dout.shape[0] != T:
-        raise ValueError(f"dout must have {T} rows, got {dout.shape[0]}")
+    if rows != T:
+        raise ValueError(f"dout must have {T} rows, got {rows}")
     if topk_w is not None:
         _need_like(topk_w, (T, k), "topk_w", _F32, dev)
     M = T * k
+    dtype = dout.dtype
     if y is not None:
-        _row_type(y, "y")
+        if type(y) is not _Tensor or y.dim() != 2:
+            _need(y, dtype, "y", 2)
         M = y.shape[0]
-        _need_like(y, (M, K), "y", dout.dtype, dev)
+        _need_like(y, (M, K), "y", dtype, dev)
     if out is not None:
         dy, dw = out
         if y is None:
-            _need(dy, dout.dtype, "dy", 2)
+            _need(dy, dtype, "dy", 2)
             M = dy.shape[0]
-        _need_like(dy, (M, K), "dy", dout.dtype, dev)
+        _need_like(dy, (M, K), "dy", dtype, dev)
         if (dw is None) != (y is None):
             raise ValueError("dw goes with y")
         if dw is not None:
@@ -1174,7 +1185,7 @@ def moe_unpermute_backward(dout, expanded_row_idx, k, topk_w=None, y=None, out=N
         with there:
             return moe_unpermute_backward(dout, expanded_row_idx, k, topk_w, y, out)
     if out is None:
-        dy = torch.zeros((M, K), dtype=dout.dtype, device=dev)
+        dy = torch.zeros((M, K), dtype=dtype, device=dev)
         dw = torch.empty((T, k), dtype=_F32, device=dev) if y is not None else None
     rc = load().moe_unpermute_backward(dout.data_ptr(), kind, _addr(y), _addr(topk_w), expanded_row_idx.data_ptr(), T,
                                        K, k, M, dy.data_ptr(), _addr(dw), _raw_stream(dev.index))

@@ -99,11 +99,10 @@ __device__ __forceinline__ int expert_of(const int* tile0, int E, int t) {
   return uniform(block * per + __popcll(__ballot(lane < per && e < E && tile0[std::min(e, E)] <= t)) - 1);
 }
 
-// 8 consecutive features of a token, the first cnt of which exist, to bf16 at
-// element el + lane_el of y.
-__device__ __forceinline__ void store8(uint16_t* y, int64_t el, uint32_t lane_el, int cnt, const float (&z)[8]) {
+// 8 consecutive features of a token, the first cnt of which exist, to element el +
+// lane_el of y: as bf16, or rounded here.
+__device__ __forceinline__ void store8_bits(uint16_t* y, int64_t el, uint32_t lane_el, int cnt, const u32x4_any& o) {
   if (cnt <= 0) return;
-  const u32x4_any o = {bf16x2(z[0], z[1]), bf16x2(z[2], z[3]), bf16x2(z[4], z[5]), bf16x2(z[6], z[7])};
   y = at(y, el, lane_el);
   if (cnt >= 8) {
     // written once: past the caches, which hold the operands of the tiles to come
@@ -113,6 +112,10 @@ __device__ __forceinline__ void store8(uint16_t* y, int64_t el, uint32_t lane_el
     for (int i = 0; i < 7; ++i)
       if (i < cnt) y[i] = static_cast<uint16_t>(o[i >> 1] >> (16 * (i & 1)));
   }
+}
+__device__ __forceinline__ void store8(uint16_t* y, int64_t el, uint32_t lane_el, int cnt, const float (&z)[8]) {
+  store8_bits(y, el, lane_el, cnt,
+              u32x4_any{bf16x2(z[0], z[1]), bf16x2(z[2], z[3]), bf16x2(z[4], z[5]), bf16x2(z[6], z[7])});
 }
 // The linear's epilogue: bias, activation, residual (load_res8's), then store8.
 __device__ __forceinline__ void finish8(const LinParams& p, int64_t el, uint32_t lane_el, int cnt, const float (&b)[8],

@@ -27,6 +27,9 @@ namespace {
 
 typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) const volatile u32x4 lds_u32x4_v;
+typedef __attribute__((address_space(3))) u32x4 lds_u32x4;
+typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
+typedef __attribute__((address_space(3))) u32x2 lds_u32x2;
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) i32x4 lds_i32x4;
 
@@ -50,11 +53,18 @@ __global__ __launch_bounds__(64 * WN * WM) void int8_tile_kernel(Int8Params p, i
   constexpr int kRowsA = BN / kWaves, kRowsB = BM / kWaves;   // rows each wave fetches
   constexpr int kOpsA = kRowsA / 8, kOpsB = kRowsB / 8;
   constexpr int kSlot = (BN + BM) * kStageK;
-  static_assert(NA % 2 == 0 && NB == 2, "the epilogue's 64 features x 64 tokens");
+  static_assert(NA % 2 == 0, "the epilogue's blocks of 64 weight rows");
+  // SwiGLU's epilogue has LDS of its own (2 KB a wave), so that the next tile's second
+  // stage is on its way before its stores (16K tokens to 8 of 128 experts, K = 2048, N =
+  // 768: 496 -> 472 us); the other one uses the last stage's slot (with twice the
+  // outputs of its own: K = 2048, N = 1536 447 -> 453).
+  constexpr bool kEarly = kSwiglu;
+  constexpr int kStage = 2048;
   __shared__ __attribute__((aligned(16))) uint8_t ring[2 * kSlot];
   __shared__ __attribute__((aligned(16))) float s_ws[BN];     // the tile's scales and bias
   __shared__ __attribute__((aligned(16))) float s_xs[BM];
   __shared__ __attribute__((aligned(16))) float s_bias[kGrouped ? 4 : BN];
+  __shared__ __attribute__((aligned(16))) uint8_t s_out[kEarly ? kWaves * kStage : 16];
   extern __shared__ int s_tab[];   // kGrouped: tile0 and row0, E + 1 each
 
   const int tid = threadIdx.x, lane = tid & 63;
@@ -183,11 +193,15 @@ __global__ __launch_bounds__(64 * WN * WM) void int8_tile_kernel(Int8Params p, i
   drain_barrier();
 
   int g = 0;   // stages so far: stage g is in slot g % 2
+  constexpr int kStores = NA * NB;   // kEarly: store instructions of a wave's whole tile
+  bool stored = false;   // the last tile was one
   for (int cj = 0; cj < my_tiles; ++cj) {
     const Tile cur = tile_at(cj);
     const Src csrc = src_of(cur);
-    const bool has_next = cj + 1 < my_tiles;
-    const Src nsrc = has_next ? src_of(tile_at(cj + 1)) : csrc;
+    // the tile whose stages the last two stages' loads bring (one stage a tile: the one after next)
+    const int ahead = nk > 1 ? cj + 1 : cj + 2;
+    const bool has_next = ahead < my_tiles;
+    const Src nsrc = has_next ? src_of(tile_at(ahead)) : csrc;
     // waves with no row that exists compute nothing, but load their share and meet the barriers
     const bool active = 32 * NA * wn < (kSwiglu ? 2 * cur.rows_n : cur.rows_n) && 32 * NB * wm < cur.rows_t;
     v4i fa[2][NA], fb[2][NB];   // chunk pairs 2 s and 2 s + 1 of sub-step s
@@ -196,17 +210,17 @@ __global__ __launch_bounds__(64 * WN * WM) void int8_tile_kernel(Int8Params p, i
       fa[0][f] = frag_at(gs, 2 * s, rd_a + f * 32 * kStageK);
       fa[1][f] = frag_at(gs, 2 * s + 1, rd_a + f * 32 * kStageK);
     };
-    // ks: the stage in memory
-    auto load_b = [&](int gs, int s, int f, int ks) __attribute__((always_inline)) {
+    // last: the stage is the tile's last one, whose absent chunks hold other bytes
+    auto load_b = [&](int gs, int s, int f, bool last) __attribute__((always_inline)) {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         fb[h][f] = frag_at(gs, 2 * s + h, rd_b + f * 32 * kStageK);
-        if (p.present < 8 && ks == nk - 1) {
+        if (last && p.present < 8) {
           if (2 * (2 * s + h) + lg >= p.present) fb[h][f] = v4i{0, 0, 0, 0};
         }
       }
     };
-    auto substep = [&](int gs, int ns, int nks, auto kReload, auto extra) __attribute__((always_inline)) {
+    auto substep = [&](int gs, int ns, bool last, auto kReload, auto extra) __attribute__((always_inline)) {
       if (!active) {
 #pragma unroll
         for (int m = 0; m < NA * NB; ++m) extra(m);
@@ -224,7 +238,7 @@ __global__ __launch_bounds__(64 * WN * WM) void int8_tile_kernel(Int8Params p, i
         __builtin_amdgcn_sched_barrier(0);
         if constexpr (decltype(kReload)::value) {
           if (fm == NB - 1) load_a(gs, ns, fn);
-          if (fn == NA - 1) load_b(gs, ns, fm, nks);
+          if (fn == NA - 1) load_b(gs, ns, fm, last);
         }
         extra(m);
         __builtin_amdgcn_sched_barrier(0);
@@ -240,31 +254,31 @@ __global__ __launch_bounds__(64 * WN * WM) void int8_tile_kernel(Int8Params p, i
 #pragma unroll
       for (int f = 0; f < NA; ++f) load_a(g, 0, f);
 #pragma unroll
-      for (int f = 0; f < NB; ++f) load_b(g, 0, f, 0);
+      for (int f = 0; f < NB; ++f) load_b(g, 0, f, nk == 1);
     }
-    auto stage = [&](int ks, auto kLoad) __attribute__((always_inline)) {
+    // wait: the memory instructions that may be outstanding at the stage's barrier
+    auto stage = [&](int ks, auto kLast, auto wait) __attribute__((always_inline)) {
       __builtin_amdgcn_sched_barrier(0);
-      substep(g, 1, ks, std::true_type{}, [&](int) {});
-      wait_loads<0>();    // this wave's part of stage g + 1 has landed
+      substep(g, 1, decltype(kLast)::value, std::true_type{}, [&](int) {});
+      wait();             // this wave's part of stage g + 1 has landed
       drain_barrier();    // every wave's has, and nobody reads slot g % 2 any more
-      if constexpr (decltype(kLoad)::value) {
-        // stage ks + 2 of the tile, else the first of the next one, else a repeat of
-        // the last that is never read
-        const bool in_tile = ks + 2 < nk;
-        Src t;
-        t.w = in_tile ? csrc.w : nsrc.w;
-        t.x = in_tile ? csrc.x : nsrc.x;
-        t.last_n = in_tile ? csrc.last_n : nsrc.last_n;
-        t.last_t = in_tile ? csrc.last_t : nsrc.last_t;
-        const int tks = in_tile ? ks + 2 : has_next ? 0 : nk - 1;
-        substep(g + 1, 0, ks + 1, std::true_type{}, [&](int m) __attribute__((always_inline)) {
+      // the stage after next: ks + 2 of the tile, else one of the next tile's first
+      // two, else a repeat of the last that is never read
+      const bool in_tile = ks + 2 < nk;
+      Src t;
+      t.w = in_tile ? csrc.w : nsrc.w;
+      t.x = in_tile ? csrc.x : nsrc.x;
+      t.last_n = in_tile ? csrc.last_n : nsrc.last_n;
+      t.last_t = in_tile ? csrc.last_t : nsrc.last_t;
+      const int tks = in_tile ? ks + 2 : has_next ? ks + 2 - (nk > 1 ? nk : 2) : nk - 1;
+      auto loads = [&](int m) __attribute__((always_inline)) {
 #pragma unroll
-          for (int i = kPer * m; i < kPer * m + kPer; ++i)
-            if (i < kLoadOps) load_part(i, t, tks, g + 2);
-        });
-      } else {
-        substep(g + 1, 0, 0, std::false_type{}, [&](int) {});
-      }
+        for (int i = kPer * m; i < kPer * m + kPer; ++i)
+          if (i < kLoadOps) load_part(i, t, tks, g + 2);
+      };
+      if constexpr (decltype(kLast)::value && kEarly) substep(g + 1, 0, false, std::false_type{}, loads);
+      else if constexpr (decltype(kLast)::value) substep(g + 1, 0, false, std::false_type{}, [&](int) {});
+      else substep(g + 1, 0, ks + 1 == nk - 1, std::true_type{}, loads);
       __builtin_amdgcn_sched_barrier(0);
       ++g;
     };
@@ -281,122 +295,185 @@ __global__ __launch_bounds__(64 * WN * WM) void int8_tile_kernel(Int8Params p, i
         if (p.e.bias && tid < cur.rows_n) my_bias = bias_at(p.e, cur.n0 + tid);
       }
     }
-    for (int ks = 0; ks + 1 < nk; ++ks) stage(ks, std::true_type{});
+    auto all = [] { wait_loads<0>(); };
+    int ks = 0;
+    if constexpr (kEarly) {
+      // The last tile's outputs are on their way while this one's first stage runs:
+      // the loads that it waits for were issued before them, and a wave's memory
+      // operations complete in order.
+      if (nk > 1) {
+        stage(0, std::false_type{}, [&] {
+          if (stored) wait_loads<kStores>();
+          else wait_loads<0>();
+        });
+        ks = 1;
+      }
+    }
+    for (; ks + 1 < nk; ++ks) stage(ks, std::false_type{}, all);
     if (tid < BN) s_ws[tid] = my_ws;
     if (tid < BM) s_xs[tid] = my_xs;
     if constexpr (!kGrouped) {
       if (tid < BN) s_bias[tid] = my_bias;
     }
-    stage(nk - 1, std::false_type{});
+    stage(nk - 1, std::true_type{}, all);
 
     // ---- epilogue ---------------------------------------------------------------------
-    // The slot of the last stage is free until the barrier below.  A wave stages 32
-    // tokens x 64 weight rows at a time as int32 rows of 256 bytes, 16-byte chunk c of
-    // row r at c ^ (r % 16): the writes (16 rows, one chunk) and the reads (8 lanes
-    // of a row) hit distinct banks.  Read back, a lane holds 8 consecutive features
-    // of a token, so the residual comes in and the output leaves 128 bytes of a row
-    // at a time (64 with SwiGLU, whose gates and up products are the two halves of a
-    // row).
+    // A wave's fragments turn through LDS, so that 8 lanes hold 128 bytes of a
+    // token's outputs.
+    stored = false;
     if (active) {
       const int li = opaque(lane & 31), lg = opaque(lane >> 5), lane_e = opaque(lane);
-      constexpr int kTok = 32;
-      static_assert(kWaves * kTok * 256 <= kSlot, "staging fits the slot");
-      lds_u8* stg = (lds_u8*)(uintptr_t)(ring0 + (uint32_t)((g - 1) & 1) * (uint32_t)kSlot +
-                                         (uint32_t)(wave * kTok * 256));
-      constexpr int kLanes = kSwiglu ? 4 : 8;   // lanes of a token's features
-      const int rr = lane_e / kLanes, rc = lane_e % kLanes;
-      constexpr int kStep = 64 / kLanes;        // tokens at a time
       const int64_t t_w = cur.t0 + 32 * NB * wm;   // the wave's first token
       const int t_left = cur.rows_t - 32 * NB * wm;
+      if constexpr (kEarly) {
+        // A lane has 4 consecutive features of token li in each quarter q of a
+        // fragment: scales and SwiGLU are applied there (gate fragment 2 f, up 2 f + 1),
+        // and 16 tokens at a time go as bf16 through 2 KB per wave, 16-byte chunk c of
+        // row r at c ^ (r % 8): writes and reads hit distinct banks.
+        stored = cur.rows_t == BM && cur.rows_n == kOut;   // every store instruction is issued
+        lds_u8* stg = (lds_u8*)(uintptr_t)(lds_offset(s_out) + (uint32_t)(wave * kStage));
+        // 16 sums of a fragment (rows `row` .. of the tile) times their scales
+        auto scaled = [&](const v16i& c, int row, float xs, float (&z)[16]) __attribute__((always_inline)) {
 #pragma unroll
-      for (int h = 0; h < NA / 2; ++h) {
-        const int row = 32 * NA * wn + 64 * h;        // first weight row of the 64 in the tile
-        const int f = (kSwiglu ? row / 2 : row) + 8 * rc;   // the lane's first feature in the tile
-        const int cnt = cur.rows_n - f;
-        const uint32_t lane_el = (uint32_t)rr * (uint32_t)N + (uint32_t)(8 * rc);
-        __builtin_amdgcn_sched_barrier(0);
-        // the lane's tokens are rr + kStep i
-        auto el_of = [&](int i) __attribute__((always_inline)) -> int64_t {
-          return (t_w + kStep * i) * N + cur.n0 + (kSwiglu ? row / 2 : row);
+          for (int q = 0; q < 4; ++q) {
+            const float4 w = *reinterpret_cast<const float4*>(s_ws + opaque(row + 4 * lg) + 8 * q);
+            z[4 * q] = (float)c[4 * q] * xs * w.x;
+            z[4 * q + 1] = (float)c[4 * q + 1] * xs * w.y;
+            z[4 * q + 2] = (float)c[4 * q + 2] * xs * w.z;
+            z[4 * q + 3] = (float)c[4 * q + 3] * xs * w.w;
+          }
         };
-        uint4 res[8];   // (not kGrouped)
+        constexpr int kF = NA / 2;             // fragments of outputs
+        constexpr int kLanes = 4 * kF;         // of a token's row
+        constexpr int kStep = 64 / kLanes;     // tokens an instruction stores
+        const int rr = lane_e / kLanes, rc = lane_e % kLanes;
+        const int f0 = 32 * kF * wn, cnt = cur.rows_n - f0 - 8 * rc;   // the wave's first feature in the tile
+        const uint32_t lane_el = (uint32_t)rr * (uint32_t)N + (uint32_t)(8 * rc);
 #pragma unroll
         for (int fm = 0; fm < NB; ++fm) {
+          __builtin_amdgcn_sched_barrier(0);
+          const float xs = s_xs[32 * NB * wm + 32 * fm + li];
+          uint32_t o[kF][8];
 #pragma unroll
-          for (int ff = 0; ff < 2; ++ff)
+          for (int f = 0; f < kF; ++f) {
+            float z[16], u[16];
+            scaled(acc[2 * f][fm], 32 * NA * wn + 64 * f, xs, z);
+            scaled(acc[2 * f + 1][fm], 32 * NA * wn + 64 * f + 32, xs, u);
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              const v16i& c = acc[2 * h + ff][fm];
-              const i32x4 o = {c[4 * q], c[4 * q + 1], c[4 * q + 2], c[4 * q + 3]};
-              *reinterpret_cast<lds_i32x4*>(stg + li * 256 + (((8 * ff + 2 * q + lg) ^ (li & 15)) << 4)) = o;
+            for (int v = 0; v < 16; ++v) z[v] = silu_mul(z[v], u[v]);
+#pragma unroll
+            for (int v = 0; v < 8; ++v) o[f][v] = bf16x2(z[2 * v], z[2 * v + 1]);
+          }
+#pragma unroll
+          for (int pass = 0; pass < 2; ++pass) {
+            if ((li >> 4) == pass) {
+#pragma unroll
+              for (int f = 0; f < kF; ++f)
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                  *reinterpret_cast<lds_u32x2*>(stg + (li & 15) * 128 + (((4 * f + q) ^ (li & 7)) << 4) + 8 * lg) =
+                      u32x2{o[f][2 * q], o[f][2 * q + 1]};
             }
-          asm volatile("" ::: "memory");   // a wave's LDS accesses execute in issue order
-          if constexpr (!kGrouped) {
-            if (fm == 0) {
-              // after the first accumulators left their registers
-              __builtin_amdgcn_sched_barrier(0);
+            asm volatile("" ::: "memory");   // a wave's LDS accesses execute in issue order
 #pragma unroll
-              for (int i = 0; i < 8; ++i) res[i] = make_uint4(0, 0, 0, 0);
-              if (p.e.res && cnt > 0) {
-                if (p.e.stream_res) {
+            for (int it = 0; it < 16 / kStep; ++it) {
+              const int r = kStep * it + rr, tok = 32 * fm + 16 * pass + kStep * it;
+              const u32x4 v = *reinterpret_cast<const lds_u32x4*>(stg + r * 128 + ((rc ^ (r & 7)) << 4));
+              store8_bits(p.e.y, (t_w + tok) * N + cur.n0 + f0, lane_el, tok + rr < t_left ? cnt : 0,
+                          u32x4_any{v.x, v.y, v.z, v.w});
+            }
+            asm volatile("" ::: "memory");
+          }
+        }
+      } else {
+        // Through the slot of the last stage, which is free until the barrier below: 32
+        // tokens x 64 features at a time as int32 rows of 256 bytes, 16-byte chunk c of
+        // row r at c ^ (r % 16).  Read back, a lane holds 8 consecutive features of a
+        // token, where the residual is added before the rounding.
+        constexpr int kTok = 32;
+        static_assert(kWaves * kTok * 256 <= kSlot, "staging fits the slot");
+        lds_u8* stg = (lds_u8*)(uintptr_t)(ring0 + (uint32_t)((g - 1) & 1) * (uint32_t)kSlot +
+                                           (uint32_t)(wave * kTok * 256));
+        const int rr = lane_e >> 3, rc = lane_e & 7;
 #pragma unroll
-                  for (int i = 0; i < 8; ++i)
-                    if (rr + 8 * i < t_left) res[i] = load_res8<true>(at(p.e.res, el_of(i), lane_el), cnt);
-                } else {
+        for (int h = 0; h < NA / 2; ++h) {
+          const int row = 32 * NA * wn + 64 * h;        // first weight row of the 64 in the tile
+          const int cnt = cur.rows_n - row - 8 * rc;
+          const uint32_t lane_el = (uint32_t)rr * (uint32_t)N + (uint32_t)(8 * rc);
+          __builtin_amdgcn_sched_barrier(0);
+          // the lane's tokens are rr + 8 i
+          auto el_of = [&](int i) __attribute__((always_inline)) -> int64_t {
+            return (t_w + 8 * i) * N + cur.n0 + row;
+          };
+          uint4 res[8];
 #pragma unroll
-                  for (int i = 0; i < 8; ++i)
-                    if (rr + 8 * i < t_left) res[i] = load_res8<false>(at(p.e.res, el_of(i), lane_el), cnt);
+          for (int fm = 0; fm < NB; ++fm) {
+#pragma unroll
+            for (int ff = 0; ff < 2; ++ff)
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
+                const v16i& c = acc[2 * h + ff][fm];
+                const i32x4 o = {c[4 * q], c[4 * q + 1], c[4 * q + 2], c[4 * q + 3]};
+                *reinterpret_cast<lds_i32x4*>(stg + li * 256 + (((8 * ff + 2 * q + lg) ^ (li & 15)) << 4)) = o;
+              }
+            asm volatile("" ::: "memory");   // a wave's LDS accesses execute in issue order
+            if constexpr (!kGrouped) {
+              if (fm == 0) {
+                // after the first accumulators left their registers
+                __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) res[i] = make_uint4(0, 0, 0, 0);
+                if (p.e.res && cnt > 0) {
+                  if (p.e.stream_res) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                      if (rr + 8 * i < t_left) res[i] = load_res8<true>(at(p.e.res, el_of(i), lane_el), cnt);
+                  } else {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                      if (rr + 8 * i < t_left) res[i] = load_res8<false>(at(p.e.res, el_of(i), lane_el), cnt);
+                  }
                 }
               }
             }
-          }
-          auto get8 = [&](const float* src, float (&v)[8]) __attribute__((always_inline)) {
-            const float4 a = reinterpret_cast<const float4*>(src)[0], c = reinterpret_cast<const float4*>(src)[1];
-            v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-            v[4] = c.x; v[5] = c.y; v[6] = c.z; v[7] = c.w;
-          };
+            auto get8 = [&](const float* src, float (&v)[8]) __attribute__((always_inline)) {
+              const float4 a = reinterpret_cast<const float4*>(src)[0], c = reinterpret_cast<const float4*>(src)[1];
+              v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+              v[4] = c.x; v[5] = c.y; v[6] = c.z; v[7] = c.w;
+            };
 #pragma unroll
-          for (int it = 0; it < kTok / kStep; ++it) {
-            const int r = kStep * it + rr, i = kTok / kStep * fm + it;
-            const float xs = s_xs[32 * NB * wm + 32 * fm + r];
-            // (read again for every token: held, they would spill)
-            float b[8] = {}, sg[8], su[8];
-            const int at_row = opaque(row + 8 * rc);
-            get8(s_ws + at_row, sg);
-            if constexpr (kSwiglu) get8(s_ws + at_row + 32, su);
-            if constexpr (!kGrouped) get8(s_bias + at_row, b);
-            auto read8 = [&](int chunk, const float (&ws)[8], float (&z)[8]) __attribute__((always_inline)) {
-              const i32x4 z0 = *reinterpret_cast<const lds_i32x4*>(stg + r * 256 + ((chunk ^ (r & 15)) << 4));
-              const i32x4 z1 = *reinterpret_cast<const lds_i32x4*>(stg + r * 256 + (((chunk + 1) ^ (r & 15)) << 4));
+            for (int it = 0; it < kTok / 8; ++it) {
+              const int r = 8 * it + rr, i = kTok / 8 * fm + it;
+              const float xs = s_xs[32 * NB * wm + 32 * fm + r];
+              // (read again for every token: held, they would spill)
+              float b[8] = {}, ws[8], z[8];
+              const int at_row = opaque(row + 8 * rc);
+              get8(s_ws + at_row, ws);
+              if constexpr (!kGrouped) get8(s_bias + at_row, b);
+              const i32x4 z0 = *reinterpret_cast<const lds_i32x4*>(stg + r * 256 + (((2 * rc) ^ (r & 15)) << 4));
+              const i32x4 z1 = *reinterpret_cast<const lds_i32x4*>(stg + r * 256 + (((2 * rc + 1) ^ (r & 15)) << 4));
 #pragma unroll
               for (int v = 0; v < 4; ++v) {
                 z[v] = (float)z0[v] * xs * ws[v];
                 z[4 + v] = (float)z1[v] * xs * ws[4 + v];
               }
-            };
-            float z[8];
-            read8(2 * rc, sg, z);
-            if constexpr (kSwiglu) {
-              float u[8];
-              read8(8 + 2 * rc, su, u);
-#pragma unroll
-              for (int v = 0; v < 8; ++v) z[v] = silu_mul(z[v], u[v]);
+              const int have = rr + 8 * i < t_left ? cnt : 0;
+              if constexpr (kGrouped) store8(p.e.y, el_of(i), lane_el, have, z);
+              else finish8(p.e, el_of(i), lane_el, have, b, res[i], z);
+              __builtin_amdgcn_sched_barrier(0);   // one row at a time
             }
-            const int have = rr + kStep * i < t_left ? cnt : 0;
-            if constexpr (kGrouped) store8(p.e.y, el_of(i), lane_el, have, z);
-            else finish8(p.e, el_of(i), lane_el, have, b, res[i], z);
-            __builtin_amdgcn_sched_barrier(0);   // one row at a time
+            asm volatile("" ::: "memory");
           }
-          asm volatile("" ::: "memory");
         }
       }
     }
-    // the staging slot is done with: the loads that the last stage left out
-    drain_barrier();
-    if (nk > 1) {
-      if (has_next) load_stage(nsrc, 1, g + 1);
-    } else if (cj + 2 < my_tiles) {
-      load_stage(src_of(tile_at(cj + 2)), 0, g + 1);
+    if constexpr (kEarly) {
+      // (the next tile's scales are written behind its first stage's barrier, if there is one)
+      if (nk == 1) drain_barrier();
+    } else {
+      // the staging slot is done with: the loads that the last stage left out
+      drain_barrier();
+      if (has_next) load_stage(nsrc, nk > 1 ? 1 : 0, g + 1);
     }
   }
   wait_loads<0>();   // nothing may land in LDS that is no longer ours
