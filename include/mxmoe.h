@@ -555,7 +555,8 @@ size_t int8_linear_workspace_size(int64_t T, int64_t K, int64_t N, int x_is_int8
  * the sum exact (int32), everything after it in fp32.  Codes may be any int8,
  * -128 among them; scales any finite fp32.
  *   x         int8 [T, K] with x_s fp32 [T], or with a NULL x_s bf16 [T, K],
- *             quantised first (as int8_quantize)
+ *             quantised first (as int8_quantize; up to 16 tokens of up to 65536
+ *             elements together need no workspace for it while N <= 8192)
  *   w, w_s    int8 [N, K], fp32 [N]
  *   bias      [N] bf16 or fp32 (bias_type), or NULL
  *   residual  bf16 [T, N] or NULL;  y bf16 [T, N]
@@ -589,6 +590,26 @@ int gmm_int8(const void* a_i8, const float* a_s, const void* w_i8,
              const float* w_s, const int64_t* group_list, int group_list_type,
              int swiglu, int64_t M, int64_t N, int64_t K, int64_t E,
              void* y_bf16, void* stream);
+
+/* The kernels of int8_linear and gmm_int8, by their tiles (weight rows x rows of
+ * x). */
+typedef enum mx_int8_kernel {
+  MX_INT8_32X16 = 0,
+  MX_INT8_32X16_WIDE = 1, /* K over 8 waves, one workgroup per CU */
+  MX_INT8_32X32 = 2,
+  MX_INT8_64X64 = 3,
+  MX_INT8_128X128 = 4,
+  MX_INT8_256X256 = 5,
+  MX_INT8_32X16_BF16 = 6  /* bf16 tokens quantised by each workgroup */
+} mx_int8_kernel;
+
+/*
+ * Which of them a size takes on the current device (256 CUs are assumed where
+ * there is none), or a negative mx_status for sizes that are refused and for no
+ * rows.  For profiles and tests; enqueues nothing.
+ */
+int int8_linear_kernel(int64_t T, int64_t K, int64_t N, int x_is_int8);
+int gmm_int8_kernel(int64_t M, int64_t N, int64_t K, int64_t E, int swiglu);
 
 /*
  * Token rows of any type sorted by expert: moe_route_quant without the

@@ -26,7 +26,7 @@ __all__ = [
     "linear_workspace_size", "mx_quantize_fp4", "moe_route_quant_noalloc", "mx_pack_weights", "route_set_wait_limit",
     "gmm_swiglu_mxquant_packed", "gmm_mx_packed", "moe_mxfp8_forward_packed", "gmm_mx_w4a8", "gmm_swiglu_mxquant_w4a8", "moe_w4a8_forward",
     "mx_linear_fused", "linear_fused_workspace_size", "linear_fused_kernel", "mx_add_rmsnorm", "moe_route_mx", "moe_mxfp8_forward_mx",
-    "int8_quantize", "int8_linear", "int8_linear_workspace_size", "gmm_int8", "moe_permute", "moe_unpermute",
+    "int8_quantize", "int8_linear", "int8_linear_workspace_size", "int8_linear_kernel", "gmm_int8", "gmm_int8_kernel", "moe_permute", "moe_unpermute",
     "moe_unpermute_backward",
 ]
 
@@ -90,6 +90,8 @@ def load():
         "int8_quantize": (I32, [P, I64, I64, I64, P, P, P]),
         "int8_linear_workspace_size": (SZ, [I64, I64, I64, I32]),
         "int8_linear": (I32, [P, P, P, P, P, I32, I32, P, I64, I64, I64, P, P, SZ, P]),
+        "int8_linear_kernel": (I32, [I64, I64, I64, I32]),
+        "gmm_int8_kernel": (I32, [I64, I64, I64, I64, I32]),
         "gmm_int8": (I32, [P, P, P, P, P, I32, I32, I64, I64, I64, I64, P, P]),
         "moe_permute": (I32, [P, I64, I64, P, P, I64, I64, I64, I64, P, P, P, P, P, P, SZ, P]),
         "moe_unpermute": (I32, [P, I32, P, P, I64, I64, I64, I64, P, P]),
@@ -926,6 +928,26 @@ def int8_quantize(x, out=None, stream=None):
 
 def int8_linear_workspace_size(T, K, N, x_is_int8):
     return int(load().int8_linear_workspace_size(T, K, N, int(x_is_int8)))
+
+
+INT8_KERNELS = ("32x16", "32x16 wide", "32x32", "64x64", "128x128", "256x256", "32x16 bf16")
+
+
+def int8_linear_kernel(T, K, N, x_is_int8):
+    """Which of INT8_KERNELS (named by their tiles, weight rows x rows of x)
+    int8_linear takes for a size on the current device."""
+    index = load().int8_linear_kernel(T, K, N, int(x_is_int8))
+    if index < 0:
+        _check(index, "int8_linear_kernel")
+    return INT8_KERNELS[index]
+
+
+def gmm_int8_kernel(M, N, K, E, swiglu=False):
+    """Which of INT8_KERNELS gmm_int8 takes for a size on the current device."""
+    index = load().gmm_int8_kernel(M, N, K, E, int(swiglu))
+    if index < 0:
+        _check(index, "gmm_int8_kernel")
+    return INT8_KERNELS[index]
 
 
 def int8_linear(x, w, w_s, x_s=None, bias=None, act="none", residual=None, out=None, workspace=None, stream=None):

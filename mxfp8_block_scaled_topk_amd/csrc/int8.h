@@ -23,6 +23,7 @@ struct Int8Params {
   int64_t rows;          // weight rows per expert (2 N with swiglu)
   int present;           // 16-byte chunks of a row in its last 128-element stage
   int swiglu;
+  int cached;            // outputs through the caches (see store8_bits)
 };
 
 // Stages are 128 bytes of each row; chunk c (16 bytes) of LDS row r lies at chunk
@@ -100,22 +101,34 @@ __device__ __forceinline__ int expert_of(const int* tile0, int E, int t) {
 }
 
 // 8 consecutive features of a token, the first cnt of which exist, to element el +
-// lane_el of y: as bf16, or rounded here.
-__device__ __forceinline__ void store8_bits(uint16_t* y, int64_t el, uint32_t lane_el, int cnt, const u32x4_any& o) {
+// lane_el of y: as bf16, or rounded here.  They are written once: past the caches,
+// which hold the operands of the tiles to come, but for gmm_int8's rows that do not
+// lie on 64 bytes, where the parts of a line that neighbouring tiles write meet in
+// the L2 (8 experts, 44922 rows, K = 640: N = 704 43 / 44 us past / through the
+// caches, N = 706 72 / 51; 64 experts, 32768 rows, K = 1024, N = 4104: 257 / 235).
+// int8_linear's and SwiGLU's tiles gain nothing by that (T = 8192, K = 1024: N = 3080
+// 62 / 58, N = 4104 66 / 78).
+__device__ __forceinline__ void store8_bits(uint16_t* y, int64_t el, uint32_t lane_el, int cnt, const u32x4_any& o,
+                                            bool cached = false) {
   if (cnt <= 0) return;
   y = at(y, el, lane_el);
   if (cnt >= 8) {
-    // written once: past the caches, which hold the operands of the tiles to come
-    __builtin_nontemporal_store(o, reinterpret_cast<u32x4_any*>(y));
+    if (cached) {
+      asm volatile("" ::: "memory");   // keeps the two stores apart: merged, the hint is lost
+      *reinterpret_cast<u32x4_any*>(y) = o;
+    } else {
+      __builtin_nontemporal_store(o, reinterpret_cast<u32x4_any*>(y));
+    }
   } else {
 #pragma unroll
     for (int i = 0; i < 7; ++i)
       if (i < cnt) y[i] = static_cast<uint16_t>(o[i >> 1] >> (16 * (i & 1)));
   }
 }
-__device__ __forceinline__ void store8(uint16_t* y, int64_t el, uint32_t lane_el, int cnt, const float (&z)[8]) {
+__device__ __forceinline__ void store8(uint16_t* y, int64_t el, uint32_t lane_el, int cnt, const float (&z)[8],
+                                       bool cached = false) {
   store8_bits(y, el, lane_el, cnt,
-              u32x4_any{bf16x2(z[0], z[1]), bf16x2(z[2], z[3]), bf16x2(z[4], z[5]), bf16x2(z[6], z[7])});
+              u32x4_any{bf16x2(z[0], z[1]), bf16x2(z[2], z[3]), bf16x2(z[4], z[5]), bf16x2(z[6], z[7])}, cached);
 }
 // The linear's epilogue: bias, activation, residual (load_res8's), then store8.
 __device__ __forceinline__ void finish8(const LinParams& p, int64_t el, uint32_t lane_el, int cnt, const float (&b)[8],

@@ -5,6 +5,7 @@
 //
 // the sum exact in int32 (K < 2^17).
 #include <algorithm>
+#include <cmath>
 
 #include "int8.h"
 
@@ -26,7 +27,7 @@ namespace {
 
 constexpr int64_t kMaxK = ((int64_t)1 << 17) - 16;
 
-// The kernels by their tiles (weight rows x rows of x), the waves that share a
+// The kernels, by their tiles (weight rows x rows of x), the waves that share a
 // tile's K, and the workgroups of a CU.
 struct Kernel {
   int64_t bn, bm, waves, per_cu;
@@ -34,37 +35,51 @@ struct Kernel {
   int64_t g_first, g_round, g_stage;   // of gmm_int8
   int (*launch)(const Int8Params&, hipStream_t, const char*);
 };
-const Kernel kKernels[] = {
-    {32, 16, 4, 2, 226, 99, 50, 507, 47, 73, launch_int8_32x16},
-    {32, 16, 8, 1, 257, 84, 56, 568, 15, 84, launch_int8_32x16_wide},
-    {32, 32, 4, 2, 210, 129, 61, 522, 40, 89, launch_int8_32x32},
-    {64, 64, 2, 2, 155, 335, 88, 521, 115, 95, launch_int8_64x64},
-    {128, 128, 1, 2, 0, 597, 81, 467, 224, 90, launch_int8_tile128},
-    {256, 256, 1, 1, 0, 924, 157, 647, 119, 134, launch_int8_tile256},
+const Kernel kKernels[] = {   // in mx_int8_kernel's order
+    {32, 16, 4, 2, 226, 99, 50, 481, 65, 78, launch_int8_32x16},
+    {32, 16, 8, 1, 257, 84, 56, 528, 23, 99, launch_int8_32x16_wide},
+    {32, 32, 4, 2, 210, 129, 61, 479, 79, 87, launch_int8_32x32},
+    {64, 64, 2, 2, 155, 335, 88, 393, 217, 99, launch_int8_64x64},
+    {128, 128, 1, 2, 0, 597, 81, 233, 475, 89, launch_int8_tile128},
+    {256, 256, 1, 1, 0, 924, 157, 349, 478, 125, launch_int8_tile256},
 };
 
 // Which kernel: the one whose time a line through its measured times says is
 // shortest.  Its tiles go over the CUs in rounds; a round costs a part per tile and
 // a part per k stage of a wave.  gmm_int8's rows lie with the experts as the device's
-// group list says: the host counts a tile for every expert (or row, if these are
-// fewer) and half a tile for what is left over behind whole ones.
-int launch_int8(Int8Params& p, hipStream_t stream, const char* name) {
-  p.e.nk = (int)((p.e.K + kStageK - 1) / kStageK);
-  p.present = (int)((p.e.K - (int64_t)(p.e.nk - 1) * kStageK) / 16);
-  const int64_t cus = num_cus(), M = p.e.T;
+// group list says: the host counts a tile for every expert that gets a row when all
+// are as likely, and a tile for every bm rows past half a tile per expert.  Fitted
+// to all kernels on 260 shapes each (up to 16384 tokens to 8 of 128 experts, K and N
+// to 8192, drawn over their logarithms): the choice takes 0.4 % longer than the fastest
+// on average (11 % at worst), gmm_int8's 2 % (49 %: few tiles, or experts' rows that
+// fall to one side of a tile's height).  (Also measured: 16 x 16 over 8 waves, 64 x 16,
+// 64 x 32, 32 x 64 and 64 x 96, which win by 0.7 % on average together.)
+int choose(int64_t M, int64_t K, int64_t rows, int64_t E, bool grouped) {
+  const int64_t cus = num_cus(), nk = (K + kStageK - 1) / kStageK;
   auto up = [](int64_t n, int64_t d) { return (n + d - 1) / d; };
-  const Kernel* best = nullptr;
+  const double used = grouped ? (double)E * -std::expm1((double)M * std::log1p(-1.0 / (double)std::max<int64_t>(E, 2))) : 0;
+  int best = 0;
   int64_t best_us = 0;
-  for (const Kernel& k : kKernels) {
-    const int64_t m_tiles = p.gl ? std::min<int64_t>(M, p.E) + std::max<int64_t>(0, M - p.E * k.bm / 2) / k.bm : up(M, k.bm);
-    const int64_t rounds = up(m_tiles * up(p.rows, k.bn), cus * k.per_cu), stages = up(p.e.nk, k.waves);
-    const int64_t us = p.gl ? k.g_first + rounds * (k.g_round + stages * k.g_stage) : k.first + rounds * (k.round + stages * k.stage);
-    if (!best || us < best_us) {
-      best = &k;
+  for (int i = 0; i < (int)(sizeof(kKernels) / sizeof(kKernels[0])); ++i) {
+    const Kernel& k = kKernels[i];
+    const double more = (double)std::max<int64_t>(0, M - E * k.bm / 2) / (double)k.bm;
+    const int64_t m_tiles = !grouped ? up(M, k.bm) : E == 1 ? up(M, k.bm) : (int64_t)std::ceil(used + more);
+    const int64_t rounds = up(m_tiles * up(rows, k.bn), cus * k.per_cu), stages = up(nk, k.waves);
+    const int64_t us = grouped ? k.g_first + rounds * (k.g_round + stages * k.g_stage)
+                               : k.first + rounds * (k.round + stages * k.stage);
+    if (i == 0 || us < best_us) {
+      best = i;
       best_us = us;
     }
   }
-  return best->launch(p, stream, name);
+  return best;
+}
+
+int launch_int8(Int8Params& p, hipStream_t stream, const char* name) {
+  p.e.nk = (int)((p.e.K + kStageK - 1) / kStageK);
+  p.present = (int)((p.e.K - (int64_t)(p.e.nk - 1) * kStageK) / 16);
+  p.cached = p.gl && !p.swiglu && p.e.N % 32 != 0;
+  return kKernels[choose(p.e.T, p.e.K, p.rows, p.E, p.gl != nullptr)].launch(p, stream, name);
 }
 
 // Tile indices are 32-bit in every kernel, also a round past the last: of tiles of
@@ -80,6 +95,17 @@ int check_sizes(const char* name, int64_t T, int64_t K, int64_t N) {
   if (K % 16 != 0) return fail(MX_ERR_UNSUPPORTED, "%s: K=%lld is not a multiple of 16", name, (long long)K);
   if (K > kMaxK) return fail(MX_ERR_UNSUPPORTED, "%s: K=%lld >= 2^17", name, (long long)K);
   if (too_many_tiles(T, N)) return fail(MX_ERR_UNSUPPORTED, "%s: 2^28 or more tiles of 32 x 32 outputs", name);
+  return MX_OK;
+}
+
+int check_experts(int64_t M, int64_t K, int64_t N, int64_t E) {
+  const int rc = check_sizes("gmm_int8", M, K, N);
+  if (rc) return rc;
+  if (E <= 0) return fail(MX_ERR_INVALID_ARG, "gmm_int8: bad E=%lld", (long long)E);
+  if (E > kInt8MaxE) return fail(MX_ERR_UNSUPPORTED, "gmm_int8: E=%lld > %d", (long long)E, kInt8MaxE);
+  // (an expert's last tile may be partly empty: E more rows of tiles)
+  if (too_many_tiles(M + 32 * E, N))
+    return fail(MX_ERR_UNSUPPORTED, "gmm_int8: 2^28 or more tiles of 32 x 32 outputs");
   return MX_OK;
 }
 
@@ -101,6 +127,22 @@ extern "C" size_t int8_linear_workspace_size(int64_t T, int64_t K, int64_t N, in
   // 0 for sizes int8_linear rejects
   if (mxmoe::check_sizes("int8_linear", T, K, N) != MX_OK) return 0;
   return mxmoe::int8_layout(T, K, N, x_is_int8).total;
+}
+
+extern "C" int int8_linear_kernel(int64_t T, int64_t K, int64_t N, int x_is_int8) {
+  using namespace mxmoe;
+  const int rc = check_sizes("int8_linear", T, K, N);
+  if (rc) return rc;
+  if (T == 0) return fail(MX_ERR_INVALID_ARG, "int8_linear_kernel: no tokens");
+  return !x_is_int8 && int8_resident(T, K, N) ? MX_INT8_32X16_BF16 : choose(T, K, N, 0, false);
+}
+
+extern "C" int gmm_int8_kernel(int64_t M, int64_t N, int64_t K, int64_t E, int swiglu) {
+  using namespace mxmoe;
+  const int rc = check_experts(M, K, N, E);
+  if (rc) return rc;
+  if (M == 0) return fail(MX_ERR_INVALID_ARG, "gmm_int8_kernel: no rows");
+  return choose(M, K, swiglu ? 2 * N : N, E, true);
 }
 
 extern "C" int int8_linear(const void* x, const float* x_s, const void* w_i8, const float* w_s, const void* bias,
@@ -178,13 +220,8 @@ extern "C" int gmm_int8(const void* a_i8, const float* a_s, const void* w_i8, co
                         const int64_t* group_list, int group_list_type, int swiglu, int64_t M, int64_t N, int64_t K,
                         int64_t E, void* y_bf16, void* stream) {
   using namespace mxmoe;
-  int rc = check_sizes("gmm_int8", M, K, N);
+  int rc = check_experts(M, K, N, E);
   if (rc) return rc;
-  if (E <= 0) return fail(MX_ERR_INVALID_ARG, "gmm_int8: bad E=%lld", (long long)E);
-  if (E > kInt8MaxE) return fail(MX_ERR_UNSUPPORTED, "gmm_int8: E=%lld > %d", (long long)E, kInt8MaxE);
-  // (an expert's last tile may be partly empty: E more rows of tiles)
-  if (too_many_tiles(M + 32 * E, N))
-    return fail(MX_ERR_UNSUPPORTED, "gmm_int8: 2^28 or more tiles of 32 x 32 outputs");
   if (group_list_type != 0 && group_list_type != 1)
     return fail(MX_ERR_INVALID_ARG, "gmm_int8: group_list_type must be 0 (cumulative) or 1 (count), got %d",
                 group_list_type);

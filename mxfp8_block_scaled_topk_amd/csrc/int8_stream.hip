@@ -317,7 +317,7 @@ __global__ __launch_bounds__(64 * WV) void int8_stream_kernel(Int8Params p, uint
 #pragma unroll
         for (int i = 0; i < 8; ++i) z[i] = silu_mul(z[i], up[i]);
       }
-      if constexpr (kGrouped) store8(p.e.y, t * N + n, 0, cnt8, z);
+      if constexpr (kGrouped) store8(p.e.y, t * N + n, 0, cnt8, z, p.cached);
       else finish8(p.e, t * N + n, 0, cnt8, b, res, z);
     }
   }

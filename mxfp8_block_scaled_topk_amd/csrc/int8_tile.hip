@@ -458,7 +458,7 @@ __global__ __launch_bounds__(64 * WN * WM) void int8_tile_kernel(Int8Params p, i
                 z[4 + v] = (float)z1[v] * xs * ws[4 + v];
               }
               const int have = rr + 8 * i < t_left ? cnt : 0;
-              if constexpr (kGrouped) store8(p.e.y, el_of(i), lane_el, have, z);
+              if constexpr (kGrouped) store8(p.e.y, el_of(i), lane_el, have, z, p.cached);
               else finish8(p.e, el_of(i), lane_el, have, b, res[i], z);
               __builtin_amdgcn_sched_barrier(0);   // one row at a time
             }
