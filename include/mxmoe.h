@@ -597,10 +597,11 @@ typedef enum mx_int8_kernel {
   MX_INT8_32X16 = 0,
   MX_INT8_32X16_WIDE = 1, /* K over 8 waves, one workgroup per CU */
   MX_INT8_32X32 = 2,
-  MX_INT8_64X64 = 3,
-  MX_INT8_128X128 = 4,
-  MX_INT8_256X256 = 5,
-  MX_INT8_32X16_BF16 = 6  /* bf16 tokens quantised by each workgroup */
+  MX_INT8_48X48 = 3,      /* int8_linear only */
+  MX_INT8_64X64 = 4,
+  MX_INT8_128X128 = 5,
+  MX_INT8_256X256 = 6,
+  MX_INT8_32X16_BF16 = 7  /* bf16 tokens quantised by each workgroup */
 } mx_int8_kernel;
 
 /*

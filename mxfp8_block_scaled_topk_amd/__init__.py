@@ -930,7 +930,7 @@ def int8_linear_workspace_size(T, K, N, x_is_int8):
     return int(load().int8_linear_workspace_size(T, K, N, int(x_is_int8)))
 
 
-INT8_KERNELS = ("32x16", "32x16 wide", "32x32", "64x64", "128x128", "256x256", "32x16 bf16")
+INT8_KERNELS = ("32x16", "32x16 wide", "32x32", "48x48", "64x64", "128x128", "256x256", "32x16 bf16")
 
 
 def int8_linear_kernel(T, K, N, x_is_int8):

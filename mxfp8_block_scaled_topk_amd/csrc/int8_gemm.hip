@@ -17,6 +17,7 @@ int launch_int8_quantize(const uint16_t* x, int64_t rows, int64_t kd, int64_t ld
 int launch_int8_32x16(const Int8Params& p, hipStream_t stream, const char* name);
 int launch_int8_32x16_wide(const Int8Params& p, hipStream_t stream, const char* name);
 int launch_int8_32x32(const Int8Params& p, hipStream_t stream, const char* name);
+int launch_int8_48x48(const Int8Params& p, hipStream_t stream, const char* name);
 int launch_int8_64x64(const Int8Params& p, hipStream_t stream, const char* name);
 int launch_int8_tile128(const Int8Params& p, hipStream_t stream, const char* name);
 int launch_int8_tile256(const Int8Params& p, hipStream_t stream, const char* name);
@@ -32,16 +33,17 @@ constexpr int64_t kMaxK = ((int64_t)1 << 17) - 16;
 struct Kernel {
   int64_t bn, bm, waves, per_cu;
   int64_t first, round, stage;         // time in 0.01 us: first + rounds (round + stages of a wave * stage)
-  int64_t g_first, g_round, g_stage;   // of gmm_int8
+  int64_t g_first, g_round, g_stage;   // of gmm_int8, which does without 48 x 48 (g_stage = 0)
   int (*launch)(const Int8Params&, hipStream_t, const char*);
 };
 const Kernel kKernels[] = {   // in mx_int8_kernel's order
-    {32, 16, 4, 2, 226, 99, 50, 481, 65, 78, launch_int8_32x16},
-    {32, 16, 8, 1, 257, 84, 56, 528, 23, 99, launch_int8_32x16_wide},
-    {32, 32, 4, 2, 210, 129, 61, 479, 79, 87, launch_int8_32x32},
-    {64, 64, 2, 2, 155, 335, 88, 393, 217, 99, launch_int8_64x64},
-    {128, 128, 1, 2, 0, 597, 81, 233, 475, 89, launch_int8_tile128},
-    {256, 256, 1, 1, 0, 924, 157, 349, 478, 125, launch_int8_tile256},
+    {32, 16, 4, 2, 223, 102, 51, 487, 77, 68, launch_int8_32x16},
+    {32, 16, 8, 1, 251, 82, 60, 520, 51, 77, launch_int8_32x16_wide},
+    {32, 32, 4, 2, 214, 129, 61, 483, 91, 77, launch_int8_32x32},
+    {48, 48, 3, 2, 205, 230, 76, 0, 0, 0, launch_int8_48x48},
+    {64, 64, 2, 2, 152, 332, 92, 415, 211, 96, launch_int8_64x64},
+    {128, 128, 1, 2, 32, 570, 95, 333, 405, 89, launch_int8_tile128},
+    {256, 256, 1, 1, 236, 915, 147, 495, 341, 133, launch_int8_tile256},
 };
 
 // Which kernel: the one whose time a line through its measured times says is
@@ -49,11 +51,13 @@ const Kernel kKernels[] = {   // in mx_int8_kernel's order
 // a part per k stage of a wave.  gmm_int8's rows lie with the experts as the device's
 // group list says: the host counts a tile for every expert that gets a row when all
 // are as likely, and a tile for every bm rows past half a tile per expert.  Fitted
-// to all kernels on 260 shapes each (up to 16384 tokens to 8 of 128 experts, K and N
-// to 8192, drawn over their logarithms): the choice takes 0.4 % longer than the fastest
-// on average (11 % at worst), gmm_int8's 2 % (49 %: few tiles, or experts' rows that
+// to all kernels on 400 shapes each (up to 16384 tokens to 8 of 128 experts, K and N
+// to 8192, drawn over their logarithms): the choice takes 0.7 % longer than the fastest
+// on average (30 % at worst), gmm_int8's 2 % (45 %: few tiles, or experts' rows that
 // fall to one side of a tile's height).  (Also measured: 16 x 16 over 8 waves, 64 x 16,
-// 64 x 32, 32 x 64 and 64 x 96, which win by 0.7 % on average together.)
+// 64 x 32, 32 x 64, 64 x 96, 80 x 32 to 80 x 64 and 64 x 64 over 4 waves, which win by
+// less than 0.5 % on average together; without 48 x 48 the linear's choice takes 1.2 %
+// longer: T = 203, K = 2096, N = 4099 13.1 instead of 11.9 us.)
 int choose(int64_t M, int64_t K, int64_t rows, int64_t E, bool grouped) {
   const int64_t cus = num_cus(), nk = (K + kStageK - 1) / kStageK;
   auto up = [](int64_t n, int64_t d) { return (n + d - 1) / d; };
@@ -62,6 +66,7 @@ int choose(int64_t M, int64_t K, int64_t rows, int64_t E, bool grouped) {
   int64_t best_us = 0;
   for (int i = 0; i < (int)(sizeof(kKernels) / sizeof(kKernels[0])); ++i) {
     const Kernel& k = kKernels[i];
+    if (grouped && k.g_stage == 0) continue;
     const double more = (double)std::max<int64_t>(0, M - E * k.bm / 2) / (double)k.bm;
     const int64_t m_tiles = !grouped ? up(M, k.bm) : E == 1 ? up(M, k.bm) : (int64_t)std::ceil(used + more);
     const int64_t rounds = up(m_tiles * up(rows, k.bn), cus * k.per_cu), stages = up(nk, k.waves);

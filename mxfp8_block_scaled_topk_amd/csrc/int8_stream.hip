@@ -357,6 +357,9 @@ int launch_int8_32x16_wide(const Int8Params& p, hipStream_t stream, const char* 
 int launch_int8_32x32(const Int8Params& p, hipStream_t stream, const char* name) {
   return launch_any<2, 2, 4, 2, true>(p, 2, stream, name);
 }
+int launch_int8_48x48(const Int8Params& p, hipStream_t stream, const char* name) {   // (int8_linear only)
+  return launch_stream<3, 3, 3, 2, false, false, true>(p, 2, stream, name);
+}
 int launch_int8_64x64(const Int8Params& p, hipStream_t stream, const char* name) {
   return launch_any<4, 4, 2, 2, true>(p, 2, stream, name);
 }

@@ -17,10 +17,11 @@ from test_gpu_int8_products import codes, experts_case, i8_dev, linear_case, sca
 pytestmark = pytest.mark.gpu
 
 LINEAR = [   # kernel, T, K, N
-    ("32x16", 5, 112, 20500), ("32x16", 16, 128, 20500), ("32x16", 40, 208, 8200), ("32x16", 100, 256, 4100),
-    ("32x16", 100, 16, 4100), ("32x16 wide", 5, 1040, 4100), ("32x16 wide", 16, 2064, 97), ("32x16 wide", 1, 4096, 8192),
-    ("32x32", 40, 400, 12300), ("32x32", 333, 1040, 2050), ("32x32", 700, 400, 1030), ("32x32", 4300, 400, 97),
-    ("64x64", 333, 112, 4100), ("64x64", 100, 128, 12300), ("64x64", 333, 384, 4100), ("64x64", 333, 80, 2050),
+    ("32x16", 5, 112, 70000), ("32x16", 16, 16, 33000), ("32x16", 16, 400, 33000), ("32x16", 13, 256, 40000),
+    ("32x16 wide", 5, 1040, 4100), ("32x16 wide", 16, 2064, 97), ("32x16 wide", 1, 4096, 8192), ("32x16 wide", 100, 1040, 1030),
+    ("32x32", 30, 400, 70000), ("32x32", 60, 1040, 12300), ("32x32", 30, 256, 33000), ("32x32", 200, 256, 2050),
+    ("48x48", 40, 112, 70000), ("48x48", 40, 400, 70000), ("48x48", 333, 1040, 2050), ("48x48", 40, 16, 70000), ("48x48", 100, 256, 4100),
+    ("64x64", 60, 208, 70000), ("64x64", 60, 1040, 70000), ("64x64", 2900, 112, 515), ("64x64", 2900, 256, 515),
     ("128x128", 1500, 112, 12300), ("128x128", 4300, 128, 4100), ("128x128", 4300, 208, 4100), ("128x128", 1500, 400, 12300),
     ("128x128", 333, 256, 8200), ("256x256", 2900, 112, 4100), ("256x256", 2900, 128, 4100), ("256x256", 2900, 256, 4100),
     ("256x256", 2900, 400, 4100), ("256x256", 8100, 272, 4090), ("256x256", 8192, 128, 4096),
@@ -38,9 +39,9 @@ def test_linear(i):
 EXPERTS = [   # kernel, swiglu, rows per expert, K, N
     ("32x16", 0, [3] * 40, 112, 2050), ("32x16", 0, [17] * 8, 128, 1030), ("32x16", 1, [3, 0, 5, 1] * 10, 256, 1030),
     ("32x16", 1, [1] * 40, 16, 200), ("32x16 wide", 0, [17] * 8, 1040, 515), ("32x16 wide", 1, [1] * 8, 1040, 515),
-    ("32x32", 0, [17] * 40, 400, 1030), ("32x32", 0, [17] * 8, 1040, 4100), ("32x32", 1, [17, 33, 1, 16] * 2, 112, 4100),
-    ("32x32", 1, [130] * 8, 208, 200), ("64x64", 0, [17] * 40, 112, 2050), ("64x64", 0, [17] * 40, 256, 2050),
-    ("64x64", 1, [20, 17, 0, 31] * 10, 128, 1030), ("64x64", 1, [17] * 40, 256, 1024), ("128x128", 0, [60, 61, 0, 119] * 10, 112, 4100),
+    ("32x32", 0, [17] * 40, 400, 1030), ("32x32", 0, [17] * 8, 1040, 4100), ("32x32", 1, [17, 33, 1, 16] * 2, 208, 4100),
+    ("32x32", 1, [130] * 8, 208, 200), ("64x64", 0, [17] * 40, 208, 2050), ("64x64", 0, [17] * 40, 256, 2050),
+    ("64x64", 1, [20, 17, 0, 31] * 10, 256, 1030), ("64x64", 1, [17] * 40, 256, 1024), ("128x128", 0, [60, 61, 0, 119] * 10, 112, 4100),
     ("128x128", 0, [130] * 8, 128, 4096), ("128x128", 0, [60] * 40, 256, 4100), ("128x128", 1, [130] * 8, 112, 4100),
     ("128x128", 1, [128] * 8, 128, 2048), ("128x128", 1, [60] * 40, 256, 1030), ("256x256", 0, [300] * 8, 128, 4100),
     ("256x256", 0, [130] * 40, 112, 2050), ("256x256", 0, [256, 300, 212, 257] * 10, 400, 1024), ("256x256", 1, [300] * 8, 128, 4100),
