@@ -539,7 +539,8 @@ int mx_linear_fused_kernel(int64_t T, int64_t K, int64_t N, int x_is_mx);
  *   s[r] = max(amax[r] * fl(1/127), 2^-126),   amax[r] = max |x[r, :]|
  *   q[r, c] = nearest integer to fl(x[r, c] * fl(1 / s[r])), ties to even
  * with fl and the products rounded to fp32, so that every code is determined;
- * |q| <= 127.  Any kd from 1 to 2^24, any alignment of whole elements (rows of a
+ * |q| <= 127.  A row with a NaN gets the scale NaN, else one with an infinity the
+ * scale infinity, and codes 0 both, so that its products are NaN.  Any kd from 1 to 2^24, any alignment of whole elements (rows of a
  * multiple of 8 elements on 16-byte boundaries, q on 8, are the fastest).
  */
 int int8_quantize(const void* x_bf16, int64_t rows, int64_t kd, int64_t ld,
@@ -553,9 +554,9 @@ size_t int8_linear_workspace_size(int64_t T, int64_t K, int64_t N, int x_is_int8
  *   z[t, n]   = (sum_k xq[t, k] * wq[n, k]) * x_s[t] * w_s[n]
  *   y[t, n]   = bf16_rne( activation(z[t, n] + bias[n]) + residual[t, n] )
  * the sum exact (int32), everything after it in fp32.  Codes may be any int8,
- * -128 among them; scales any finite fp32.
+ * -128 among them; scales any fp32.
  *   x         int8 [T, K] with x_s fp32 [T], or with a NULL x_s bf16 [T, K],
- *             quantised first (as int8_quantize; up to 16 tokens of up to 65536
+ *             quantised first (as int8_quantize; up to 16 tokens of up to 16384
  *             elements together need no workspace for it while N <= 8192)
  *   w, w_s    int8 [N, K], fp32 [N]
  *   bias      [N] bf16 or fp32 (bias_type), or NULL

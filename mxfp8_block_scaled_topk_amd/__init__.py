@@ -897,7 +897,8 @@ _I8, _I32 = torch.int8, torch.int32
 def int8_quantize(x, out=None, stream=None):
     """bf16 rows [..., K] (rows may be strided) to int8 with one fp32 scale per
     row: s = max(amax / 127, 2^-126), q = round(x / s), in the fp32 steps that
-    include/mxmoe.h gives.  The tokens of int8_linear and gmm_int8, or their
+    include/mxmoe.h gives; a row with a NaN or an infinity gets that scale and
+    codes 0.  The tokens of int8_linear and gmm_int8, or their
     weights at load time ([N, K], [E, N, K]: a scale per output channel).
     Returns (q int8 [..., K], s fp32 [...]); ``out`` gives the two instead."""
     if type(x) is not _Tensor or x.dtype is not _BF16:

@@ -39,9 +39,11 @@ __device__ __forceinline__ u32x2_any int8_codes8(const u32x4_any& u, float r) {
   return u32x2_any{codes4(v[0], v[1], v[2], v[3]), codes4(v[4], v[5], v[6], v[7])};
 }
 
-// int8_quantize's scale of a row from the bits of its largest magnitude.
+// int8_quantize's scale of a row from the bits of its largest magnitude (a NaN's lie
+// above infinity's and stay one; a NaN's last byte, its code, is 0).
 __device__ __forceinline__ float int8_scale(uint32_t amax_bits) {
-  return fmaxf(bf16_to_f32(amax_bits) * (1.0f / 127.0f), 0x1p-126f);
+  const float s = bf16_to_f32(amax_bits) * (1.0f / 127.0f);
+  return s < 0x1p-126f ? 0x1p-126f : s;
 }
 
 template <int kCtrl, int kRowMask = 0xf>

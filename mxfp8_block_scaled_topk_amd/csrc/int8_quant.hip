@@ -124,9 +124,13 @@ int launch_int8_quantize(const uint16_t* x, int64_t rows, int64_t kd, int64_t ld
     const int64_t grid = std::min(cap, (rows + per - 1) / per);                                           \
     int8_quantize_kernel<W, C><<<dim3((unsigned)grid), dim3(64 * (W < 4 ? 4 : W)), 0, stream>>>(p);       \
   } while (0)
+  // Rows of up to 2048 elements: 4 waves each for few rows, whose loads are then all in
+  // flight (64 rows of 2048: 2.4 us, a wave each 2.6; 300: 2.45, 2.7), a wave each for
+  // many (16384 of 2048: 19.0, 4 waves 19.4; 4096 of 1024: 4.1, 5.0).  Longer rows as many
+  // waves as hold them, up to 32768 elements.
   if (kd < 8) int8_quantize_tiny<<<dim3((unsigned)std::min(cap, (rows + 255) / 256)), dim3(256), 0, stream>>>(p);
   else if (chunks <= 64) MX_QUANT_LAUNCH(1, 1);
-  else if (chunks <= 256 && rows > num_cus()) MX_QUANT_LAUNCH(1, 4);
+  else if (chunks <= 256 && rows > 4 * num_cus()) MX_QUANT_LAUNCH(1, 4);
   else if (chunks <= 256) MX_QUANT_LAUNCH(4, 1);
   else if (chunks <= 1024) MX_QUANT_LAUNCH(4, 4);
   else if (chunks <= 4096) MX_QUANT_LAUNCH(16, 4);

@@ -26,9 +26,10 @@ namespace mxmoe {
 
 namespace {
 
-constexpr int kMaxResident = 65536;
+constexpr int kMaxResident = 16384;
+constexpr int S = 2;   // stages a wave's ring holds
 
-template <int NR, int MT, int WV, int S, bool kGrouped, bool kSwiglu, bool kOnce, bool kBf16>
+template <int NR, int MT, int WV, bool kGrouped, bool kSwiglu, bool kOnce, bool kBf16>
 __global__ __launch_bounds__(64 * WV) void int8_stream_kernel(Int8Params p, uint32_t n_tiles, uint32_t t_tiles) {
   constexpr int kRowsW = 16 * NR, kRowsX = 16 * MT, kRows = kRowsW + (kBf16 ? 0 : kRowsX);   // LDS rows per slot
   constexpr int kOut = kSwiglu ? kRowsW / 2 : kRowsW;   // features a tile computes
@@ -38,7 +39,7 @@ __global__ __launch_bounds__(64 * WV) void int8_stream_kernel(Int8Params p, uint
   constexpr int kRing = WV * S * kSlot;
   constexpr int kPitch = kRowsW + 4;                    // ints per token of a partial tile
   constexpr int kPart = WV * kRowsX * kPitch * 4 + kScaleOps * 256;
-  static_assert(S >= 2 && S <= 4 && (S - 1) * kOps < 64, "vmcnt range");
+  static_assert(kOps < 64, "vmcnt range");
   static_assert(!kOnce || kPart <= kRing, "the partial tiles reuse the ring");
   static_assert(!kSwiglu || NR % 2 == 0, "gate and up fragments");
   static_assert(!kBf16 || (kOnce && !kGrouped && MT == 1), "resident tokens");
@@ -214,12 +215,9 @@ __global__ __launch_bounds__(64 * WV) void int8_stream_kernel(Int8Params p, uint
       for (int m = 0; m < MT; ++m) acc[f][m] = v4i{0, 0, 0, 0};
     uint32_t sc[kScaleOps] = {};
     for (int i = 0; i < cnt; ++i) {
-      // the stage has landed once only the later ones' loads are outstanding
-      const int later = in_flight - 1;
-      if (later == 0) wait_loads<0>();
-      else if (later == 1) wait_loads<kOps>();
-      else if (S == 3 || later == 2) wait_loads<(S >= 3 ? 2 : 1) * kOps>();
-      else wait_loads<(S >= 4 ? 3 : 1) * kOps>();
+      // the stage has landed once only the later one's loads are outstanding
+      if (in_flight == 1) wait_loads<0>();
+      else wait_loads<kOps>();
       const uint8_t* sl = ring + wave * S * kSlot + slot * kSlot;
       v4i fa[2][NR], fb[2][MT];
 #pragma unroll
@@ -323,50 +321,51 @@ __global__ __launch_bounds__(64 * WV) void int8_stream_kernel(Int8Params p, uint
   }
 }
 
-template <int NR, int MT, int WV, int S, bool kGrouped, bool kSwiglu, bool kOnce, bool kBf16 = false>
+template <int NR, int MT, int WV, bool kGrouped, bool kSwiglu, bool kOnce, bool kBf16 = false>
 int launch_stream(const Int8Params& p, int per_cu, hipStream_t stream, const char* name) {
   constexpr int kOut = kSwiglu ? 8 * NR : 16 * NR;
   const int64_t n_tiles = (p.e.N + kOut - 1) / kOut;
   const int64_t t_tiles = (p.e.T + 16 * MT - 1) / (16 * MT) + (kGrouped ? p.E : 0);
   const int64_t grid = std::min<int64_t>(n_tiles * t_tiles, (int64_t)num_cus() * per_cu);
   const size_t tab = kGrouped ? (size_t)(p.E + 1) * 8 : 0;
-  int8_stream_kernel<NR, MT, WV, S, kGrouped, kSwiglu, kOnce, kBf16>
+  int8_stream_kernel<NR, MT, WV, kGrouped, kSwiglu, kOnce, kBf16>
       <<<dim3((unsigned)grid), dim3(64 * WV), tab, stream>>>(p, (uint32_t)n_tiles, (uint32_t)t_tiles);
   return check_launch(name);
 }
 
-}  // namespace
-
-namespace {
-
-template <int NR, int MT, int WV, int S, bool kOnce>
+template <int NR, int MT, int WV, bool kOnce>
 int launch_any(const Int8Params& p, int per_cu, hipStream_t stream, const char* name) {
-  if (!p.gl) return launch_stream<NR, MT, WV, S, false, false, kOnce>(p, per_cu, stream, name);
-  if (p.swiglu) return launch_stream<NR, MT, WV, S, true, true, kOnce>(p, per_cu, stream, name);
-  return launch_stream<NR, MT, WV, S, true, false, kOnce>(p, per_cu, stream, name);
+  if (!p.gl) return launch_stream<NR, MT, WV, false, false, kOnce>(p, per_cu, stream, name);
+  if (p.swiglu) return launch_stream<NR, MT, WV, true, true, kOnce>(p, per_cu, stream, name);
+  return launch_stream<NR, MT, WV, true, false, kOnce>(p, per_cu, stream, name);
 }
 
 }  // namespace
 
 int launch_int8_32x16(const Int8Params& p, hipStream_t stream, const char* name) {
-  return launch_any<2, 1, 4, 2, false>(p, 2, stream, name);
+  return launch_any<2, 1, 4, false>(p, 2, stream, name);
 }
 int launch_int8_32x16_wide(const Int8Params& p, hipStream_t stream, const char* name) {
-  return launch_any<2, 1, 8, 2, false>(p, 1, stream, name);
+  return launch_any<2, 1, 8, false>(p, 1, stream, name);
 }
 int launch_int8_32x32(const Int8Params& p, hipStream_t stream, const char* name) {
-  return launch_any<2, 2, 4, 2, true>(p, 2, stream, name);
+  return launch_any<2, 2, 4, true>(p, 2, stream, name);
 }
 int launch_int8_48x48(const Int8Params& p, hipStream_t stream, const char* name) {   // (int8_linear only)
-  return launch_stream<3, 3, 3, 2, false, false, true>(p, 2, stream, name);
+  return launch_stream<3, 3, 3, false, false, true>(p, 2, stream, name);
 }
 int launch_int8_64x64(const Int8Params& p, hipStream_t stream, const char* name) {
-  return launch_any<4, 4, 2, 2, true>(p, 2, stream, name);
+  return launch_any<4, 4, 2, true>(p, 2, stream, name);
 }
 
+// bf16 tokens quantised by every workgroup itself, where that takes no longer than a
+// kernel of its own before the product: of up to 16384 elements (1 x 2048, N = 4096: 5.4
+// us, two kernels 6.6; 5 x 2096, N = 4099: 7.0, 7.5; 16 x 1024, N = 8192: 6.9, 6.8; with
+// room for 65536: 16 x 4096, N = 4096 14.7, 8.5) for one workgroup a CU (16 x 1024, N =
+// 32768: 13.8, 11.2).  A call saves a launch and the workspace besides.
 bool int8_resident(int64_t T, int64_t K, int64_t N) { return T <= 16 && T * K <= kMaxResident && N <= 32 * 256; }
 int launch_int8_resident(const Int8Params& p, hipStream_t stream, const char* name) {
-  return launch_stream<2, 1, 8, 2, false, false, true, true>(p, 1, stream, name);
+  return launch_stream<2, 1, 8, false, false, true, true>(p, 1, stream, name);
 }
 
 }  // namespace mxmoe

@@ -367,6 +367,7 @@ int launch_unpermute(const UnpermuteParams& p, int type, hipStream_t stream) {
   return by_type(type, [&](auto t) {
     constexpr int kType = decltype(t)::value;
     auto grid = [&](int64_t n, int64_t per) { return dim3((unsigned)std::min<int64_t>((n + per - 1) / per, cap)); };
+    // rows of 16 pieces share waves: 65536 tokens, 8 experts each, 128 bf16 30 us, a wave each 48
     if (p.row_bytes < 16) unpermute_tiny<kType><<<grid(p.T * p.K, kThreads), dim3(kThreads), 0, stream>>>(p);
     else if (pieces <= 16) unpermute_kernel<kType, 16><<<grid((p.T + 3) / 4, 4), dim3(kThreads), 0, stream>>>(p);
     else unpermute_kernel<kType, 64><<<grid(p.T * ((pieces + 63) / 64), 4), dim3(kThreads), 0, stream>>>(p);
@@ -380,6 +381,7 @@ int launch_unpermute_backward(const UnpermuteParams& p, int type, hipStream_t st
     constexpr int kType = decltype(t)::value;
     auto grid = [&](int64_t n, int64_t per) { return dim3((unsigned)std::min<int64_t>((n + per - 1) / per, cap)); };
     // a token's assignments over several units until there are four workgroups a CU
+    // (8 experts of a token, 64 tokens of 2048 bf16: 3.5 us, unsplit 13.3)
     auto go = [&](auto w, auto c, auto lanes) {
       constexpr int W = decltype(w)::value, C = decltype(c)::value, L = decltype(lanes)::value;
       const int64_t tokens = L == 64 ? p.T : (p.T + 3) / 4, in_wg = W < 4 ? 4 : 1;
@@ -389,16 +391,21 @@ int launch_unpermute_backward(const UnpermuteParams& p, int type, hipStream_t st
       unpermute_backward_kernel<kType, W, C, L><<<grid(tokens * used, in_wg), dim3(64 * (W < 4 ? 4 : W)), 0, stream>>>(
           p, (int)used, (int)per);
     };
+    // As many waves as a token's row has pieces for, one each lane: more waves than
+    // with several pieces a lane, and a token's loads all in flight (16384 tokens, 8
+    // experts each, 2048 bf16: 4 waves 224 us, one wave of 4 pieces a lane 230; 2049 tokens,
+    // 4 experts, 2100 bf16: 8 waves 19.9, 4 of 4 pieces 21.9; 256 tokens, 4 experts, 8192:
+    // 16 waves 10.0, 4 of 4 pieces 10.5).  Two pieces a lane of one wave take less than
+    // 4 waves half idle (1000 tokens, 8 experts, 1024 bf16: 7.6, 9.9); rows of 16
+    // pieces share waves (65536 tokens, 8 experts, 128 bf16: 59, a wave each 122).
     using std::integral_constant;
-    const bool few = p.T * p.k <= num_cus();
     if (p.row_bytes < 16) unpermute_backward_tiny<kType><<<grid(p.T * p.k, kThreads), dim3(kThreads), 0, stream>>>(p);
     else if (pieces <= 16) go(integral_constant<int, 1>{}, integral_constant<int, 1>{}, integral_constant<int, 16>{});
     else if (pieces <= 64) go(integral_constant<int, 1>{}, integral_constant<int, 1>{}, integral_constant<int, 64>{});
-    else if (few && pieces <= 256) go(integral_constant<int, 4>{}, integral_constant<int, 1>{}, integral_constant<int, 64>{});
-    else if (few && pieces <= 1024) go(integral_constant<int, 16>{}, integral_constant<int, 1>{}, integral_constant<int, 64>{});
     else if (pieces <= 128) go(integral_constant<int, 1>{}, integral_constant<int, 2>{}, integral_constant<int, 64>{});
-    else if (pieces <= 256) go(integral_constant<int, 1>{}, integral_constant<int, 4>{}, integral_constant<int, 64>{});
-    else if (pieces <= 1024) go(integral_constant<int, 4>{}, integral_constant<int, 4>{}, integral_constant<int, 64>{});
+    else if (pieces <= 256) go(integral_constant<int, 4>{}, integral_constant<int, 1>{}, integral_constant<int, 64>{});
+    else if (pieces <= 512) go(integral_constant<int, 8>{}, integral_constant<int, 1>{}, integral_constant<int, 64>{});
+    else if (pieces <= 1024) go(integral_constant<int, 16>{}, integral_constant<int, 1>{}, integral_constant<int, 64>{});
     else if (pieces <= 4096) go(integral_constant<int, 16>{}, integral_constant<int, 4>{}, integral_constant<int, 64>{});
     else unpermute_backward_long<kType><<<grid(p.T * p.k, 1), dim3(64 * kLongWaves), 0, stream>>>(p);
     return check_launch("moe_unpermute_backward");

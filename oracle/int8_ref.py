@@ -17,9 +17,11 @@ F32 = np.float32
 def int8_quantize_ref(x):
     """x: float64 [R, K] holding fp32 values.  Returns (q int8, s fp32)."""
     x = x.astype(F32)
-    s = np.maximum(np.abs(x).max(axis=1) * (F32(1) / F32(127)), F32(2.0 ** -126))
+    s = np.maximum(np.abs(x).max(axis=1) * (F32(1) / F32(127)), F32(2.0 ** -126))   # (a NaN stays one)
     r = F32(1) / s
-    return np.rint(x * r[:, None]).astype(np.int8), s
+    with np.errstate(invalid="ignore"):
+        q = np.rint(x * r[:, None])
+    return np.where(np.isnan(q), F32(0), q).astype(np.int8), s
 
 
 def int8_product_ref(xq, xs, wq, ws):

@@ -105,11 +105,12 @@ def test_linear(i):
 @pytest.mark.parametrize("T,K,N", [
     (1, 16, 5), (1, 2048, 4096), (1, 65536, 33), (2, 4112, 100), (3, 144, 257), (5, 2048, 8192), (7, 9360, 64), (13, 240, 70),
     (16, 4096, 96), (16, 16, 64), (15, 2064, 31), (9, 528, 8190), (1, 2048, 8224), (16, 4112, 40),
+    (1, 16384, 33), (1, 16400, 33), (16, 1024, 8192), (16, 1040, 40), (2, 8192, 100), (3, 5456, 64), (15, 1088, 8191),
 ])
 def test_few_bf16_tokens(T, K, N):
     """Tokens that every workgroup quantises itself, and the sizes just past them."""
     linear_case(T, K, N, T + K, int8_in=False, bias="fp32", act="silu", residual=True, what="bf16 tokens")
-    if T <= 16 and T * K <= 65536 and N <= 8192:
+    if T <= 16 and T * K <= 16384 and N <= 8192:
         assert mx.int8_linear_workspace_size(T, K, N, False) == 0
     # the same codes and scales as int8_quantize's
     x = torch.randn((T, K), device="cuda").bfloat16()

@@ -23,7 +23,7 @@ def draw(rows, K, seed):
 
 def check(q, s, bits, what):
     rq, rs = int8_ref.int8_quantize_ref(mx_ref.bf16_to_f64(bits))
-    assert np.array_equal(host(s), rs), (what, "scales")
+    assert np.array_equal(host(s), rs, equal_nan=True), (what, "scales")
     assert np.array_equal(host(q), rq), (what, "codes", np.argwhere(host(q) != rq)[:4].tolist())
 
 
@@ -73,6 +73,25 @@ def test_ties_and_the_floor():
     q, s = mx.int8_quantize(bf16_dev(xb))
     torch.cuda.synchronize()
     check(q, s, xb, "edges")
+
+
+@pytest.mark.parametrize("rows,K", [(9, 7), (9, 100), (9, 2048), (300, 2048), (9, 8000), (9, 30000), (9, 33000)])
+def test_no_numbers(rows, K):
+    """Rows with a NaN (of either sign, quiet or signalling), an infinity, both; the
+    others as ever.  Products of such rows are NaN, also where the linear quantises."""
+    xb = draw(rows, K, K)
+    bad = {0: [0x7FC0], 1: [0xFF81], 2: [0x7F80], 3: [0xFF80], 5: [0x7F80, 0x7FFF], 6: [0xFFFF, 0xFF80]}
+    for r, bits in bad.items():
+        xb[r, [(r * 977 + 5 * i) % K for i in range(len(bits))]] = bits
+    q, s = mx.int8_quantize(bf16_dev(xb))
+    torch.cuda.synchronize()
+    check(q, s, xb, "no numbers")
+    assert not host(s)[sorted(set(range(9)) - set(bad))].max() == np.inf
+    if K % 16 == 0:
+        w, ws = mx.int8_quantize(torch.ones((40, K), dtype=torch.bfloat16, device="cuda"))
+        y = mx.int8_linear(bf16_dev(xb), w, ws)
+        assert torch.equal(y.isnan().all(dim=1), y.isnan().any(dim=1))
+        assert torch.nonzero(y.isnan().any(dim=1)).flatten().tolist() == sorted(bad)
 
 
 @pytest.mark.parametrize("K,ld,offset", [(2048, 2064, 0), (2048, 2049, 1), (100, 333, 3), (5, 9, 1), (33000, 33007, 1)])

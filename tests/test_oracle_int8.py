@@ -23,6 +23,13 @@ def test_quantiser_by_hand():
     assert q.tolist() == [[127, -127, 0]] and np.isfinite(s).all()
 
 
+def test_quantiser_of_no_number():
+    q, s = int8_ref.int8_quantize_ref(np.array([[1.0, np.nan, np.inf], [1.0, -np.inf, 3e38], [1.0, -2.0, 0.0]]))
+    assert np.isnan(s[0]) and s[1] == np.inf and not q[:2].any() and q[2].tolist() == [64, -127, 0]
+    with np.errstate(invalid="ignore"):
+        assert np.isnan(int8_ref.int8_product_ref(q[:2], s[:2], np.ones((4, 3)), np.ones(4))).all()
+
+
 @pytest.mark.parametrize("scale", [1e-30, 1.0, 1e30])
 def test_quantiser_error(scale):
     """A value is off by half a step, and 3 roundings of its 127 steps at most."""
