@@ -16,6 +16,13 @@
 //
 // With SwiGLU every 64 weight rows of a tile are 32 gate rows and the up rows of
 // the same 32 features.
+//
+// Bounds: the main loop, which runs at the rate of the library's plain int8 product
+// (about 2100 TOP/s: the matrix units busy half of the time at the 1.9 GHz that the
+// card keeps under them), then the epilogue.  T = 16384, K = N = 4096 with residual
+// 263 to 277 us (the library without scales or residual 254); 16384 tokens to 8 of
+// 128 experts, K = 2048, N = 768, SwiGLU 470 to 480 us: 393 of main loop with 1024 rows
+// each, 40 to 45 of stores, the rest the experts' last tiles.
 #include <algorithm>
 #include <type_traits>
 
