@@ -563,7 +563,7 @@ size_t int8_linear_workspace_size(int64_t T, int64_t K, int64_t N, int x_is_int8
  *   residual  bf16 [T, N] or NULL;  y bf16 [T, N]
  * y may be the residual itself (the same address); any other overlap of y or of
  * the workspace is MX_ERR_INVALID_ARG.  Limits: K % 16 == 0, K < 2^17 (the sum
- * stays within int32), N < 2^30, fewer than 2^28 tiles of 32 x 32 outputs.
+ * stays within int32), N < 2^27, fewer than 2^28 tiles of 32 x 32 outputs.
  * Alignment: int8 operands on 16-byte boundaries, the workspace on 256, the rest
  * on their elements.
  */

@@ -74,7 +74,7 @@ __device__ __forceinline__ void group_tables(const Int8Params& p, int* tile0, in
     const int e = lane * per + i;
     const int r0 = (int)std::min(before, T), r1 = (int)std::min(before + n[i], T);
     before += n[i];
-    n[i] = (r1 - r0 + kBM - 1) / kBM;
+    n[i] = ((int64_t)r1 - r0 + kBM - 1) / kBM;
     tiles += (int)n[i];
     if (i < per && e < E) row0[e] = r0;
     if (i < per && e == E - 1) row0[E] = r1;

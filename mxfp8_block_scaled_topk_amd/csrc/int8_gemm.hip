@@ -27,6 +27,7 @@ int launch_int8_resident(const Int8Params& p, hipStream_t stream, const char* na
 namespace {
 
 constexpr int64_t kMaxK = ((int64_t)1 << 17) - 16;
+constexpr int64_t kMaxN = ((int64_t)1 << 27) - 1;   // 16 rows of outputs stay within the 32-bit byte offsets of a store
 
 // The kernels, by their tiles (weight rows x rows of x), the waves that share a
 // tile's K, and the workgroups of a CU.
@@ -95,8 +96,8 @@ int check_sizes(const char* name, int64_t T, int64_t K, int64_t N) {
   if (T < 0 || K <= 0 || N <= 0)
     return fail(MX_ERR_INVALID_ARG, "%s: bad sizes rows=%lld K=%lld N=%lld", name, (long long)T, (long long)K,
                 (long long)N);
-  if (!dims_in_range({T, 2 * std::min<int64_t>(N, kMaxDim)}))
-    return fail(MX_ERR_UNSUPPORTED, "%s: rows above 2^31 - 1 or N above 2^30 - 1", name);
+  if (!dims_in_range({T}) || N > kMaxN)
+    return fail(MX_ERR_UNSUPPORTED, "%s: rows above 2^31 - 1 or N above 2^27 - 1", name);
   if (K % 16 != 0) return fail(MX_ERR_UNSUPPORTED, "%s: K=%lld is not a multiple of 16", name, (long long)K);
   if (K > kMaxK) return fail(MX_ERR_UNSUPPORTED, "%s: K=%lld >= 2^17", name, (long long)K);
   if (too_many_tiles(T, N)) return fail(MX_ERR_UNSUPPORTED, "%s: 2^28 or more tiles of 32 x 32 outputs", name);

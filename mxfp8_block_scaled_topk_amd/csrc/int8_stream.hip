@@ -19,7 +19,7 @@
 // Bounds: the weights' way from HBM where they are read once (32 tokens to 8 of 128
 // experts, K = 2048, N = 768, SwiGLU: 63 us, 5.5 TB/s); operand delivery to the CUs that
 // a round of tiles fills where they fit the caches (T = 203, K = 2096, N = 4099: 430 tiles
-// of 48 x 48, 12 us, of which 32 x 32 would take 14); one token launch, first loads and
+// of 48 x 48, 12 us; the other shapes 13 at best); one token launch, first loads and
 // one round (K = 2048, N = 4096, bf16: 5.4 us).
 //
 // kBf16: p.x is bf16 [T, K], T <= 16 and T K <= kMaxResident (host): every

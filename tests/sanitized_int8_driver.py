@@ -77,8 +77,8 @@ for v in BIG:
     expect(lin(N=v), UNSUPPORTED, f"linear N {v}")
     expect(lin(K=v), UNSUPPORTED, f"linear K {v}")
     expect(lin(K=v // 16 * 16), UNSUPPORTED, f"linear K {v} rounded")
-expect(lin(T=TOP, N=(1 << 30) - 1), UNSUPPORTED, "linear tiles")
-for T, K, N in ((1, 16, 1), (1, (1 << 17) - 16, (1 << 30) - 1), (TOP, (1 << 17) - 16, 1), (TOP, 16, 96), (1 << 19, 4096, (1 << 19) - 32)):
+expect(lin(T=TOP, N=(1 << 27) - 1), UNSUPPORTED, "linear tiles")
+for T, K, N in ((1, 16, 1), (1, (1 << 17) - 16, (1 << 27) - 1), (TOP, (1 << 17) - 16, 1), (TOP, 16, 96), (1 << 19, 4096, (1 << 19) - 32)):
     for kw in (dict(y=at(0)), dict(y=at(1)), dict(y=at(2)), dict(y=at(3)), dict(y=at(4)),
                dict(y=at(9), xs=None, T=max(T, 40)), dict(wsp=at(0), xs=None, T=max(T, 40))):
         expect(lin(**{**dict(T=T, K=K, N=N), **kw}), INVALID, f"linear overlap {T} {K} {N} {kw}")

@@ -233,3 +233,42 @@ def test_captured_backward():
         torch.cuda.synchronize()
         for a, b in zip(captured, eager):
             assert torch.equal(a, b), i
+
+
+def test_graphs_that_share_a_workspace():
+    """Two captured sorts of different sizes and one of moe_route_quant, replayed in
+    turn over one workspace."""
+    E = 24
+    shapes = [(300, 48, 8), (1100, 33, 3), (260, 64, 5)]
+    need = max(mx.route_workspace_size(T, k, E) for T, _, k in shapes)
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    xs = [torch.randn((T, K), device="cuda").bfloat16() for T, K, _ in shapes]
+    ids = [i32_dev(routes(T, k, E, T)) for T, _, k in shapes]
+
+    def calls(i):
+        if i == 2:
+            return mx.moe_route_quant(xs[2], ids[2], E, workspace=ws)
+        return mx.moe_permute(xs[i], ids[i], E, workspace=ws)
+    graphs, got = [], []
+    for i in range(3):
+        calls(i)
+        torch.cuda.synchronize()
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[i]):
+            got.append(calls(i))
+    for turn in range(4):
+        for i in range(3):
+            ids[i].copy_(i32_dev(routes(shapes[i][0], shapes[i][2], E, 10 * turn + i)))
+            xs[i].copy_(torch.randn(xs[i].shape, device="cuda"))
+            for t in got[i]:
+                if t is not None:
+                    t.zero_()
+            say(f"turn {turn} graph {i}")
+            graphs[i].replay()
+            torch.cuda.synchronize()
+            ref = int8_ref.permute_ref(host(xs[i].view(torch.int16)), host(ids[i]), E)
+            maps = got[i][2:]
+            for a, b in zip(maps, ref[1:]):
+                assert np.array_equal(host(a), b), (turn, i)
+            if i < 2:
+                assert np.array_equal(host(got[i][0].view(torch.int16)), ref[0]), (turn, i)

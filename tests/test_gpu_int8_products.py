@@ -276,3 +276,61 @@ def test_past_32_bits():
     torch.cuda.synchronize()
     check_bf16(mx_ref.bf16_to_f64(bf16_host(y[pick])), xq.astype(np.float64) @ w.T.astype(np.float64), 3.01 * F32_HALF)
     assert int((y != 0).any(dim=1).sum()) == len(pick)
+    del x, y
+    torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("swiglu", [None, False, True])
+def test_widest_outputs(swiglu):
+    """N at its limit, where 16 rows of outputs span 4 GiB: each part equals a call on its weights."""
+    T, K, N = 64, 16, (1 << 27) - 5
+    gen = torch.Generator(device="cuda").manual_seed(1)
+
+    def draw(*shape):
+        return torch.randint(-128, 128, shape, generator=gen, device="cuda", dtype=torch.int8)
+    rows = 2 * N if swiglu else N
+    x, xs, w, ws = draw(T, K), torch.rand(T, device="cuda"), draw(rows, K), torch.rand(rows, device="cuda") * 2.0 ** -12
+    counts = i64_dev([T])
+    res = torch.rand((T, N), device="cuda", dtype=torch.bfloat16) if swiglu is None else None
+    say(f"N={N} swiglu={swiglu}")
+    if swiglu is None:
+        y = mx.int8_linear(x, w, ws, x_s=xs, residual=res)
+    else:
+        y = mx.gmm_int8(x, xs, w[None], ws[None], counts, swiglu=swiglu)
+    step = 1 << 24
+    for a in range(0, N, step):
+        b = min(N, a + step)
+        if swiglu is None:
+            part = mx.int8_linear(x, w[a:b], ws[a:b], x_s=xs, residual=res[:, a:b].contiguous())
+        elif swiglu:
+            part = mx.gmm_int8(x, xs, torch.cat([w[a:b], w[N + a:N + b]])[None], torch.cat([ws[a:b], ws[N + a:N + b]])[None],
+                               counts, swiglu=True)
+        else:
+            part = mx.gmm_int8(x, xs, w[a:b][None], ws[a:b][None], counts)
+        assert torch.equal(y[:, a:b], part), a
+    del x, w, ws, y, res, part
+    torch.cuda.empty_cache()
+
+
+def test_most_rows():
+    """Row numbers up to 2^31 - 1, a tile's rounding past it."""
+    M, K, N = (1 << 31) - 1, 16, 8
+    rng = np.random.default_rng(5)
+    pick = [0, (1 << 30) + 3, M - 1001, M - 1000, M - 2]
+    mine, w = codes(rng, (len(pick), K)), codes(rng, (2, N, K))
+    a = torch.zeros((M, K), dtype=torch.int8, device="cuda")
+    a[pick] = i8_dev(mine)
+    a_s = torch.ones(M, device="cuda")
+    for counts in ([M - 1000, 999], [0, M]):
+        say(f"gmm_int8 M={M} counts={counts}")
+        y = torch.zeros((M, N), dtype=torch.bfloat16, device="cuda")
+        mx.gmm_int8(a, a_s, i8_dev(w), torch.ones((2, N), device="cuda"), i64_dev(counts), out=y)
+        torch.cuda.synchronize()
+        e = [int(p >= counts[0]) for p in pick]
+        ref = np.stack([w[j].astype(np.float64) @ m.astype(np.float64) for j, m in zip(e, mine)])
+        check_bf16(mx_ref.bf16_to_f64(bf16_host(y[pick])), ref, 3.01 * F32_HALF)
+        y[pick] = 0
+        assert not y.any()
+        del y
+    del a, a_s
+    torch.cuda.empty_cache()

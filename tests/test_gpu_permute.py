@@ -270,3 +270,56 @@ def test_odd_addresses(offset):
         check(dy, ref, 2.0 ** -24 * np.abs(ref), dtype, "dy")
         mag = int8_ref.unpermute_backward_ref(np.abs(f64(d)), eri, k, M, None, np.abs(f64(y)))[1]
         assert (np.abs(host(dw) - rw) <= dw_bound(K, mag)).all()
+
+
+def test_same_row_and_same_expert_twice():
+    """A row that several entries name counts each time; ids that repeat within a
+    token are assignments of their own."""
+    T, K, k, M = 40, 264, 5, 7
+    rng = np.random.default_rng(2)
+    y, w = rows_of(rng, (M, K), "fp32"), rng.random((T, k)).astype(np.float32)
+    eri = rng.integers(0, M, T * k).astype(np.int32)
+    out = mx.moe_unpermute(y.cuda(), i32_dev(eri), k, topk_w=f32_dev(w))
+    ref, mag = (int8_ref.unpermute_ref(v, eri, k, w) for v in (f64(y), np.abs(f64(y))))
+    check(out, ref, 2 * k * 2.0 ** -24 * mag, "fp32", "out")
+    # dw reads the shared rows (of dy they would be unspecified)
+    d = rows_of(rng, (T, K), "fp32")
+    _, dw = mx.moe_unpermute_backward(d.cuda(), i32_dev(eri), k, topk_w=f32_dev(w), y=y.cuda())
+    mag = np.einsum("tc,tjc->tj", np.abs(f64(d)), np.abs(f64(y))[eri.reshape(T, k)])
+    ref = np.einsum("tc,tjc->tj", f64(d), f64(y)[eri.reshape(T, k)])
+    assert (np.abs(f64(dw) - ref) <= (K + 2) * 2.0 ** -24 * mag).all()
+    for T in (9, 700):
+        ids = np.repeat(rng.integers(0, 6, (T, 1)), 4, axis=1).astype(np.int32)
+        x = rows_of(rng, (T, K), "fp32")
+        got = mx.moe_permute(x.cuda(), i32_dev(ids), 6)
+        torch.cuda.synchronize()
+        ref = int8_ref.permute_ref(x.numpy(), ids, 6)
+        assert np.array_equal(host(got[0]), ref[0])
+        for a, b in zip(got[2:], ref[1:]):
+            assert np.array_equal(host(a), b)
+
+
+def test_differences():
+    """The gradients against central differences of the operators themselves, in
+    fp32 with steps and values that are exact: the loss is linear in each."""
+    T, K, k, E = 12, 20, 3, 4
+    rng = np.random.default_rng(8)
+    ids = i32_dev(routes(T, k, E, 8))
+    small = lambda *s: torch.from_numpy(rng.integers(-8, 9, s).astype(np.float32)).cuda()   # sums of exact integers
+    x, w, d = small(T, K), small(T, k), small(T, K)
+    _, _, sr, eri, _ = mx.moe_permute(x, ids, E)
+
+    def loss(x, w):
+        xp = mx.moe_permute(x, ids, E)[0]
+        return float((mx.moe_unpermute(xp, eri, k, topk_w=w) * d).double().sum())
+    xp = mx.moe_permute(x, ids, E)[0]
+    dxp, dw = mx.moe_unpermute_backward(d, eri, k, topk_w=w, y=xp)
+    dx = mx.moe_unpermute(dxp, eri, k)
+    for grad, at_ in ((dx, 0), (dw, 1)):
+        for _ in range(25):
+            args = [x.clone(), w.clone()]
+            i = tuple(int(rng.integers(n)) for n in grad.shape)
+            args[at_][i] += 1
+            up = loss(*args)
+            args[at_][i] -= 2
+            assert (up - loss(*args)) / 2 == float(grad[i])

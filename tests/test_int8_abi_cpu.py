@@ -67,7 +67,7 @@ def test_linear_validation(lib):
     for v in BIG:
         for n in ("T", "N"):
             assert lin(lib, **{n: v}) == UNSUPPORTED, (n, v)
-    for kw in (dict(K=8), dict(K=72), dict(K=1 << 17), dict(K=1 << 20), dict(N=1 << 30), dict(T=1 << 30, N=1 << 10),
+    for kw in (dict(K=8), dict(K=72), dict(K=1 << 17), dict(K=1 << 20), dict(N=1 << 30), dict(N=1 << 27), dict(T=1 << 30, N=1 << 10),
                dict(x=odd(0, 8)), dict(w=odd(2, 8)), dict(xs=odd(1, 2)), dict(ws=odd(3, 1)), dict(b=odd(4, 1)),
                dict(b=odd(4, 2), bt=1), dict(r=odd(5, 1)), dict(y=odd(6, 1)), dict(xs=None, x=odd(0, 1), wsp=at(9), wsb=1 << 20),
                dict(T=40, xs=None, wsp=odd(9, 128), wsb=1 << 20)):
@@ -96,7 +96,7 @@ def test_experts_validation(lib):
     for v in BIG:
         for n in ("M", "N", "E"):
             assert experts(lib, **{n: v}) == UNSUPPORTED, (n, v)
-    for kw in (dict(K=24), dict(K=1 << 17), dict(N=1 << 30), dict(E=1025), dict(a=odd(0, 4)), dict(w=odd(2, 4)),
+    for kw in (dict(K=24), dict(K=1 << 17), dict(N=1 << 30), dict(N=1 << 27), dict(E=1025), dict(a=odd(0, 4)), dict(w=odd(2, 4)),
                dict(a_s=odd(1, 2)), dict(ws=odd(3, 2)), dict(gl=odd(4, 4)), dict(y=odd(5, 1)), dict(M=1 << 28, N=1 << 14)):
         assert experts(lib, **kw) == UNSUPPORTED, kw
     assert experts(lib, M=0, a=None, a_s=None, w=None, ws=None, y=None) == OK
