@@ -413,6 +413,18 @@ __global__ __launch_bounds__(64 * WN * WM) void int8_tile_kernel(Int8Params p, i
             return (t_w + 8 * i) * N + cur.n0 + row;
           };
           uint4 res[8];
+          auto get8 = [&](const float* src, float (&v)[8]) __attribute__((always_inline)) {
+            const float4 a = reinterpret_cast<const float4*>(src)[0], c = reinterpret_cast<const float4*>(src)[1];
+            v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+            v[4] = c.x; v[5] = c.y; v[6] = c.z; v[7] = c.w;
+          };
+          // of its features, in registers where there are some left (T = 2048, K = 1024, N =
+          // 2048: 14.2 us, read for every token 14.5; with 256 rows they would spill)
+          float b[8] = {}, ws[8];
+          if constexpr (kWaves == 4) {
+            get8(s_ws + row + 8 * rc, ws);
+            if constexpr (!kGrouped) get8(s_bias + row + 8 * rc, b);
+          }
 #pragma unroll
           for (int fm = 0; fm < NB; ++fm) {
 #pragma unroll
@@ -443,20 +455,16 @@ __global__ __launch_bounds__(64 * WN * WM) void int8_tile_kernel(Int8Params p, i
                 }
               }
             }
-            auto get8 = [&](const float* src, float (&v)[8]) __attribute__((always_inline)) {
-              const float4 a = reinterpret_cast<const float4*>(src)[0], c = reinterpret_cast<const float4*>(src)[1];
-              v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-              v[4] = c.x; v[5] = c.y; v[6] = c.z; v[7] = c.w;
-            };
 #pragma unroll
             for (int it = 0; it < kTok / 8; ++it) {
               const int r = 8 * it + rr, i = kTok / 8 * fm + it;
               const float xs = s_xs[32 * NB * wm + 32 * fm + r];
-              // (read again for every token: held, they would spill)
-              float b[8] = {}, ws[8], z[8];
-              const int at_row = opaque(row + 8 * rc);
-              get8(s_ws + at_row, ws);
-              if constexpr (!kGrouped) get8(s_bias + at_row, b);
+              float z[8];
+              if constexpr (kWaves > 4) {
+                const int at_row = opaque(row + 8 * rc);
+                get8(s_ws + at_row, ws);
+                if constexpr (!kGrouped) get8(s_bias + at_row, b);
+              }
               const i32x4 z0 = *reinterpret_cast<const lds_i32x4*>(stg + r * 256 + (((2 * rc) ^ (r & 15)) << 4));
               const i32x4 z1 = *reinterpret_cast<const lds_i32x4*>(stg + r * 256 + (((2 * rc + 1) ^ (r & 15)) << 4));
 #pragma unroll
