@@ -334,3 +334,39 @@ def test_most_rows():
         del y
     del a, a_s
     torch.cuda.empty_cache()
+
+
+def off(t, n=1):
+    """The same values n elements past the start of an allocation."""
+    buf = torch.empty(t.numel() + n, dtype=t.dtype, device="cuda")
+    view = buf[n:].view(t.shape)
+    view.copy_(t)
+    return view
+
+
+@pytest.mark.parametrize("T,K,N", [(1, 144, 40), (5, 512, 77), (16, 1024, 512), (40, 272, 131), (203, 528, 515), (700, 256, 1030)])
+def test_odd_addresses(T, K, N):
+    """Everything but the int8 operands on any element: the outputs are the same."""
+    rng = np.random.default_rng(T)
+    x = torch.from_numpy(rng.standard_normal((T, K)).astype(np.float32)).cuda().bfloat16()
+    w, ws = i8_dev(codes(rng, (N, K))), f32_dev(scales(rng, N))
+    q, s = mx.int8_quantize(x)
+    r = torch.from_numpy(rng.standard_normal((T, N)).astype(np.float32)).cuda().bfloat16()
+    for b in (f32_dev(rng.standard_normal(N)), f32_dev(rng.standard_normal(N)).bfloat16()):
+        for n in (1, 3):
+            say(f"T={T} K={K} N={N} bias={b.dtype} offset={n}")
+            a = mx.int8_linear(x, w, ws, bias=b, act="silu", residual=r)
+            c = mx.int8_linear(off(x, n), w, off(ws, n), bias=off(b, n), act="silu", residual=off(r, n), out=off(r, n))
+            d = off(r, n)
+            d = mx.int8_linear(q, w, off(ws, n), x_s=off(s, n), bias=off(b, n), act="silu", residual=d, out=d)
+            torch.cuda.synchronize()
+            assert torch.equal(a, c) and torch.equal(a, d)
+    for swiglu in (False, True):
+        wr = w[:N // 2 * 2] if swiglu else w
+        wsr = ws[:wr.shape[0]]
+        counts = i64_dev([T // 2, T - T // 2])
+        w2, ws2 = torch.stack([wr, wr.flip(0)]), torch.stack([wsr, wsr.flip(0)])
+        a = mx.gmm_int8(q, s, w2, ws2, counts, swiglu=swiglu)
+        c = mx.gmm_int8(q, off(s), w2, off(ws2), off(counts), swiglu=swiglu, out=off(torch.zeros_like(a)))
+        torch.cuda.synchronize()
+        assert torch.equal(a, c)
