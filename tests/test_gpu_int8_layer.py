@@ -210,9 +210,12 @@ def test_training_step(T, K, N, E, k):
         assert ((a.double().cpu() - b).abs() <= (n + 4) * F32_HALF * m.detach()).all(), what
 
 
-def test_captured_backward():
+@pytest.mark.parametrize("dropped", [False, True])
+def test_captured_backward(dropped):
     T, K, E, k = 260, 320, 16, 4
     ids = i32_dev(routes(T, k, E, 2))
+    if dropped:
+        ids[::7, 1] = -1   # (rows of dy that no entry names are zeros)
     x, w = torch.randn((T, K), device="cuda").bfloat16(), torch.rand((T, k), device="cuda")
 
     def run(x, w):
