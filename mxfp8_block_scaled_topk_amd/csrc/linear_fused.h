@@ -90,9 +90,9 @@ __device__ __forceinline__ float half_erfc(float x) {
 template <int n>
 __device__ __forceinline__ void activate(float (&z)[n], int act) {
   switch (act) {
-    case MX_ACT_RELU:
+    case MX_ACT_RELU:   // (a maximum with 0 would turn NaN into 0)
 #pragma unroll
-      for (int i = 0; i < n; ++i) z[i] = fmaxf(z[i], 0.0f);
+      for (int i = 0; i < n; ++i) z[i] = z[i] <= 0.0f ? 0.0f : z[i];
       break;
     case MX_ACT_SILU:   // z / (1 + e^-z)
 #pragma unroll
