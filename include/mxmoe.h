@@ -642,8 +642,8 @@ int moe_permute(const void* x, int64_t ldx, int64_t elem_bytes, const float* x_s
  * [0, M) are skipped; a token with none left gets zeros.
  *   y [M, K], out [T, K] of `type` (mx_type); topk_w fp32 [T, k] or NULL;
  *   expanded_row_idx int32 [T*k]
- * K from 1 to 2^24, T*k < 2^31, any alignment of whole elements.  out overlaps no
- * input (MX_ERR_INVALID_ARG).
+ * K from 1 to 2^24, k from 1 to 2^20, T*k < 2^31, any alignment of whole elements.
+ * out overlaps no input (MX_ERR_INVALID_ARG).
  */
 int moe_unpermute(const void* y, int type, const float* topk_w,
                   const int32_t* expanded_row_idx, int64_t T, int64_t K,

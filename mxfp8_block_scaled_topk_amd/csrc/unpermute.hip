@@ -344,6 +344,10 @@ __global__ __launch_bounds__(kThreads) void unpermute_backward_tiny(UnpermutePar
   }
 }
 
+// Entries a token may have: one wave or thread takes a token's in turn, and their
+// indices, a batch or a share past the last included, are ints.
+constexpr int64_t kMaxEntries = (int64_t)1 << 20;
+
 int64_t elem_bytes(int type) { return type == MX_TYPE_F32 ? 4 : 2; }
 
 int check_unpermute(const char* name, int type, int64_t T, int64_t K, int64_t k, int64_t M) {
@@ -354,6 +358,7 @@ int check_unpermute(const char* name, int type, int64_t T, int64_t K, int64_t k,
     return fail(MX_ERR_INVALID_ARG, "%s: type must be MX_TYPE_BF16, MX_TYPE_F32 or MX_TYPE_F16, got %d", name, type);
   if (!dims_in_range({T, k, M})) return fail(MX_ERR_UNSUPPORTED, "%s: T, k or M above 2^31 - 1", name);
   if (K > (int64_t)1 << 24) return fail(MX_ERR_UNSUPPORTED, "%s: K=%lld > 2^24", name, (long long)K);
+  if (k > kMaxEntries) return fail(MX_ERR_UNSUPPORTED, "%s: k=%lld > 2^20", name, (long long)k);
   if (T * k >= (int64_t)1 << 31) return fail(MX_ERR_UNSUPPORTED, "%s: T*k >= 2^31", name);
   return MX_OK;
 }
