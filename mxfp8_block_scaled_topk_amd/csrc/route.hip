@@ -278,6 +278,9 @@ __device__ __forceinline__ void quant_half_block(const RouteParams& p, int64_t t
 // MXFP8 and its scales (moe_route_mx), or moves rows of any type (moe_permute).
 constexpr int kRowsQuant = 0, kRowsMx = 1, kRowsAny = 2;
 
+// 16 bytes on any byte: gfx950 loads and stores them in one instruction all the same.
+typedef unsigned int u32x4_byte __attribute__((ext_vector_type(4), aligned(1)));
+
 // moe_permute's rows are K bytes on any boundary, in pieces of 16 (fewer in a row
 // of fewer): piece i starts at byte 16 i, a row's last one 16 bytes before its
 // end, so that some bytes may come twice.  In LDS piece i lies at 16 i.  The writes
@@ -286,24 +289,24 @@ constexpr int kRowsQuant = 0, kRowsMx = 1, kRowsAny = 2;
 __device__ __forceinline__ int64_t piece_at(const RouteParams& p, int i) {
   return p.K >= 16 ? std::min<int64_t>(16 * (int64_t)i, p.K - 16) : 0;
 }
-__device__ __forceinline__ u32x4_any load_piece(const RouteParams& p, const uint8_t* src) {
-  if (p.K >= 16) return *reinterpret_cast<const u32x4_any*>(src);
-  u32x4_any u = {0, 0, 0, 0};
+__device__ __forceinline__ u32x4_byte load_piece(const RouteParams& p, const uint8_t* src) {
+  if (p.K >= 16) return *reinterpret_cast<const u32x4_byte*>(src);
+  u32x4_byte u = {0, 0, 0, 0};
 #pragma unroll
   for (int b = 0; b < 15; ++b)
     if (b < (int)p.K) u[b >> 2] |= (uint32_t)src[b] << (8 * (b & 3));
   return u;
 }
-__device__ __forceinline__ void store_piece(const RouteParams& p, uint8_t* dst, const u32x4_any& u) {
+__device__ __forceinline__ void store_piece(const RouteParams& p, uint8_t* dst, const u32x4_byte& u) {
   if (p.K < 16) {
 #pragma unroll
     for (int b = 0; b < 15; ++b)
       if (b < (int)p.K) dst[b] = static_cast<uint8_t>(u[b >> 2] >> (8 * (b & 3)));
   } else if (p.stream) {
-    __builtin_nontemporal_store(u, reinterpret_cast<u32x4_any*>(dst));
+    __builtin_nontemporal_store(u, reinterpret_cast<u32x4_byte*>(dst));
   } else {
     asm volatile("" ::: "memory");   // keeps the two stores apart: merged, the hint is lost
-    *reinterpret_cast<u32x4_any*>(dst) = u;
+    *reinterpret_cast<u32x4_byte*>(dst) = u;
   }
 }
 
@@ -414,7 +417,7 @@ __global__ __launch_bounds__(kThreads) void route_quant_kernel(RouteParams p) {
       const uint8_t* src = p.rows + (t0 + tb + tl) * p.ld_bytes;
       uint8_t* dst = xbuf + tl * rowb;
       for (int hb0 = sub; hb0 < hpr; hb0 += kLd * lanes) {
-        u32x4_any u[kLd];
+        u32x4_byte u[kLd];
 #pragma unroll
         for (int i = 0; i < kLd; ++i)
           if (hb0 + i * lanes < hpr) u[i] = load_piece(p, src + piece_at(p, hb0 + i * lanes));
@@ -591,7 +594,7 @@ __global__ __launch_bounds__(kThreads) void route_quant_kernel(RouteParams p) {
       uint8_t* dst = p.xq + (int64_t)r * p.K;
       for (int hb = sub; hb < hpr; hb += lanes) {
         const uint4 u = *reinterpret_cast<const uint4*>(src + hb * 16);
-        store_piece(p, dst + piece_at(p, hb), u32x4_any{u.x, u.y, u.z, u.w});
+        store_piece(p, dst + piece_at(p, hb), u32x4_byte{u.x, u.y, u.z, u.w});
       }
     }
     if (p.row_s)
@@ -602,7 +605,7 @@ __global__ __launch_bounds__(kThreads) void route_quant_kernel(RouteParams p) {
     // the share's tokens past the LDS budget
     for (int64_t it = (int64_t)nbt * hpr + tid; it < (int64_t)(te - tb) * hpr; it += kThreads) {
       const int tl = tb + (int)(it / hpr), hb = (int)(it % hpr);
-      const u32x4_any u = load_piece(p, p.rows + (t0 + tl) * p.ld_bytes + piece_at(p, hb));
+      const u32x4_byte u = load_piece(p, p.rows + (t0 + tl) * p.ld_bytes + piece_at(p, hb));
       for (int j = 0; j < k; ++j) {
         const int r = s_pos[tl * k + j];
         if (r >= 0) store_piece(p, p.xq + (int64_t)r * p.K + piece_at(p, hb), u);
