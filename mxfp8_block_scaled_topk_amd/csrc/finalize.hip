@@ -39,15 +39,15 @@ __global__ __launch_bounds__(kThreads) void finalize_kernel(
     float acc[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) acc[i] = 0.0f;
-    for (int j0 = 0; j0 < k; j0 += kBatch) {
+    for (uint32_t j0 = 0; j0 < (uint32_t)k; j0 += kBatch) {   // (unsigned: a batch past k = 2^31 - 1 does not wrap)
       uint4 rows[kBatch];
       float wt[kBatch];
       bool ok[kBatch];
 #pragma unroll
       for (int b = 0; b < kBatch; ++b) {
-        const int j = j0 + b;
+        const uint32_t j = j0 + b;
         ok[b] = false;
-        if (j < k) {
+        if (j < (uint32_t)k) {
           const int32_t p = eri[t * k + j];
           wt[b] = w[t * k + j];
           ok[b] = p >= 0 && p < M;
