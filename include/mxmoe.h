@@ -540,8 +540,9 @@ int mx_linear_fused_kernel(int64_t T, int64_t K, int64_t N, int x_is_mx);
  *   q[r, c] = nearest integer to fl(x[r, c] * fl(1 / s[r])), ties to even
  * with fl and the products rounded to fp32, so that every code is determined;
  * |q| <= 127.  A row with a NaN gets the scale NaN, else one with an infinity the
- * scale infinity, and codes 0 both, so that its products are NaN.  Any kd from 1 to 2^24, any alignment of whole elements (rows of a
- * multiple of 8 elements on 16-byte boundaries, q on 8, are the fastest).
+ * scale infinity, and codes 0 both, so that its products are NaN (and stay NaN through
+ * int8_linear's activations).  Any kd from 1 to 2^24, any alignment of whole elements
+ * (rows of a multiple of 8 elements on 16-byte boundaries, q on 8, are the fastest).
  */
 int int8_quantize(const void* x_bf16, int64_t rows, int64_t kd, int64_t ld,
                   void* q_i8, float* s, void* stream);

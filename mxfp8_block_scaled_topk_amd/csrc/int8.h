@@ -106,8 +106,8 @@ __device__ __forceinline__ int expert_of(const int* tile0, int E, int t) {
 // lie on 64 bytes, where the parts of a line that neighbouring tiles write meet in
 // the L2 (8 experts, 44922 rows, K = 640: N = 704 43 / 44 us past / through the
 // caches, N = 706 72 / 51; 64 experts, 32768 rows, K = 1024, N = 4104: 257 / 235).
-// int8_linear's and SwiGLU's tiles gain nothing by that (T = 8192, K = 1024: N = 3080
-// 62 / 58, N = 4104 66 / 78).
+// int8_linear's tiles gain less by that on some widths than they lose on others (T =
+// 8192, K = 1024: N = 3080 62 / 58, N = 4104 66 / 78), SwiGLU's gain nothing.
 __device__ __forceinline__ void store8_bits(uint16_t* y, int64_t el, uint32_t lane_el, int cnt, const u32x4_any& o,
                                             bool cached = false) {
   if (cnt <= 0) return;

@@ -384,8 +384,11 @@ int launch_int8_64x64(const Int8Params& p, hipStream_t stream, const char* name)
 // kernel of its own before the product: of up to 16384 elements (1 x 2048, N = 4096: 5.4
 // us, two kernels 6.6; 5 x 2096, N = 4099: 7.0, 7.5; 16 x 1024, N = 8192: 6.9, 6.8; with
 // room for 65536: 16 x 4096, N = 4096 14.7, 8.5) for one workgroup a CU (16 x 1024, N =
-// 32768: 13.8, 11.2).  A call saves a launch and the workspace besides.
-bool int8_resident(int64_t T, int64_t K, int64_t N) { return T <= 16 && T * K <= kMaxResident && N <= 32 * 256; }
+// 32768: 13.8, 11.2).  A call saves a launch and the workspace besides.  The bound on
+// N is one workgroup for each of 256 CUs whatever the device has: it says which calls
+// need a workspace, which callers read in the header and ask for without a device.
+constexpr int64_t kMaxResidentN = 32 * 256;
+bool int8_resident(int64_t T, int64_t K, int64_t N) { return T <= 16 && T * K <= kMaxResident && N <= kMaxResidentN; }
 int launch_int8_resident(const Int8Params& p, hipStream_t stream, const char* name) {
   return launch_stream<2, 1, 8, false, false, true, true>(p, 1, stream, name);
 }

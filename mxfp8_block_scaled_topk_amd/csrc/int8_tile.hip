@@ -21,8 +21,11 @@
 // (about 2100 TOP/s: the matrix units busy half of the time at the 1.9 GHz that the
 // card keeps under them), then the epilogue.  T = 16384, K = N = 4096 with residual
 // 263 to 277 us (the library without scales or residual 254); 16384 tokens to 8 of
-// 128 experts, K = 2048, N = 768, SwiGLU 470 to 480 us: 393 of main loop with 1024 rows
-// each, 40 to 45 of stores, the rest the experts' last tiles.
+// 128 experts, K = 2048, N = 768, SwiGLU 456 to 490 us: 393 of main loop with 1024 rows
+// each, 40 to 45 of stores, the rest the experts' last tiles.  Passes straight behind
+// each other run at the clock that the card's power leaves them: the linear's first 30
+// take 296 to 313 us, the next 30 281; codes that use more of their 8 bits (a normal's,
+// without the few large channels) 278 to 297.
 #include <algorithm>
 #include <type_traits>
 
