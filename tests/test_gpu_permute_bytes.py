@@ -13,14 +13,16 @@ from test_gpu_permute import routes
 pytestmark = pytest.mark.gpu
 
 
-@pytest.mark.parametrize("offset", [0, 1, 2, 3, 7])
-@pytest.mark.parametrize("T,K,ld,k,E", [
+SIZES = [
     (1, 1, 1, 1, 1), (9, 3, 5, 2, 4), (33, 15, 15, 3, 8), (33, 16, 17, 3, 8), (40, 17, 17, 8, 16), (300, 129, 131, 4, 32),
-    (300, 2047, 2049, 2, 8), (3, 50001, 50003, 2, 5), (20000, 1001, 1003, 8, 64),   # the last: over 128 MB
-])
+    (300, 2047, 2049, 2, 8), (3, 50001, 50003, 2, 5),
+]
+CASES = [(*s, offset) for s in SIZES for offset in (0, 1, 2, 3, 7)]
+CASES += [(20000, 1001, 1003, 8, 64, offset) for offset in (0, 3)]   # over 128 MB: past the caches
+
+
+@pytest.mark.parametrize("T,K,ld,k,E,offset", CASES)
 def test_odd_bytes(T, K, ld, k, E, offset):
-    if T == 20000 and offset not in (0, 3):
-        pytest.skip("one odd address is enough of the large one")
     gen = torch.Generator().manual_seed(T + offset)
     buf = torch.randint(-128, 128, (offset + T * ld,), generator=gen, dtype=torch.int8)
     x = buf[offset:].view(T, ld)[:, :K]
